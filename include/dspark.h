@@ -66,8 +66,10 @@ enum {
   DSPARK_EDEVICE = 4
 };
 
-/* Weight element types of the Markov head. */
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1 } dspark_dtype;
+/* Element types: of the Markov head's weights (F32, BF16), of logits to
+ * constrain (F32, BF16) and of a key-value cache (BF16, or E4M3: 8 bits, 4 of
+ * exponent and 3 of mantissa, largest value 448, no infinities). */
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_E4M3 = 2 } dspark_dtype;
 
 /* Library ABI version (major * 100 + minor). */
 int dspark_version(void);
@@ -92,7 +94,8 @@ const char* dspark_last_error(const dspark_ctx* ctx);
 /* Synchronise `stream`, read and clear the device error flag.  Returns
  * DSPARK_EDEVICE if any kernel since the last check met an out-of-range
  * token id, verify length or accepted length, a bad candidate temperature
- * (dspark_sts_fit), or a grid barrier of the whole-draft kernel
+ * (dspark_sts_fit), a page, length, slot or row outside its array (the
+ * calls over a paged cache), or a grid barrier of the whole-draft kernel
  * gave up waiting (see dspark_draft_markov; the message names which),
  * DSPARK_EHIP on a HIP error, else DSPARK_OK. */
 int dspark_check(dspark_ctx* ctx, hipStream_t stream);
@@ -125,7 +128,9 @@ enum {
   DSPARK_K_DRAFT_CHAIN = 12,   /* chained draft: every position in one launch */
   DSPARK_K_VERIFY_CHAIN = 13,  /* verify chain: every needed target row in one launch */
   DSPARK_K_CONF_MERGE = 14,    /* draft merge + confidences (dspark_draft_markov_conf) */
-  DSPARK_K_COUNT = 15
+  DSPARK_K_PAGES = 15,         /* page bookkeeping (reserve, commit) */
+  DSPARK_K_CACHE = 16,         /* keys and values into the cache */
+  DSPARK_K_COUNT = 17
 };
 int dspark_timing_enable(dspark_ctx* ctx, int enable);
 int dspark_timing_read(dspark_ctx* ctx, double* ms, int* launches);
@@ -431,6 +436,92 @@ int dspark_verify_packed(dspark_ctx* ctx, hipStream_t stream,
                          const float* states, const int32_t* K, const uint32_t* req_ids,
                          float temperature, uint64_t seed,
                          int32_t* accept_len, int32_t* out_tokens);
+
+/* The packed verify batch over a paged key-value cache.
+ *
+ * [summary] section 5 (variable-length verify batches) and section 4 (the
+ * scheduler's K).  Between the schedule and the verification of a step the
+ * target runs over K[b] + 1 rows of every request, laid end to end.  The
+ * calls below give those rows their places, keep the cache they attend to,
+ * and attend:
+ *     dspark_schedule -> K
+ *     dspark_pages_reserve -> t_offsets, row positions and cache slots
+ *     (per layer) dspark_cache_write, dspark_attend
+ *     dspark_verify_packed (t_offsets, K) -> accept_len
+ *     dspark_pages_commit -> new lengths, surplus pages back in the pool
+ * Every number they need stays on the device, so a whole step can be
+ * captured.
+ *
+ * Pages: the cache holds n_pages pages of page_size tokens (a power of two,
+ * 8..1024; n_pages * page_size < 2^31).  Token t of request b lives in page
+ * table[b][t / page_size] at place t % page_size; its slot is that page's id
+ * * page_size + the place.  table: int32 [B][table_stride], of which the
+ * first held[b] <= max_pages entries of row b are in use.  The pool of free
+ * pages is a stack: free_list int32 [n_pages], the top at n_free[0] - 1.
+ * B <= 4096.
+ *
+ * dspark_pages_reserve: request b takes part with K[b] + 1 rows (K[b] = -1:
+ * none), tokens len[b] .. len[b] + K[b] of its sequence; len[b] tokens are
+ * in the cache already.  Pages are popped in request order until request b
+ * holds ceil((len[b] + K[b] + 1) / page_size) (more than that stay held),
+ * their ids written behind its table row's entries.  Outputs: t_offsets int32
+ * [B + 1], the exclusive scan of the rows; for each of the packed rows its
+ * request, its position in the sequence and its slot (row_req, row_pos,
+ * row_slot: int32 [n_rows]; -1 for entries behind the last row);
+ * held_out int32 [B] and n_free_out int32 [1], which may be held and n_free.
+ * K may exceed 32 here (a prompt's rows).  If the pool, the table rows
+ * (max_pages) or n_rows cannot hold the batch, or a K, length or count is
+ * invalid, nothing is taken: the device error flag is raised, t_offsets are 0,
+ * the row arrays -1, held_out = held, n_free_out = n_free.  A page id outside
+ * [0, n_pages) is flagged and its rows get slot -1.
+ *
+ * dspark_pages_commit: after verification request b keeps accept_len[b] + 1
+ * of its rows (accept_len[b] = -1: none): len_out[b] = len[b] +
+ * accept_len[b] + 1, and the pages from ceil(len_out[b] / page_size) on are
+ * pushed back, in request order and by ascending place.  finished (int32 [B],
+ * or NULL): where nonzero, the request ends: accept_len[b] is then only
+ * checked to be >= -1, len_out[b] = 0 and every page goes back.  len_out and held_out may
+ * be len and held, n_free_out may be n_free.  Table entries of pages given
+ * back are left as they are.  If a length or count is invalid, a request
+ * holds too few pages for its length, or the pool would overflow, nothing
+ * changes (len_out = len, ...) and the error flag is raised.
+ *
+ * One launch each (timing class DSPARK_K_PAGES), no workspace.  Errors:
+ * DSPARK_EINVAL for shapes, limits and null pointers. */
+int dspark_pages_reserve(dspark_ctx* ctx, hipStream_t stream, int B, int page_size, int n_pages,
+                         const int32_t* K, const int32_t* len,
+                         int32_t* table, int64_t table_stride, int max_pages,
+                         const int32_t* held, int32_t* held_out,
+                         const int32_t* free_list, const int32_t* n_free, int32_t* n_free_out,
+                         int n_rows, int32_t* t_offsets, int32_t* row_req, int32_t* row_pos, int32_t* row_slot);
+
+int dspark_pages_commit(dspark_ctx* ctx, hipStream_t stream, int B, int page_size, int n_pages,
+                        const int32_t* len, int32_t* len_out, const int32_t* accept_len, const int32_t* finished,
+                        const int32_t* table, int64_t table_stride, int max_pages,
+                        const int32_t* held, int32_t* held_out,
+                        int32_t* free_list, const int32_t* n_free, int32_t* n_free_out);
+
+/* Keys and values of packed rows into the paged cache: for every row with
+ * slot s = row_slot[row] >= 0 and every head, page s / page_size, place
+ * s % page_size of kcache and vcache take k[row] and v[row]; rows with slot
+ * -1 are skipped, slots outside [-1, n_pages * page_size) are flagged and
+ * skipped.  Slots are distinct (what a slot given twice holds afterwards is
+ * one row's bytes or another's, in 16-byte pieces).
+ * k, v: bf16 [n_rows][heads][d] through row and head strides (multiples of
+ * 8; 16-byte aligned pointers).  kcache, vcache: kv_dtype BF16 or E4M3,
+ * [n_pages][page_size][heads][d] through page, token and head strides in
+ * elements (multiples of 16 bytes; heads inside tokens or tokens inside
+ * heads, d contiguous); d = 64, 128 or 256.  E4M3: the value nearest
+ * k / k_scale[head] (ties to even, magnitudes above 448 become 448; NaN
+ * stays), a single rounding of the exact quotient; k_scale, v_scale float
+ * [heads], positive and normal, or NULL for 1; they must be NULL for BF16.
+ * One launch (timing class DSPARK_K_CACHE).  Errors: DSPARK_EINVAL. */
+int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
+                       const void* k, int64_t k_stride_row, int64_t k_stride_head,
+                       const void* v, int64_t v_stride_row, int64_t v_stride_head,
+                       const int32_t* row_slot, void* kcache, void* vcache,
+                       int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                       dspark_dtype kv_dtype, const float* k_scale, const float* v_scale);
 
 /* Fit the per-position confidence temperatures (sequential temperature
  * scaling) on held-out drafts.

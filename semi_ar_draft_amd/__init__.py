@@ -18,18 +18,19 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdspark.so")
 
 DSPARK_OK, DSPARK_EINVAL, DSPARK_EHIP, DSPARK_ENOMEM, DSPARK_EDEVICE = 0, 1, 2, 3, 4
-DSPARK_F32, DSPARK_BF16 = 0, 1
+DSPARK_F32, DSPARK_BF16, DSPARK_E4M3 = 0, 1, 2
 
 EXPORTS = (
     "dspark_version", "dspark_create", "dspark_destroy", "dspark_last_error", "dspark_check",
     "dspark_draft_markov", "dspark_draft_markov_static", "dspark_draft_markov_conf", "dspark_draft_rnn",
     "dspark_confidence", "dspark_schedule", "dspark_schedule_async", "dspark_verify",
     "dspark_verify_packed", "dspark_accept_prob", "dspark_sts_fit", "dspark_stream_read",
+    "dspark_pages_reserve", "dspark_pages_commit", "dspark_cache_write",
     "dspark_timing_enable", "dspark_timing_read",
 )
 KERNEL_CLASSES = ("draft_sweep", "draft_combine", "confidence", "survival", "schedule",
                   "verify_rows", "verify_decide", "resid_sweep", "resid_combine", "gru", "diag", "sts_fit",
-                  "draft_chain", "verify_chain", "conf_merge")
+                  "draft_chain", "verify_chain", "conf_merge", "pages", "cache")
 
 _lib = None
 _vp, _i32, _i64, _u64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
@@ -104,6 +105,16 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         _vp, _vp, _i64, _i32, _vp, _i64, _vp, _vp, _i32, _i32, _vp, _vp, _vp]
     lib.dspark_stream_read.restype = _i32
     lib.dspark_stream_read.argtypes = [_vp, _vp, _vp, _i64, _vp]
+    lib.dspark_pages_reserve.restype = _i32
+    lib.dspark_pages_reserve.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp, _i32, _vp, _vp, _vp, _vp]
+    lib.dspark_pages_commit.restype = _i32
+    lib.dspark_pages_commit.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _vp, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _vp, _vp, _vp]
+    lib.dspark_cache_write.restype = _i32
+    lib.dspark_cache_write.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64,
+        _i32, _vp, _vp]
     if path is None:
         _lib = lib
     return lib
@@ -150,6 +161,55 @@ def _logits3(t: torch.Tensor, name: str, device):
     if t.stride(2) != 1:
         raise ValueError(f"{name} rows must be contiguous over the vocabulary")
     return t.stride(0), t.stride(1)
+
+
+def _ints(t: torch.Tensor, n: int, name: str, device):
+    """A contiguous int32 vector of n entries."""
+    _need(t, name, torch.int32, device, 1)
+    if t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+
+
+def _table(table: torch.Tensor, B: int, device):
+    """Row stride and columns of a block table."""
+    _need(table, "table", torch.int32, device, 2, contiguous=False)
+    if table.shape[0] != B or table.stride(1) != 1:
+        raise ValueError(f"table must be [{B}][max_pages] with contiguous rows")
+    return table.stride(0), table.shape[1]
+
+
+def _cache(kc: torch.Tensor, vc: torch.Tensor, k_scale, v_scale, device):
+    """Element type of a pair of caches, and their strides of a page, a token and a head."""
+    if kc.dtype == torch.bfloat16:
+        kind = DSPARK_BF16
+    elif kc.dtype == torch.float8_e4m3fn:
+        kind = DSPARK_E4M3
+    else:
+        raise TypeError(f"the cache must be bf16 or float8_e4m3fn, got {kc.dtype}")
+    _need(kc, "kcache", None, device, 4, contiguous=False)
+    _need(vc, "vcache", kc.dtype, device, 4, contiguous=False)
+    sp, st, sh, sd = kc.stride()
+    if vc.shape != kc.shape or vc.stride() != (sp, st, sh, sd):
+        raise ValueError("kcache and vcache must have one shape and one set of strides")
+    n, page, heads, d = kc.shape
+    if heads == 1:                     # steps that are never taken: torch leaves them arbitrary
+        sh = d
+    if n == 1:
+        sp = max(page * st, heads * sh)
+    if sd != 1:
+        raise ValueError("the cache must be contiguous over a head's values")
+    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if t is not None:
+            _need(t, name, torch.float32, device, 1)
+            _len(t, kc.shape[2], name)
+    return kind, sp, st, sh
+
+
+def _steps(t: torch.Tensor):
+    """Strides of the two leading dimensions, 0 for one that has a single entry."""
+    a, b, _ = t.stride()
+    n, m, _ = t.shape
+    return (a if n > 1 else 0), (b if m > 1 else 0)
 
 
 class Context:
@@ -512,6 +572,87 @@ class Context:
             _ptr(states), float(temperature), out.data_ptr()))
         return out
 
+    # -- dspark_pages_reserve ---------------------------------------------------------
+    def pages_reserve(self, K, length, table, held, free_list, n_free, page_size: int, n_pages: int,
+                      held_out=None, n_free_out=None, n_rows: Optional[int] = None, out=None, stream=None):
+        """Pages and places for K[b] + 1 rows of every request.
+
+        K, length, held: int32 [B]; table: int32 [B][max_pages]; free_list:
+        int32 [n_pages]; n_free: int32 [1].  held and n_free are updated in
+        place unless held_out and n_free_out are given; table is.  The row
+        arrays have n_rows entries (or those of ``out``).  Returns t_offsets
+        [B + 1], row_req, row_pos, row_slot [n_rows] (int32)."""
+        dev = self.device
+        _need(K, "K", torch.int32, dev, 1)
+        B = K.shape[0]
+        ts, cols = _table(table, B, dev)
+        held_out = held if held_out is None else held_out
+        n_free_out = n_free if n_free_out is None else n_free_out
+        if out is None:
+            if n_rows is None:
+                raise ValueError("n_rows is needed where out is not given")
+            out = tuple(torch.empty((n,), dtype=torch.int32, device=dev) for n in (B + 1, n_rows, n_rows, n_rows))
+        offs, req, pos, slot = out
+        n_rows = slot.shape[0] if n_rows is None else n_rows
+        for t, n, name in ((length, B, "length"), (held, B, "held"), (held_out, B, "held_out"),
+                           (free_list, n_pages, "free_list"), (n_free, 1, "n_free"), (n_free_out, 1, "n_free_out"),
+                           (offs, B + 1, "t_offsets"), (req, n_rows, "row_req"), (pos, n_rows, "row_pos"),
+                           (slot, n_rows, "row_slot")):
+            _ints(t, n, name, dev)
+        self._rc(self.lib.dspark_pages_reserve(
+            self._h, _stream(dev, stream), B, page_size, n_pages, K.data_ptr(), length.data_ptr(), table.data_ptr(),
+            ts, cols, held.data_ptr(), held_out.data_ptr(), free_list.data_ptr(), n_free.data_ptr(),
+            n_free_out.data_ptr(), n_rows, offs.data_ptr(), req.data_ptr(), pos.data_ptr(), slot.data_ptr()))
+        return offs, req, pos, slot
+
+    # -- dspark_pages_commit ----------------------------------------------------------
+    def pages_commit(self, length, accept_len, table, held, free_list, n_free, page_size: int, n_pages: int,
+                     finished=None, len_out=None, held_out=None, n_free_out=None, stream=None):
+        """Lengths advanced by accept_len[b] + 1 and the surplus pages pushed
+        back on the free list (every page where finished[b] is nonzero).
+        length, held and n_free are updated in place unless their _out is
+        given.  Returns the new lengths."""
+        dev = self.device
+        _need(length, "length", torch.int32, dev, 1)
+        B = length.shape[0]
+        ts, cols = _table(table, B, dev)
+        len_out = length if len_out is None else len_out
+        held_out = held if held_out is None else held_out
+        n_free_out = n_free if n_free_out is None else n_free_out
+        for t, n, name in ((len_out, B, "len_out"), (accept_len, B, "accept_len"), (held, B, "held"),
+                           (held_out, B, "held_out"), (free_list, n_pages, "free_list"), (n_free, 1, "n_free"),
+                           (n_free_out, 1, "n_free_out")):
+            _ints(t, n, name, dev)
+        if finished is not None:
+            _ints(finished, B, "finished", dev)
+        self._rc(self.lib.dspark_pages_commit(
+            self._h, _stream(dev, stream), B, page_size, n_pages, length.data_ptr(), len_out.data_ptr(),
+            accept_len.data_ptr(), _ptr(finished), table.data_ptr(), ts, cols, held.data_ptr(), held_out.data_ptr(),
+            free_list.data_ptr(), n_free.data_ptr(), n_free_out.data_ptr()))
+        return len_out
+
+    # -- dspark_cache_write -----------------------------------------------------------
+    def cache_write(self, k, v, row_slot, kcache, vcache, k_scale=None, v_scale=None, stream=None):
+        """Rows k, v (bf16 [n_rows][heads][d]) into their slots of the caches
+        ([n_pages][page_size][heads][d], bf16 or float8_e4m3fn with a scale per
+        head; any order of pages, tokens and heads in memory that the strides
+        describe)."""
+        dev = self.device
+        kind, sp, st, sh = _cache(kcache, vcache, k_scale, v_scale, dev)
+        n_pages, page_size, heads, d = kcache.shape
+        _need(k, "k", torch.bfloat16, dev, 3, contiguous=False)
+        _need(v, "v", torch.bfloat16, dev, 3, contiguous=False)
+        n_rows = k.shape[0]
+        if tuple(k.shape) != (n_rows, heads, d) or tuple(v.shape) != (n_rows, heads, d):
+            raise ValueError("k and v must be [n_rows][heads][d] of the cache")
+        if k.stride(2) != 1 or v.stride(2) != 1:
+            raise ValueError("k and v must be contiguous over a head's values")
+        _ints(row_slot, n_rows, "row_slot", dev)
+        self._rc(self.lib.dspark_cache_write(
+            self._h, _stream(dev, stream), n_rows, heads, d, page_size, n_pages, k.data_ptr(), *_steps(k),
+            v.data_ptr(), *_steps(v), row_slot.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), sp, st, sh, kind,
+            _ptr(k_scale), _ptr(v_scale)))
+
     # -- dspark_sts_fit ---------------------------------------------------------------
     def sts_fit(self, logit, accept_len, grid, n_bins: int, out=None, stream=None):
         """Per-position temperatures by ECE grid search on held-out drafts.
@@ -557,4 +698,4 @@ class Context:
 
 __all__ = ["Context", "DSparkError", "load_library", "LIB_PATH", "EXPORTS", "KERNEL_CLASSES",
            "DSPARK_OK", "DSPARK_EINVAL", "DSPARK_EHIP", "DSPARK_ENOMEM", "DSPARK_EDEVICE",
-           "DSPARK_F32", "DSPARK_BF16"]
+           "DSPARK_F32", "DSPARK_BF16", "DSPARK_E4M3"]

@@ -97,6 +97,7 @@ struct dspark_ctx {
   void* ws = nullptr;
   size_t ws_bytes = 0;
   int32_t* dev_err = nullptr;
+  unsigned int* pages_done = nullptr;   // finished workgroups of a page call (inside dev_err's block, zero between calls)
   bool use_graph = false;
   int sweep_waves_per_cu = 8;     // occupancy target of the vocabulary sweeps
   // whole-draft kernel (Markov head, bf16, r = 256): used up to persist_max_b
@@ -1155,6 +1156,46 @@ struct TraceRange {
     if (on) roctx().pop();
   }
 };
+// log2 of a page size, or -1 where it is not one of 8, 16, .. 1024.
+int page_shift(int page_size) {
+  for (int s = 3; s <= 10; ++s)
+    if (page_size == 1 << s) return s;
+  return -1;
+}
+
+int check_pages(dspark_ctx* c, int B, int page_size, int n_pages, int max_pages, int64_t table_stride,
+                const int32_t* table) {
+  if (B < 1 || B > kPagesMaxB) return fail(c, DSPARK_EINVAL, "B must be in 1..%d (got %d)", kPagesMaxB, B);
+  const int sh = page_shift(page_size);
+  if (sh < 0) return fail(c, DSPARK_EINVAL, "page_size must be a power of two in 8..1024 (got %d)", page_size);
+  if (n_pages < 1 || n_pages > (INT32_MAX >> sh))
+    return fail(c, DSPARK_EINVAL, "n_pages must be >= 1 and n_pages * page_size < 2^31");
+  if (max_pages < 1 || max_pages > (INT32_MAX >> sh))
+    return fail(c, DSPARK_EINVAL, "max_pages must be >= 1 and max_pages * page_size < 2^31");
+  if (table_stride < max_pages) return fail(c, DSPARK_EINVAL, "table_stride must be >= max_pages");
+  if (!table) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  return DSPARK_OK;
+}
+
+// Cache placement: tokens of a page one after the other with their heads
+// inside, or heads one after the other with their tokens inside; 16-byte
+// steps.
+int check_cache(dspark_ctx* c, int heads, int d, int page_size, const void* kc, const void* vc, int64_t c_page,
+                int64_t c_tok, int64_t c_head, int kv_dtype) {
+  if (heads < 1 || heads > 1024) return fail(c, DSPARK_EINVAL, "cache heads must be in 1..1024 (got %d)", heads);
+  if (d != 64 && d != 128 && d != 256) return fail(c, DSPARK_EINVAL, "head size must be 64, 128 or 256 (got %d)", d);
+  if (kv_dtype != DSPARK_BF16 && kv_dtype != DSPARK_E4M3)
+    return fail(c, DSPARK_EINVAL, "the cache must be bf16 or e4m3");
+  if (!kc || !vc) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  const int64_t step = kv_dtype == DSPARK_E4M3 ? 16 : 8;
+  if (!aligned16(kc) || !aligned16(vc) || c_page % step || c_tok % step || c_head % step)
+    return fail(c, DSPARK_EINVAL, "the caches must be 16-byte aligned, their strides multiples of 16 bytes");
+  const bool tok_major = c_head >= d && c_tok >= heads * c_head && c_page >= page_size * c_tok;
+  const bool head_major = c_tok >= d && c_head >= page_size * c_tok && c_page >= heads * c_head;
+  if (!tok_major && !head_major) return fail(c, DSPARK_EINVAL, "cache strides overlap");
+  return DSPARK_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1183,6 +1224,7 @@ int dspark_create(dspark_ctx** out, int device) {
   }
   c->bar = reinterpret_cast<unsigned int*>(reinterpret_cast<char*>(c->dev_err) + 128);
   c->chain = reinterpret_cast<unsigned int*>(reinterpret_cast<char*>(c->dev_err) + 512);
+  c->pages_done = reinterpret_cast<unsigned int*>(reinterpret_cast<char*>(c->dev_err) + 896);
   if (hipMalloc(&c->chain_flags, (size_t)kChainMaxGrid * 128) != hipSuccess ||
       hipMemset(c->chain_flags, 0, (size_t)kChainMaxGrid * 128) != hipSuccess) {
     (void)hipGetLastError();
@@ -1344,13 +1386,16 @@ int dspark_check(dspark_ctx* c, hipStream_t stream) {
   DSPARK_HIP(c, hipMemcpy(&flag, c->dev_err, sizeof(flag), hipMemcpyDeviceToHost));
   if (flag) {
     DSPARK_HIP(c, hipMemset(c->dev_err, 0, sizeof(int32_t)));
-    return fail(c, DSPARK_EDEVICE, "device error flag 0x%x:%s%s%s%s%s%s", flag,
+    return fail(c, DSPARK_EDEVICE, "device error flag 0x%x:%s%s%s%s%s%s%s%s%s%s", flag,
                 (flag & kErrToken) ? " token id out of range" : "",
                 (flag & kErrK) ? " verify length out of range" : "",
                 (flag & kErrRow) ? " packed target row out of range" : "",
                 (flag & kErrBarrier) ? " grid barrier timed out" : "",
                 (flag & kErrGrid) ? " candidate temperature not positive and finite" : "",
-                (flag & kErrLen) ? " accepted length out of range" : "");
+                (flag & kErrLen) ? " accepted length out of range" : "",
+                (flag & kErrPool) ? " page pool too small" : "", (flag & kErrPage) ? " page id out of range" : "",
+                (flag & kErrCache) ? " cache length, page or row count out of range" : "",
+                (flag & kErrSlot) ? " cache slot out of range" : "");
   }
   c->err.clear();
   return DSPARK_OK;
@@ -1659,6 +1704,140 @@ int dspark_stream_read(dspark_ctx* c, hipStream_t stream, const float* x, int64_
   a.out = out;
   if ((rc = klaunch(c, DSPARK_K_DIAG, stream_read_kernel(), dim3(grid), dim3(kStreamThreads), &a, stream))) return rc;
   return klaunch(c, DSPARK_K_DIAG, stream_sum_kernel(), dim3(1), dim3(kStreamThreads), &a, stream);
+}
+
+int dspark_pages_reserve(dspark_ctx* c, hipStream_t stream, int B, int page_size, int n_pages, const int32_t* K,
+                         const int32_t* len, int32_t* table, int64_t table_stride, int max_pages,
+                         const int32_t* held, int32_t* held_out, const int32_t* free_list, const int32_t* n_free,
+                         int32_t* n_free_out, int n_rows, int32_t* t_offsets, int32_t* row_req, int32_t* row_pos,
+                         int32_t* row_slot) {
+  TraceRange trace_range("dspark_pages_reserve");
+  if (!c) return DSPARK_EINVAL;
+  int rc = check_pages(c, B, page_size, n_pages, max_pages, table_stride, table);
+  if (rc) return rc;
+  if (n_rows < 0) return fail(c, DSPARK_EINVAL, "n_rows must be >= 0");
+  if (!K || !len || !held || !held_out || !free_list || !n_free || !n_free_out || !t_offsets ||
+      (n_rows > 0 && (!row_req || !row_pos || !row_slot)))
+    return fail(c, DSPARK_EINVAL, "null pointer argument");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
+  PagesArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = B;
+  a.page_shift = page_shift(page_size);
+  a.n_pages = n_pages;
+  a.cols = max_pages;
+  a.n_rows = n_rows;
+  a.K = K;
+  a.len = len;
+  a.table = table;
+  a.tstride = table_stride;
+  a.held = held;
+  a.held_out = held_out;
+  a.free_list = const_cast<int32_t*>(free_list);
+  a.n_free = n_free;
+  a.n_free_out = n_free_out;
+  a.offs = t_offsets;
+  a.row_req = row_req;
+  a.row_pos = row_pos;
+  a.row_slot = row_slot;
+  a.done = c->pages_done;
+  a.err = c->dev_err;
+  // a workgroup per 1024 rows, at most one per CU
+  const int grid = std::max(1, std::min(c->cu_count, (n_rows + 1023) / 1024));
+  return klaunch(c, DSPARK_K_PAGES, pages_reserve_kernel(), dim3(grid), dim3(kPagesThreads), &a, stream);
+}
+
+int dspark_pages_commit(dspark_ctx* c, hipStream_t stream, int B, int page_size, int n_pages, const int32_t* len,
+                        int32_t* len_out, const int32_t* accept_len, const int32_t* finished, const int32_t* table,
+                        int64_t table_stride, int max_pages, const int32_t* held, int32_t* held_out,
+                        int32_t* free_list, const int32_t* n_free, int32_t* n_free_out) {
+  TraceRange trace_range("dspark_pages_commit");
+  if (!c) return DSPARK_EINVAL;
+  int rc = check_pages(c, B, page_size, n_pages, max_pages, table_stride, table);
+  if (rc) return rc;
+  if (!len || !len_out || !accept_len || !held || !held_out || !free_list || !n_free || !n_free_out)
+    return fail(c, DSPARK_EINVAL, "null pointer argument");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
+  PagesArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = B;
+  a.page_shift = page_shift(page_size);
+  a.n_pages = n_pages;
+  a.cols = max_pages;
+  a.len = len;
+  a.accept = accept_len;
+  a.finished = finished;
+  a.table = const_cast<int32_t*>(table);
+  a.tstride = table_stride;
+  a.held = held;
+  a.held_out = held_out;
+  a.len_out = len_out;
+  a.free_list = free_list;
+  a.n_free = n_free;
+  a.n_free_out = n_free_out;
+  a.done = c->pages_done;
+  a.err = c->dev_err;
+  // how many pages come back is known on the device alone: a workgroup per 32
+  // requests, and where whole requests may end one per 4096 table entries
+  const int64_t most = finished ? (int64_t)B * max_pages / 4096 : 0;
+  const int grid = (int)std::max<int64_t>(1, std::min<int64_t>(c->cu_count, std::max<int64_t>(B / 32, most)));
+  return klaunch(c, DSPARK_K_PAGES, pages_commit_kernel(), dim3(grid), dim3(kPagesThreads), &a, stream);
+}
+
+int dspark_cache_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
+                       const void* k, int64_t k_stride_row, int64_t k_stride_head, const void* v,
+                       int64_t v_stride_row, int64_t v_stride_head, const int32_t* row_slot, void* kcache,
+                       void* vcache, int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                       dspark_dtype kv_dtype, const float* k_scale, const float* v_scale) {
+  TraceRange trace_range("dspark_cache_write");
+  if (!c) return DSPARK_EINVAL;
+  const int sh = page_shift(page_size);
+  if (sh < 0) return fail(c, DSPARK_EINVAL, "page_size must be a power of two in 8..1024 (got %d)", page_size);
+  if (n_pages < 1 || n_pages > (INT32_MAX >> sh))
+    return fail(c, DSPARK_EINVAL, "n_pages must be >= 1 and n_pages * page_size < 2^31");
+  int rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype);
+  if (rc) return rc;
+  const bool e4m3 = kv_dtype == DSPARK_E4M3;
+  if (!e4m3 && (k_scale || v_scale)) return fail(c, DSPARK_EINVAL, "scales belong to an e4m3 cache");
+  if (n_rows < 0) return fail(c, DSPARK_EINVAL, "n_rows must be >= 0");
+  if (n_rows == 0) return DSPARK_OK;
+  if (!k || !v || !row_slot) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  if (!aligned16(k) || !aligned16(v) || (k_stride_row & 7) || (k_stride_head & 7) || (v_stride_row & 7) ||
+      (v_stride_head & 7) || k_stride_row < 0 || k_stride_head < 0 || v_stride_row < 0 || v_stride_head < 0)
+    return fail(c, DSPARK_EINVAL, "k and v must be 16-byte aligned, their strides multiples of 8");
+  const int per_head = e4m3 ? d / 16 : d / 8;
+  if ((int64_t)n_rows * heads * per_head > INT32_MAX - kCacheThreads)
+    return fail(c, DSPARK_EINVAL, "too many rows (%d)", n_rows);
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
+  const int64_t size = e4m3 ? 1 : 2;
+  CacheWriteArgs a;
+  memset(&a, 0, sizeof(a));
+  a.n_slots = (int64_t)n_pages << sh;
+  a.n_rows = n_rows;
+  a.heads = heads;
+  a.chunks = heads * per_head;
+  a.chunk_shift = __builtin_ctz(per_head);
+  a.page_shift = sh;
+  a.k = static_cast<const uint16_t*>(k);
+  a.k_row = k_stride_row;
+  a.k_head = k_stride_head;
+  a.v = static_cast<const uint16_t*>(v);
+  a.v_row = v_stride_row;
+  a.v_head = v_stride_head;
+  a.slot = row_slot;
+  a.kc = static_cast<unsigned char*>(kcache);
+  a.vc = static_cast<unsigned char*>(vcache);
+  a.c_page = c_stride_page * size;
+  a.c_tok = c_stride_tok * size;
+  a.c_head = c_stride_head * size;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.err = c->dev_err;
+  const int grid = (n_rows * a.chunks + kCacheThreads - 1) / kCacheThreads;
+  return klaunch(c, DSPARK_K_CACHE, cache_write_kernel(e4m3), dim3(grid), dim3(kCacheThreads), &a, stream);
 }
 
 }  // extern "C"

@@ -23,6 +23,10 @@ constexpr int kErrRow = 4;      // a packed target row outside [0, n_rows)
 constexpr int kErrBarrier = 8;  // a grid barrier of the whole-draft kernel gave up waiting
 constexpr int kErrGrid = 16;    // a candidate temperature that is not positive and finite
 constexpr int kErrLen = 32;     // an accepted length outside [0, gamma] (temperature fit)
+constexpr int kErrPool = 64;    // the page pool is short of (or full beyond) what a call needs
+constexpr int kErrPage = 128;   // a page id outside [0, n_pages)
+constexpr int kErrCache = 256;  // a cache length, page count or row count outside its arrays
+constexpr int kErrSlot = 512;   // a cache slot outside [-1, n_pages * page_size)
 
 // Element offset of target row (b, k) (k 1-based): strided [B][gamma+1][V]
 // placement, or the packed layout where request b's rows 1 .. K_b + 1 start

@@ -224,6 +224,57 @@ struct GruArgs {
   int32_t* err;
 };
 
+// Page bookkeeping of the key-value cache (pages.hip).  Per-request arrays of
+// up to kPagesMaxB requests are scanned in LDS by every workgroup.
+constexpr int kPagesMaxB = 4096;
+constexpr int kPagesThreads = 256;
+
+struct PagesArgs {
+  int B, page_shift, n_pages, cols;   // cols: entries of a block-table row
+  int n_rows;                    // reserve: rows the packed arrays hold
+  const int32_t* K;              // reserve: rows - 1 of each request
+  const int32_t* len;            // tokens in the cache
+  const int32_t* accept;         // commit: accepted drafts, -1 = no rows
+  const int32_t* finished;       // commit: nonzero = the request ends (nullable)
+  int32_t* table;                // [B][stride] page ids
+  int64_t tstride;
+  const int32_t* held;           // pages each request holds; held_out may be the same array
+  int32_t* held_out;
+  int32_t* len_out;              // commit; may be len
+  int32_t* free_list;            // [n_pages] stack of free page ids, top at n_free - 1
+  const int32_t* n_free;         // [1]; n_free_out may be the same word
+  int32_t* n_free_out;
+  int32_t* offs;                 // reserve: [B + 1]
+  int32_t* row_req;              // reserve: [n_rows] each
+  int32_t* row_pos;
+  int32_t* row_slot;
+  unsigned int* done;            // finished workgroups, zero at launch and left zero
+  int32_t* err;
+};
+const void* pages_reserve_kernel();
+const void* pages_commit_kernel();
+
+// Cache write (cache.hip): strides in elements.
+struct CacheWriteArgs {
+  int64_t n_slots;               // n_pages * page_size
+  int n_rows, heads, chunks;     // chunks of 16 cache bytes per row: heads * d * size / 16
+  int chunk_shift;               // log2 of the chunks per head
+  int page_shift;
+  const uint16_t* k;             // bf16 rows
+  int64_t k_row, k_head;
+  const uint16_t* v;
+  int64_t v_row, v_head;
+  const int32_t* slot;           // [n_rows], -1 = skip
+  unsigned char* kc;             // caches: [n_pages][page][heads][d] through strides (in bytes)
+  unsigned char* vc;
+  int64_t c_page, c_tok, c_head;
+  const float* k_scale;          // [heads], 8-bit cache (nullable: 1)
+  const float* v_scale;
+  int32_t* err;
+};
+constexpr int kCacheThreads = 256;
+const void* cache_write_kernel(int e4m3);
+
 // Kernel lookup (host stubs usable with hipLaunchKernel and graph nodes).
 // `wdtype`: 0 = fp32, 1 = bf16.  `depth` = D > 0: the workgroup-shared
 // W2-tile variant walking `nt` 16-wide tiles per step and loading D steps
