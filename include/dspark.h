@@ -130,7 +130,8 @@ enum {
   DSPARK_K_CONF_MERGE = 14,    /* draft merge + confidences (dspark_draft_markov_conf) */
   DSPARK_K_PAGES = 15,         /* page bookkeeping (reserve, commit) */
   DSPARK_K_CACHE = 16,         /* keys and values into the cache */
-  DSPARK_K_COUNT = 17
+  DSPARK_K_ATTEND = 17,        /* attention over the paged cache, and the join of its pieces */
+  DSPARK_K_COUNT = 18
 };
 int dspark_timing_enable(dspark_ctx* ctx, int enable);
 int dspark_timing_read(dspark_ctx* ctx, double* ms, int* launches);
@@ -522,6 +523,44 @@ int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int head
                        const int32_t* row_slot, void* kcache, void* vcache,
                        int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
                        dspark_dtype kv_dtype, const float* k_scale, const float* v_scale);
+
+/* Attention of packed rows over the paged cache.
+ *
+ * Row i (0 .. K[b]) of request b stands at t_offsets[b] + i of q and out.  For
+ * query head h, reading cache head g = h / (heads_q / heads):
+ *     s_t = scale * k_scale[g] * q[row][h] . kcache[t][g]
+ *     out[row][h] = v_scale[g] * sum_t softmax(s)_t vcache[t][g]
+ *     lse[row][h] = ln sum_t exp(s_t)
+ * over the tokens t it sees: causal != 0: t <= len[b] + i (a verify row sees
+ * the cache, the drafts before it and itself); causal == 0: t < len[b] + K[b]
+ * + 1 (the positions of a draft block see each other: [blog] the backbone's
+ * non-causal query block).  gamma = 0 is one token a request.  The rows' own
+ * keys and values are in the cache already (dspark_cache_write).  Masked
+ * tokens have no effect, whatever their bits are; entries of a page behind the
+ * last token are not read.  Scores and sums are float32; a weight is rounded
+ * to bf16 before its product with the values, and the result to bf16.
+ * len, K: int32 [B] (K NULL: gamma for all; -1: no rows; outside -1..gamma:
+ * clamped and flagged); t_offsets: int32 [>= B] or NULL for b * (gamma + 1);
+ * rows that no request takes are left as they are.  A request whose length
+ * or rows pass its table row or n_rows is flagged and takes no part; a page
+ * id outside [0, n_pages) is flagged and read as page 0.
+ * q, out: bf16 [n_rows][heads_q][d] through row and head strides (multiples
+ * of 8, 16-byte aligned); lse: float [n_rows][heads_q] or NULL.  heads_q a
+ * multiple of heads, at most 64 times; 0 <= gamma <= 32; scale positive and
+ * finite; caches, scales, pages as above.  out may not overlap any input.
+ * Two launches (timing class DSPARK_K_ATTEND); the work is shared out on the
+ * device, so nothing depends on the lengths being known to the host.  The
+ * context keeps 48 MB for the pieces of tiles from its first call on; results
+ * do not depend on earlier calls and are bitwise repeatable.  Errors:
+ * DSPARK_EINVAL, DSPARK_ENOMEM. */
+int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads, int d,
+                  const void* q, int64_t q_stride_row, int64_t q_stride_head,
+                  const void* kcache, const void* vcache,
+                  int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                  dspark_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                  int page_size, int n_pages, const int32_t* table, int64_t table_stride, int max_pages,
+                  const int32_t* len, const int32_t* K, const int32_t* t_offsets, int causal, float scale,
+                  void* out, int64_t o_stride_row, int64_t o_stride_head, float* lse);
 
 /* Fit the per-position confidence temperatures (sequential temperature
  * scaling) on held-out drafts.

@@ -25,12 +25,12 @@ EXPORTS = (
     "dspark_draft_markov", "dspark_draft_markov_static", "dspark_draft_markov_conf", "dspark_draft_rnn",
     "dspark_confidence", "dspark_schedule", "dspark_schedule_async", "dspark_verify",
     "dspark_verify_packed", "dspark_accept_prob", "dspark_sts_fit", "dspark_stream_read",
-    "dspark_pages_reserve", "dspark_pages_commit", "dspark_cache_write",
+    "dspark_pages_reserve", "dspark_pages_commit", "dspark_cache_write", "dspark_attend",
     "dspark_timing_enable", "dspark_timing_read",
 )
 KERNEL_CLASSES = ("draft_sweep", "draft_combine", "confidence", "survival", "schedule",
                   "verify_rows", "verify_decide", "resid_sweep", "resid_combine", "gru", "diag", "sts_fit",
-                  "draft_chain", "verify_chain", "conf_merge", "pages", "cache")
+                  "draft_chain", "verify_chain", "conf_merge", "pages", "cache", "attend")
 
 _lib = None
 _vp, _i32, _i64, _u64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
@@ -115,6 +115,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.dspark_cache_write.argtypes = [
         _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _i64,
         _i32, _vp, _vp]
+    lib.dspark_attend.restype = _i32
+    lib.dspark_attend.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp,
+        _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _f32, _vp, _i64, _i64, _vp]
     if path is None:
         _lib = lib
     return lib
@@ -652,6 +656,47 @@ class Context:
             self._h, _stream(dev, stream), n_rows, heads, d, page_size, n_pages, k.data_ptr(), *_steps(k),
             v.data_ptr(), *_steps(v), row_slot.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), sp, st, sh, kind,
             _ptr(k_scale), _ptr(v_scale)))
+
+    # -- dspark_attend ----------------------------------------------------------------
+    def attend(self, q, kcache, vcache, table, length, gamma: int, K=None, t_offsets=None, causal: bool = True,
+               scale: Optional[float] = None, k_scale=None, v_scale=None, out=None, lse=None, stream=None):
+        """Attention of the packed rows q (bf16 [n_rows][heads_q][d]) over the
+        paged cache ([n_pages][page_size][heads][d]).  Request b has K[b] + 1
+        rows (gamma + 1 where K is None) from t_offsets[b] on (b * (gamma + 1)
+        where None).  scale defaults to d ** -0.5.  Returns out (bf16, q's
+        shape; rows of no request are left as they are); ``lse``: a float32
+        [n_rows][heads_q] tensor to fill with the log-sum-exps."""
+        dev = self.device
+        kind, sp, st, sh = _cache(kcache, vcache, k_scale, v_scale, dev)
+        n_pages, page_size, heads, d = kcache.shape
+        _need(q, "q", torch.bfloat16, dev, 3, contiguous=False)
+        n_rows, heads_q, dq = q.shape
+        if dq != d or q.stride(2) != 1:
+            raise ValueError("q must be [n_rows][heads_q][d], contiguous over a head's values")
+        _need(length, "length", torch.int32, dev, 1)
+        B = length.shape[0]
+        ts, cols = _table(table, B, dev)
+        if K is not None:
+            _ints(K, B, "K", dev)
+        if t_offsets is not None:
+            _need(t_offsets, "t_offsets", torch.int32, dev, 1)
+            if t_offsets.shape[0] < B:
+                raise ValueError(f"t_offsets must have at least {B} entries")
+        if out is None:
+            out = torch.zeros((n_rows, heads_q, d), dtype=torch.bfloat16, device=dev)
+        _need(out, "out", torch.bfloat16, dev, 3, contiguous=False)
+        if out.shape != q.shape or out.stride(2) != 1:
+            raise ValueError("out must have the shape of q and be contiguous over a head's values")
+        if lse is not None:
+            _need(lse, "lse", torch.float32, dev, 2)
+            if tuple(lse.shape) != (n_rows, heads_q):
+                raise ValueError("lse must be [n_rows][heads_q]")
+        self._rc(self.lib.dspark_attend(
+            self._h, _stream(dev, stream), B, n_rows, gamma, heads_q, heads, d, q.data_ptr(), *_steps(q),
+            kcache.data_ptr(), vcache.data_ptr(), sp, st, sh, kind, _ptr(k_scale), _ptr(v_scale), page_size, n_pages,
+            table.data_ptr(), ts, cols, length.data_ptr(), _ptr(K), _ptr(t_offsets), 1 if causal else 0,
+            d ** -0.5 if scale is None else float(scale), out.data_ptr(), *_steps(out), _ptr(lse)))
+        return out
 
     # -- dspark_sts_fit ---------------------------------------------------------------
     def sts_fit(self, logit, accept_len, grid, n_bins: int, out=None, stream=None):

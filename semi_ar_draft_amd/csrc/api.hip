@@ -177,6 +177,13 @@ struct dspark_ctx {
   // per-request counters of dspark_draft_markov_conf (zero between calls)
   unsigned int* cm_cnt = nullptr;
   size_t cm_n = 0;
+  // attention: pieces of tiles and what each stretch begins with, one size for
+  // every shape (allocated at the first call and kept, so that captured calls
+  // stay valid); resident workgroups per CU of each variant (-1 = not asked)
+  unsigned char* attend_buf = nullptr;
+  int attend_wg_per_cu[3][3][2] = {{{-1, -1}, {-1, -1}, {-1, -1}},
+                                   {{-1, -1}, {-1, -1}, {-1, -1}},
+                                   {{-1, -1}, {-1, -1}, {-1, -1}}};
   // draft: running best (key, index) per (position, request), zero between calls
   unsigned long long* best = nullptr;
   size_t best_n = 0;
@@ -1369,6 +1376,7 @@ void dspark_destroy(dspark_ctx* c) {
     if (c->dev_err) (void)hipFree(c->dev_err);
     if (c->chain_flags) (void)hipFree(c->chain_flags);
     if (c->vq) (void)hipFree(c->vq);
+    if (c->attend_buf) (void)hipFree(c->attend_buf);
     if (c->cm_cnt) (void)hipFree(c->cm_cnt);
   }
   delete c;
@@ -1838,6 +1846,112 @@ int dspark_cache_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads,
   a.err = c->dev_err;
   const int grid = (n_rows * a.chunks + kCacheThreads - 1) / kCacheThreads;
   return klaunch(c, DSPARK_K_CACHE, cache_write_kernel(e4m3), dim3(grid), dim3(kCacheThreads), &a, stream);
+}
+
+int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads, int d,
+                  const void* q, int64_t q_stride_row, int64_t q_stride_head, const void* kcache, const void* vcache,
+                  int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head, dspark_dtype kv_dtype,
+                  const float* k_scale, const float* v_scale, int page_size, int n_pages, const int32_t* table,
+                  int64_t table_stride, int max_pages, const int32_t* len, const int32_t* K,
+                  const int32_t* t_offsets, int causal, float scale, void* out, int64_t o_stride_row,
+                  int64_t o_stride_head, float* lse) {
+  TraceRange trace_range("dspark_attend");
+  if (!c) return DSPARK_EINVAL;
+  int rc = check_pages(c, B, page_size, n_pages, max_pages, table_stride, table);
+  if (rc) return rc;
+  if ((rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype)))
+    return rc;
+  const int sh = page_shift(page_size);
+  const bool e4m3 = kv_dtype == DSPARK_E4M3;
+  if (!e4m3 && (k_scale || v_scale)) return fail(c, DSPARK_EINVAL, "scales belong to an e4m3 cache");
+  if (gamma < 0 || gamma > kMaxGamma) return fail(c, DSPARK_EINVAL, "gamma must be in 0..%d", kMaxGamma);
+  if (n_rows < 0 || (!t_offsets && (int64_t)B * (gamma + 1) > n_rows))
+    return fail(c, DSPARK_EINVAL, "n_rows must hold B * (gamma + 1) rows where t_offsets is NULL");
+  if (n_rows == 0) return DSPARK_OK;
+  if (heads_q < 1 || heads_q % heads || heads_q / heads > 64)
+    return fail(c, DSPARK_EINVAL, "heads_q must be 1 to 64 times heads (got %d, %d)", heads_q, heads);
+  if (!q || !out || !len) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  if (!aligned16(q) || !aligned16(out) || (q_stride_row & 7) || (q_stride_head & 7) || (o_stride_row & 7) ||
+      (o_stride_head & 7) || q_stride_row < 0 || q_stride_head < 0 || o_stride_row < 0 || o_stride_head < 0)
+    return fail(c, DSPARK_EINVAL, "q and out must be 16-byte aligned, their strides multiples of 8");
+  // rows and heads of the result that are there more than once must not overlap
+  const bool row_major = (heads_q == 1 || o_stride_head >= d) &&
+                         (n_rows == 1 || o_stride_row >= (heads_q == 1 ? d : heads_q * o_stride_head));
+  const bool head_major = (n_rows == 1 || o_stride_row >= d) &&
+                          (heads_q == 1 || o_stride_head >= (n_rows == 1 ? d : n_rows * o_stride_row));
+  if (!row_major && !head_major) return fail(c, DSPARK_EINVAL, "out strides overlap");
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(c, DSPARK_EINVAL, "scale must be positive and finite");
+  // the fewest 16-row blocks that hold a request's rows of one cache head, up
+  // to 64 rows (d = 256: 32): a tile reads its keys once for all of them
+  const int group = heads_q / heads, most = group * (gamma + 1);
+  const int mt = most <= 16 ? 1 : most <= 32 || d == 256 ? 2 : 4;
+  const int64_t tiles = (most + 16 * mt - 1) / (16 * mt);
+  const int64_t tokens = (int64_t)max_pages << sh;
+  if (tokens > INT32_MAX - 4096 || heads * tiles * ((tokens + 127) / 128) > INT32_MAX)
+    return fail(c, DSPARK_EINVAL, "max_pages * page_size is too large");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
+  constexpr size_t kHead = kAttendMaxGrid * sizeof(AttendPiece);
+  if (!c->attend_buf) {
+    if (hipMalloc(&c->attend_buf, kHead + kAttendPartBytes) != hipSuccess) {
+      (void)hipGetLastError();
+      c->attend_buf = nullptr;
+      return fail(c, DSPARK_ENOMEM, "allocation of %zu bytes failed", kHead + kAttendPartBytes);
+    }
+  }
+  const void* fn = attend_kernel(d, mt, e4m3);
+  int& wg = c->attend_wg_per_cu[d / 128][mt / 2][e4m3];
+  if (wg < 0) {
+    int nb = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&nb, fn, kAttendThreads, 0) != hipSuccess) {
+      (void)hipGetLastError();
+      nb = 0;
+    }
+    wg = std::max(1, nb);
+  }
+  const size_t piece = (size_t)16 * mt * (d + 2) * sizeof(float);
+  const int grid = (int)std::min<size_t>(std::min(kAttendMaxGrid, wg * c->cu_count), kAttendPartBytes / (2 * piece));
+  AttendArgs a;
+  memset(&a, 0, sizeof(a));
+  const int64_t size = e4m3 ? 1 : 2;
+  a.B = B;
+  a.n_rows = n_rows;
+  a.gamma = gamma;
+  a.Hq = heads_q;
+  a.Hkv = heads;
+  a.group = group;
+  a.page_shift = sh;
+  a.n_pages = n_pages;
+  a.cols = max_pages;
+  a.causal = causal != 0;
+  a.rows = 16 * mt;
+  a.min_units = 1;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_row = q_stride_row;
+  a.q_head = q_stride_head;
+  a.kc = static_cast<const unsigned char*>(kcache);
+  a.vc = static_cast<const unsigned char*>(vcache);
+  a.c_page = c_stride_page * size;
+  a.c_tok = c_stride_tok * size;
+  a.c_head = c_stride_head * size;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.table = table;
+  a.tstride = table_stride;
+  a.len = len;
+  a.K = K;
+  a.offs = t_offsets;
+  a.scale2 = scale * kLog2e;
+  a.out = static_cast<uint16_t*>(out);
+  a.o_row = o_stride_row;
+  a.o_head = o_stride_head;
+  a.lse = lse;
+  a.pieces = reinterpret_cast<AttendPiece*>(c->attend_buf);
+  a.part = reinterpret_cast<float*>(c->attend_buf + kHead);
+  a.err = c->dev_err;
+  if ((rc = klaunch(c, DSPARK_K_ATTEND, fn, dim3(grid), dim3(kAttendThreads), &a, stream))) return rc;
+  if (grid == 1) return DSPARK_OK;
+  return klaunch(c, DSPARK_K_ATTEND, attend_join_kernel(d), dim3(grid - 1, 4 * mt), dim3(kAttendThreads), &a, stream);
 }
 
 }  // extern "C"

@@ -275,6 +275,46 @@ struct CacheWriteArgs {
 constexpr int kCacheThreads = 256;
 const void* cache_write_kernel(int e4m3);
 
+// Attention of packed rows over the paged cache (attend.hip).
+// What a workgroup's stretch of units begins with: the tile (request, cache
+// head, row tile), its units, the unit of the tile it begins at (0: at the
+// tile's start, or no stretch), and the tile's first unit in the batch's line.
+struct AttendPiece {
+  int b, h, rt, n_t, t0;
+  int64_t unit0, chunk;
+};
+
+struct AttendArgs {
+  int B, n_rows, gamma, Hq, Hkv, group, page_shift, n_pages, cols, causal;
+  int rows;                      // rows of a tile: 16 mt
+  int min_units;                 // units per workgroup at least
+  const uint16_t* q;             // bf16
+  int64_t q_row, q_head;
+  const unsigned char* kc;       // caches, strides in bytes
+  const unsigned char* vc;
+  int64_t c_page, c_tok, c_head;
+  const float* k_scale;          // [Hkv], e4m3 cache (nullable: 1)
+  const float* v_scale;
+  const int32_t* table;
+  int64_t tstride;
+  const int32_t* len;
+  const int32_t* K;              // nullable: gamma
+  const int32_t* offs;           // nullable: b * (gamma + 1)
+  float scale2;                  // scale * log2(e)
+  uint16_t* out;                 // bf16
+  int64_t o_row, o_head;
+  float* lse;                    // [n_rows][Hq], nullable
+  AttendPiece* pieces;           // [grid]
+  float* part;                   // [grid][2]: m [rows], sum [rows], unscaled result [rows][d]
+  int32_t* err;
+};
+constexpr int kAttendThreads = 256;
+constexpr int kAttendMaxGrid = 2048;
+constexpr size_t kAttendPartBytes = (size_t)48 << 20;
+// mt: 16-row blocks of a tile (1, 2; 4 where d < 256)
+const void* attend_kernel(int d, int mt, int e4m3);
+const void* attend_join_kernel(int d);
+
 // Kernel lookup (host stubs usable with hipLaunchKernel and graph nodes).
 // `wdtype`: 0 = fp32, 1 = bf16.  `depth` = D > 0: the workgroup-shared
 // W2-tile variant walking `nt` 16-wide tiles per step and loading D steps
