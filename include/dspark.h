@@ -131,7 +131,8 @@ enum {
   DSPARK_K_PAGES = 15,         /* page bookkeeping (reserve, commit) */
   DSPARK_K_CACHE = 16,         /* keys and values into the cache */
   DSPARK_K_ATTEND = 17,        /* attention over the paged cache, and the join of its pieces */
-  DSPARK_K_COUNT = 18
+  DSPARK_K_CONSTRAIN = 18,     /* penalties, biases and masks on logit rows */
+  DSPARK_K_COUNT = 19
 };
 int dspark_timing_enable(dspark_ctx* ctx, int enable);
 int dspark_timing_read(dspark_ctx* ctx, double* ms, int* launches);
@@ -448,6 +449,7 @@ int dspark_verify_packed(dspark_ctx* ctx, hipStream_t stream,
  *     dspark_schedule -> K
  *     dspark_pages_reserve -> t_offsets, row positions and cache slots
  *     (per layer) dspark_cache_write, dspark_attend
+ *     dspark_constrain -> the float32 rows that verification reads
  *     dspark_verify_packed (t_offsets, K) -> accept_len
  *     dspark_pages_commit -> new lengths, surplus pages back in the pool
  * Every number they need stays on the device, so a whole step can be
@@ -561,6 +563,54 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
                   int page_size, int n_pages, const int32_t* table, int64_t table_stride, int max_pages,
                   const int32_t* len, const int32_t* K, const int32_t* t_offsets, int causal, float scale,
                   void* out, int64_t o_stride_row, int64_t o_stride_head, float* lse);
+
+/* Penalties, biases and grammar masks on logit rows.
+ *
+ * [blog] "形式化定义": the target scores every drafted position in one pass.
+ * Row i (0-based) of request b follows the request's history and its first i
+ * drafts.  For every vocabulary entry v with logit l, c = the occurrences of v
+ * in hist[b][n_prompt[b] .. n_hist[b]) and among tokens[b][0 .. i), seen = v
+ * occurs there or in hist[b][0 .. n_prompt[b]):
+ *     l1  = seen ? (l > 0 ? l / rep[b] : l * rep[b]) : l
+ *     l2  = l1 - freq[b] * c - (c > 0 ? pres[b] : 0) + (sum of v's biases)
+ *     out = allowed(v) ? max(l2, DSPARK_MASKED) : DSPARK_MASKED
+ * in float32.  DSPARK_MASKED is finite, so that the rows can be drafted and
+ * verified from as they are (-infinity would make a log-sum-exp NaN): logits
+ * of -infinity or the type's lowest value become DSPARK_MASKED too; NaN
+ * stays.  A row whose mask allows nothing is DSPARK_MASKED throughout.
+ *
+ * logits: dtype BF16 or F32, V entries a row (any V), rows 16-byte aligned.
+ * out: float, the same rows; F32 logits may be constrained in place (out =
+ * logits with equal strides), otherwise the two may not overlap.
+ * t_offsets NULL: row i of request b at b * stride_b + i * stride_k
+ * (elements; request-major or position-major), n_rows unused; else packed:
+ * row t_offsets[b] + i of n_rows rows of stride_k.  Requests have K[b] + 1
+ * rows (-1 .. n_pos - 1; outside: clamped and flagged), n_pos where K is
+ * NULL; a request whose packed rows pass n_rows is flagged and left alone.
+ * hist: int32 [B][hist_stride], n_hist (0 .. hist_max), n_prompt int32 [B]
+ * (n_prompt NULL: no prompt); hist NULL: no history.  tokens: int32 [B]
+ * [tok_stride], the drafts (>= n_pos - 1 a request), or NULL: drafts do not
+ * count (a draft's own rows).  rep (positive, finite; else flagged and 1),
+ * freq, pres: float [B], or NULL for 1, 0, 0.  bias_ids, bias_values:
+ * [B][bias_stride], of which the first n_bias[b] (NULL: bias_max) count; ids
+ * ascend (else flagged), equal ids add up in order.  mask: int32 words, bit v
+ * % 32 of word v / 32 set where v is allowed, placed like the rows with its
+ * own strides (in words); NULL: all allowed.  Token ids outside [0, V) are
+ * flagged and ignored.
+ * 1 <= n_pos <= 33, B <= 65535.  One launch (timing class
+ * DSPARK_K_CONSTRAIN), no workspace.  Errors: DSPARK_EINVAL. */
+#define DSPARK_MASKED (-1.0e30f)
+int dspark_constrain(dspark_ctx* ctx, hipStream_t stream, int B, int n_pos, int V,
+                     const void* logits, dspark_dtype dtype, int64_t l_stride_b, int64_t l_stride_k,
+                     const int32_t* t_offsets, const int32_t* K, int n_rows,
+                     const int32_t* hist, int64_t hist_stride, int hist_max,
+                     const int32_t* n_hist, const int32_t* n_prompt,
+                     const int32_t* tokens, int64_t tok_stride,
+                     const float* rep, const float* freq, const float* pres,
+                     const int32_t* bias_ids, const float* bias_values, int64_t bias_stride, int bias_max,
+                     const int32_t* n_bias,
+                     const int32_t* mask, int64_t mask_stride_b, int64_t mask_stride_k,
+                     float* out, int64_t o_stride_b, int64_t o_stride_k);
 
 /* Fit the per-position confidence temperatures (sequential temperature
  * scaling) on held-out drafts.

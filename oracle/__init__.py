@@ -35,6 +35,7 @@ from .schedule import schedule, schedule_async, ScheduleResult
 from .verify import verify, VerifyResult, target_logprobs, accept_ratio, residual_weights, accept_prob
 from .step import run_step, step_lengths, StepResult
 from .paged import pages_reserve, pages_commit, e4m3_levels, to_e4m3, attend
+from .constrain import constrain, MASKED
 from .sts_fit import ece, labels, candidate_scores, sts_fit, StsFit
 
 __all__ = [
@@ -43,5 +44,5 @@ __all__ = [
     "DraftResult", "confidence", "ConfidenceResult", "schedule", "schedule_async", "ScheduleResult", "verify",
     "VerifyResult", "target_logprobs", "accept_ratio", "residual_weights", "accept_prob", "run_step", "step_lengths",
     "StepResult", "ece", "labels", "candidate_scores", "sts_fit", "StsFit",
-    "pages_reserve", "pages_commit", "e4m3_levels", "to_e4m3", "attend",
+    "pages_reserve", "pages_commit", "e4m3_levels", "to_e4m3", "attend", "constrain", "MASKED",
 ]

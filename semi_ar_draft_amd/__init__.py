@@ -19,18 +19,20 @@ LIB_PATH = os.path.join(_HERE, "libdspark.so")
 
 DSPARK_OK, DSPARK_EINVAL, DSPARK_EHIP, DSPARK_ENOMEM, DSPARK_EDEVICE = 0, 1, 2, 3, 4
 DSPARK_F32, DSPARK_BF16, DSPARK_E4M3 = 0, 1, 2
+MASKED = ctypes.c_float(-1.0e30).value  # what constrain writes where nothing is allowed
 
 EXPORTS = (
     "dspark_version", "dspark_create", "dspark_destroy", "dspark_last_error", "dspark_check",
     "dspark_draft_markov", "dspark_draft_markov_static", "dspark_draft_markov_conf", "dspark_draft_rnn",
     "dspark_confidence", "dspark_schedule", "dspark_schedule_async", "dspark_verify",
     "dspark_verify_packed", "dspark_accept_prob", "dspark_sts_fit", "dspark_stream_read",
-    "dspark_pages_reserve", "dspark_pages_commit", "dspark_cache_write", "dspark_attend",
+    "dspark_pages_reserve", "dspark_pages_commit", "dspark_cache_write", "dspark_attend", "dspark_constrain",
     "dspark_timing_enable", "dspark_timing_read",
 )
 KERNEL_CLASSES = ("draft_sweep", "draft_combine", "confidence", "survival", "schedule",
                   "verify_rows", "verify_decide", "resid_sweep", "resid_combine", "gru", "diag", "sts_fit",
-                  "draft_chain", "verify_chain", "conf_merge", "pages", "cache", "attend")
+                  "draft_chain", "verify_chain", "conf_merge", "pages", "cache", "attend",
+                  "constrain")
 
 _lib = None
 _vp, _i32, _i64, _u64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
@@ -119,6 +121,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.dspark_attend.argtypes = [
         _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp,
         _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _f32, _vp, _i64, _i64, _vp]
+    lib.dspark_constrain.restype = _i32
+    lib.dspark_constrain.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i64,
+        _vp, _vp, _vp, _vp, _vp, _i64, _i32, _vp, _vp, _i64, _i64, _vp, _i64, _i64]
     if path is None:
         _lib = lib
     return lib
@@ -698,6 +704,110 @@ class Context:
             d ** -0.5 if scale is None else float(scale), out.data_ptr(), *_steps(out), _ptr(lse)))
         return out
 
+    # -- dspark_constrain -------------------------------------------------------------
+    def constrain(self, logits, n_pos: int, K=None, t_offsets=None, hist=None, n_hist=None, n_prompt=None, tokens=None,
+                  rep=None, freq=None, pres=None, bias=None, mask=None, out=None, stream=None):
+        """Penalties, biases and grammar masks: float32 rows for draft and verify.
+
+        logits (bf16 or float32): [B][>= n_pos][V], or with t_offsets (int32
+        [>= B]) packed rows [n_rows][V], request b's K[b] + 1 from t_offsets[b]
+        on.  hist int32 [B][hist_max] with n_hist (and n_prompt) int32 [B];
+        tokens int32 [B][>= n_pos - 1], the drafts; rep, freq, pres float32
+        [B]; bias = (ids int32 [B][n], ascending, values float32 [B][n],
+        counts int32 [B] or None); mask int32 words of allowed bits, shaped as
+        the rows are with ceil(V / 32) words.  ``out`` may be float32 logits
+        themselves.  Returns out; rows of no request are left as they are (a
+        new out holds zeros there)."""
+        dev = self.device
+        packed = t_offsets is not None
+        dims = 2 if packed else 3
+        _need(logits, "logits", None, dev, dims, contiguous=False)
+        if logits.dtype == torch.bfloat16:
+            kind = DSPARK_BF16
+        elif logits.dtype == torch.float32:
+            kind = DSPARK_F32
+        else:
+            raise TypeError(f"logits must be bf16 or float32, got {logits.dtype}")
+        if out is None:
+            n, m = (1, logits.shape[0]) if packed else logits.shape[:2]
+            wide = -(-logits.shape[-1] // 4) * 4
+            out = torch.zeros((n, m, wide), dtype=torch.float32, device=dev)[:, :, :logits.shape[-1]]
+            out = out[0] if packed else out
+        _need(out, "out", torch.float32, dev, dims, contiguous=False)
+        V = logits.shape[-1]
+        if out.shape != logits.shape:
+            raise ValueError("out must have the shape of logits")
+        if V > 1 and (logits.stride(-1) != 1 or out.stride(-1) != 1):
+            raise ValueError("logits and out must be contiguous over the vocabulary")
+        if packed:
+            n_rows = logits.shape[0]
+            _need(t_offsets, "t_offsets", torch.int32, dev, 1)
+            if K is None:
+                B = t_offsets.shape[0]
+            else:
+                _need(K, "K", torch.int32, dev, 1)
+                B = K.shape[0]
+            if t_offsets.shape[0] < B:
+                raise ValueError(f"t_offsets must have at least {B} entries")
+        else:
+            B, n_rows = logits.shape[0], 0
+            if logits.shape[1] < n_pos:
+                raise ValueError(f"logits have {logits.shape[1]} positions, n_pos is {n_pos}")
+            if K is not None:
+                _ints(K, B, "K", dev)
+
+        def steps(t, width):
+            """Strides of a request and of a row; a row that is the only one takes its width."""
+            if packed:
+                return 0, t.stride(0) if t.shape[0] > 1 else width
+            return t.stride(0) if B > 1 else 0, t.stride(1) if t.shape[1] > 1 else width
+
+        wide = -(-V // 8) * 8
+        hs = hm = ts = bs = bm = 0
+        if hist is not None:
+            _need(hist, "hist", torch.int32, dev, 2, contiguous=False)
+            if hist.shape[0] != B or (hist.shape[1] > 1 and hist.stride(1) != 1):
+                raise ValueError(f"hist must be [{B}][hist_max] with contiguous rows")
+            hm = hist.shape[1]
+            hs = hist.stride(0) if B > 1 else hm
+            _ints(n_hist, B, "n_hist", dev)
+            if n_prompt is not None:
+                _ints(n_prompt, B, "n_prompt", dev)
+        if tokens is not None:
+            _need(tokens, "tokens", torch.int32, dev, 2, contiguous=False)
+            if tokens.shape[0] != B or tokens.shape[1] < n_pos - 1 or (tokens.shape[1] > 1 and tokens.stride(1) != 1):
+                raise ValueError(f"tokens must be [{B}][>= n_pos - 1] with contiguous rows")
+            ts = tokens.stride(0) if B > 1 else tokens.shape[1]
+        for t, name in ((rep, "rep"), (freq, "freq"), (pres, "pres")):
+            if t is not None:
+                _need(t, name, torch.float32, dev, 1)
+                _len(t, B, name)
+        ids = values = n_bias = None
+        if bias is not None:
+            ids, values, n_bias = bias
+            _need(ids, "bias ids", torch.int32, dev, 2)
+            _need(values, "bias values", torch.float32, dev, 2)
+            if ids.shape[0] != B or values.shape != ids.shape:
+                raise ValueError(f"bias ids and values must be [{B}][n]")
+            bs = bm = ids.shape[1]
+            if n_bias is not None:
+                _ints(n_bias, B, "bias counts", dev)
+        mb = mk = 0
+        if mask is not None:
+            _need(mask, "mask", torch.int32, dev, dims, contiguous=False)
+            words = -(-V // 32)
+            if mask.shape[:-1] != logits.shape[:-1] or mask.shape[-1] < words or (
+                    mask.shape[-1] > 1 and mask.stride(-1) != 1):
+                raise ValueError(f"mask must have the rows of logits and {words} words in each")
+            mb, mk = steps(mask, mask.shape[-1])
+        lb, lk = steps(logits, wide)
+        ob, ok = steps(out, wide)
+        self._rc(self.lib.dspark_constrain(
+            self._h, _stream(dev, stream), B, n_pos, V, logits.data_ptr(), kind, lb, lk, _ptr(t_offsets), _ptr(K),
+            n_rows, _ptr(hist), hs, hm, _ptr(n_hist), _ptr(n_prompt), _ptr(tokens), ts, _ptr(rep), _ptr(freq),
+            _ptr(pres), _ptr(ids), _ptr(values), bs, bm, _ptr(n_bias), _ptr(mask), mb, mk, out.data_ptr(), ob, ok))
+        return out
+
     # -- dspark_sts_fit ---------------------------------------------------------------
     def sts_fit(self, logit, accept_len, grid, n_bins: int, out=None, stream=None):
         """Per-position temperatures by ECE grid search on held-out drafts.
@@ -743,4 +853,4 @@ class Context:
 
 __all__ = ["Context", "DSparkError", "load_library", "LIB_PATH", "EXPORTS", "KERNEL_CLASSES",
            "DSPARK_OK", "DSPARK_EINVAL", "DSPARK_EHIP", "DSPARK_ENOMEM", "DSPARK_EDEVICE",
-           "DSPARK_F32", "DSPARK_BF16", "DSPARK_E4M3"]
+           "DSPARK_F32", "DSPARK_BF16", "DSPARK_E4M3", "MASKED"]

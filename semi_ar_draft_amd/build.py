@@ -17,7 +17,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libdspark.so")
 SOURCES = ["api.hip", "sweep.hip", "verify.hip", "confidence.hip", "schedule.hip", "gru.hip", "sts.hip",
-           "stream.hip", "pages.hip", "cache.hip", "attend.hip"]
+           "stream.hip", "pages.hip", "cache.hip", "attend.hip", "constrain.hip"]
 ARCH = os.environ.get("DSPARK_OFFLOAD_ARCH", "gfx950")
 
 COMMON_FLAGS = [

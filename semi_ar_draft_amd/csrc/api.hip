@@ -1394,7 +1394,7 @@ int dspark_check(dspark_ctx* c, hipStream_t stream) {
   DSPARK_HIP(c, hipMemcpy(&flag, c->dev_err, sizeof(flag), hipMemcpyDeviceToHost));
   if (flag) {
     DSPARK_HIP(c, hipMemset(c->dev_err, 0, sizeof(int32_t)));
-    return fail(c, DSPARK_EDEVICE, "device error flag 0x%x:%s%s%s%s%s%s%s%s%s%s", flag,
+    return fail(c, DSPARK_EDEVICE, "device error flag 0x%x:%s%s%s%s%s%s%s%s%s%s%s%s%s", flag,
                 (flag & kErrToken) ? " token id out of range" : "",
                 (flag & kErrK) ? " verify length out of range" : "",
                 (flag & kErrRow) ? " packed target row out of range" : "",
@@ -1403,7 +1403,10 @@ int dspark_check(dspark_ctx* c, hipStream_t stream) {
                 (flag & kErrLen) ? " accepted length out of range" : "",
                 (flag & kErrPool) ? " page pool too small" : "", (flag & kErrPage) ? " page id out of range" : "",
                 (flag & kErrCache) ? " cache length, page or row count out of range" : "",
-                (flag & kErrSlot) ? " cache slot out of range" : "");
+                (flag & kErrSlot) ? " cache slot out of range" : "",
+                (flag & kErrHist) ? " history or bias length out of range" : "",
+                (flag & kErrBias) ? " bias ids not ascending" : "",
+                (flag & kErrPenalty) ? " repetition penalty not positive and finite" : "");
   }
   c->err.clear();
   return DSPARK_OK;
@@ -1952,6 +1955,88 @@ int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   if ((rc = klaunch(c, DSPARK_K_ATTEND, fn, dim3(grid), dim3(kAttendThreads), &a, stream))) return rc;
   if (grid == 1) return DSPARK_OK;
   return klaunch(c, DSPARK_K_ATTEND, attend_join_kernel(d), dim3(grid - 1, 4 * mt), dim3(kAttendThreads), &a, stream);
+}
+
+int dspark_constrain(dspark_ctx* c, hipStream_t stream, int B, int n_pos, int V, const void* logits,
+                     dspark_dtype dtype, int64_t l_stride_b, int64_t l_stride_k, const int32_t* t_offsets,
+                     const int32_t* K, int n_rows, const int32_t* hist, int64_t hist_stride, int hist_max,
+                     const int32_t* n_hist, const int32_t* n_prompt, const int32_t* tokens, int64_t tok_stride,
+                     const float* rep, const float* freq, const float* pres, const int32_t* bias_ids,
+                     const float* bias_values, int64_t bias_stride, int bias_max, const int32_t* n_bias,
+                     const int32_t* mask, int64_t mask_stride_b, int64_t mask_stride_k, float* out,
+                     int64_t o_stride_b, int64_t o_stride_k) {
+  TraceRange trace_range("dspark_constrain");
+  if (!c) return DSPARK_EINVAL;
+  if (B < 1 || B > 65535) return fail(c, DSPARK_EINVAL, "B must be in 1..65535 (got %d)", B);
+  if (n_pos < 1 || n_pos > kMaxGamma + 1) return fail(c, DSPARK_EINVAL, "n_pos must be in 1..%d", kMaxGamma + 1);
+  if (V < 1 || V > (1 << 29)) return fail(c, DSPARK_EINVAL, "V must be in 1..2^29");
+  if (dtype != DSPARK_F32 && dtype != DSPARK_BF16) return fail(c, DSPARK_EINVAL, "logits must be float32 or bf16");
+  if (n_rows < 0) return fail(c, DSPARK_EINVAL, "n_rows must be >= 0");
+  if (t_offsets && n_rows == 0) return DSPARK_OK;
+  if (!logits || !out || (hist && !n_hist) || (bias_ids && !bias_values))
+    return fail(c, DSPARK_EINVAL, "null pointer argument");
+  const bool bf16 = dtype == DSPARK_BF16;
+  const int64_t step = bf16 ? 8 : 4;
+  if (!aligned16(logits) || !aligned16(out) || l_stride_k % step || o_stride_k % 4 ||
+      (!t_offsets && (l_stride_b % step || o_stride_b % 4)))
+    return fail(c, DSPARK_EINVAL, "logit rows must be 16-byte aligned");
+  // rows that are there more than once must not overlap: packed, request-major or position-major
+  auto apart = [&](int64_t sb, int64_t sk, int64_t width) {
+    if (t_offsets) return sk >= width;
+    return (n_pos == 1 || sk >= width) && (B == 1 || sb >= (n_pos == 1 ? width : n_pos * sk)) ? true
+           : (B == 1 || sb >= width) && (n_pos == 1 || sk >= (B == 1 ? width : B * sb));
+  };
+  if (!apart(l_stride_b, l_stride_k, V) || !apart(o_stride_b, o_stride_k, V))
+    return fail(c, DSPARK_EINVAL, "logit strides overlap rows of %d values", V);
+  if (mask && !apart(mask_stride_b, mask_stride_k, (V + 31) / 32))
+    return fail(c, DSPARK_EINVAL, "mask strides overlap rows of %d words", (V + 31) / 32);
+  if (hist && (hist_max < 0 || hist_max >= (1 << 29) || hist_stride < hist_max))
+    return fail(c, DSPARK_EINVAL, "hist_max must be in 0..2^29 - 1 and at most hist_stride");
+  if (tokens && tok_stride < n_pos - 1) return fail(c, DSPARK_EINVAL, "tokens must hold n_pos - 1 entries a request");
+  if (bias_ids && (bias_max < 0 || bias_stride < bias_max))
+    return fail(c, DSPARK_EINVAL, "bias_max must be >= 0 and at most bias_stride");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
+  ConstrainArgs a;
+  memset(&a, 0, sizeof(a));
+  a.B = B;
+  a.n_pos = n_pos;
+  a.V = V;
+  a.n_rows = n_rows;
+  a.offs = t_offsets;
+  a.K = K;
+  a.in = logits;
+  a.in_b = l_stride_b;
+  a.in_k = l_stride_k;
+  a.out = out;
+  a.out_b = o_stride_b;
+  a.out_k = o_stride_k;
+  a.hist = hist;
+  a.hist_stride = hist_stride;
+  a.hist_max = hist_max;
+  a.n_hist = n_hist;
+  a.n_prompt = n_prompt;
+  a.tokens = tokens;
+  a.tok_stride = tok_stride;
+  a.rep = rep;
+  a.freq = freq;
+  a.pres = pres;
+  a.bias_id = bias_max > 0 ? bias_ids : nullptr;
+  a.bias_val = bias_values;
+  a.bias_stride = bias_stride;
+  a.bias_max = bias_max;
+  a.n_bias = n_bias;
+  a.mask = reinterpret_cast<const uint32_t*>(mask);
+  a.mask_b = mask_stride_b;
+  a.mask_k = mask_stride_k;
+  a.err = c->dev_err;
+  // the largest slice that leaves four workgroups a CU (each reads the
+  // request's whole history)
+  int slice = kConstrainMaxSlice;
+  while (slice > 1024 && (int64_t)B * ((V + slice - 1) / slice) < 4L * c->cu_count) slice /= 2;
+  a.slice = slice;
+  return klaunch(c, DSPARK_K_CONSTRAIN, constrain_kernel(bf16), dim3((V + slice - 1) / slice, B),
+                 dim3(kConstrainThreads), &a, stream);
 }
 
 }  // extern "C"

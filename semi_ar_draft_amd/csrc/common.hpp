@@ -27,6 +27,14 @@ constexpr int kErrPool = 64;    // the page pool is short of (or full beyond) wh
 constexpr int kErrPage = 128;   // a page id outside [0, n_pages)
 constexpr int kErrCache = 256;  // a cache length, page count or row count outside its arrays
 constexpr int kErrSlot = 512;   // a cache slot outside [-1, n_pages * page_size)
+constexpr int kErrHist = 1024;  // a history or bias length outside its array
+constexpr int kErrBias = 2048;  // bias ids that do not ascend
+constexpr int kErrPenalty = 4096;   // a repetition penalty that is not positive and finite
+
+// What dspark_constrain writes where nothing is allowed: low enough for a
+// weight of zero at any temperature, high enough that scaling and sums of
+// logits stay finite.
+constexpr float kMasked = -1.0e30f;
 
 // Element offset of target row (b, k) (k 1-based): strided [B][gamma+1][V]
 // placement, or the packed layout where request b's rows 1 .. K_b + 1 start

@@ -315,6 +315,39 @@ constexpr size_t kAttendPartBytes = (size_t)48 << 20;
 const void* attend_kernel(int d, int mt, int e4m3);
 const void* attend_join_kernel(int d);
 
+// Logit constraints (constrain.hip): rows (b, i) at b * stride_b + i *
+// stride_k, or packed rows offs[b] + i at stride_k.
+struct ConstrainArgs {
+  int B, n_pos, V, slice, n_rows;
+  const int32_t* offs;           // nullable
+  const int32_t* K;              // rows - 1 of each request; nullable: n_pos rows
+  const void* in;                // bf16 or float
+  int64_t in_b, in_k;
+  float* out;
+  int64_t out_b, out_k;
+  const int32_t* hist;           // [B][hist_stride], nullable
+  int64_t hist_stride;
+  int hist_max;
+  const int32_t* n_hist;
+  const int32_t* n_prompt;       // nullable: 0
+  const int32_t* tokens;         // [B][tok_stride] drafted tokens, nullable
+  int64_t tok_stride;
+  const float* rep;              // [B], each nullable
+  const float* freq;
+  const float* pres;
+  const int32_t* bias_id;        // [B][bias_stride], nullable
+  const float* bias_val;
+  int64_t bias_stride;
+  int bias_max;
+  const int32_t* n_bias;         // nullable: bias_max
+  const uint32_t* mask;          // words of allowed bits, nullable
+  int64_t mask_b, mask_k;
+  int32_t* err;
+};
+constexpr int kConstrainThreads = 256;
+constexpr int kConstrainMaxSlice = 8192;
+const void* constrain_kernel(int bf16);
+
 // Kernel lookup (host stubs usable with hipLaunchKernel and graph nodes).
 // `wdtype`: 0 = fp32, 1 = bf16.  `depth` = D > 0: the workgroup-shared
 // W2-tile variant walking `nt` 16-wide tiles per step and loading D steps
