@@ -130,7 +130,7 @@ enum {
   DSPARK_K_CONF_MERGE = 14,    /* draft merge + confidences (dspark_draft_markov_conf) */
   DSPARK_K_PAGES = 15,         /* page bookkeeping (reserve, commit) */
   DSPARK_K_CACHE = 16,         /* keys and values into the cache */
-  DSPARK_K_ATTEND = 17,        /* attention over the paged cache, and the join of its pieces */
+  DSPARK_K_ATTEND = 17,        /* attention over the paged cache */
   DSPARK_K_CONSTRAIN = 18,     /* penalties, biases and masks on logit rows */
   DSPARK_K_COUNT = 19
 };
@@ -538,8 +538,8 @@ int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int head
  * + 1 (the positions of a draft block see each other: [blog] the backbone's
  * non-causal query block).  gamma = 0 is one token a request.  The rows' own
  * keys and values are in the cache already (dspark_cache_write).  Masked
- * tokens have no effect, whatever their bits are; entries of a page behind the
- * last token are not read.  Scores and sums are float32; a weight is rounded
+ * tokens and the places of a page behind the last token have no effect,
+ * whatever their bits are. Scores and sums are float32; a weight is rounded
  * to bf16 before its product with the values, and the result to bf16.
  * len, K: int32 [B] (K NULL: gamma for all; -1: no rows; outside -1..gamma:
  * clamped and flagged); t_offsets: int32 [>= B] or NULL for b * (gamma + 1);
@@ -552,8 +552,8 @@ int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int head
  * finite; caches, scales, pages as above.  out may not overlap any input.
  * Two launches (timing class DSPARK_K_ATTEND); the work is shared out on the
  * device, so nothing depends on the lengths being known to the host.  The
- * context keeps 48 MB for the pieces of tiles from its first call on; results
- * do not depend on earlier calls and are bitwise repeatable.  Errors:
+ * context keeps 34 MB for the pieces of the work from its first call on;
+ * results do not depend on earlier calls and are bitwise repeatable.  Errors:
  * DSPARK_EINVAL, DSPARK_ENOMEM. */
 int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads, int d,
                   const void* q, int64_t q_stride_row, int64_t q_stride_head,

@@ -29,6 +29,8 @@ EXPORTS = (
     "dspark_pages_reserve", "dspark_pages_commit", "dspark_cache_write", "dspark_attend", "dspark_constrain",
     "dspark_timing_enable", "dspark_timing_read",
 )
+_LOGIT_TYPES = {torch.bfloat16: DSPARK_BF16, torch.float32: DSPARK_F32}
+_CACHE_TYPES = {torch.bfloat16: DSPARK_BF16, torch.float8_e4m3fn: DSPARK_E4M3}
 KERNEL_CLASSES = ("draft_sweep", "draft_combine", "confidence", "survival", "schedule",
                   "verify_rows", "verify_decide", "resid_sweep", "resid_combine", "gru", "diag", "sts_fit",
                   "draft_chain", "verify_chain", "conf_merge", "pages", "cache", "attend",
@@ -136,7 +138,8 @@ def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
 
 def _stream(device: torch.device, stream) -> int:
     if stream is None:
-        stream = torch.cuda.current_stream(device)
+        # the current stream's handle without a Stream object around it
+        return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream
 
 
@@ -173,45 +176,62 @@ def _logits3(t: torch.Tensor, name: str, device):
     return t.stride(0), t.stride(1)
 
 
-def _ints(t: torch.Tensor, n: int, name: str, device):
-    """A contiguous int32 vector of n entries."""
-    _need(t, name, torch.int32, device, 1)
-    if t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+def _ints(device: torch.device, *vectors):
+    """Contiguous int32 vectors on the device, given as (tensor, entries, name).
+
+    The calls over a paged cache take ten of them at a few microseconds a
+    call, so what is right is told from four attributes; what is not goes
+    through the full checks for its message."""
+    index = device.index
+    for t, n, name in vectors:
+        if type(t) is torch.Tensor and t.numel() == n and t.dtype is torch.int32 and t.get_device() == index and \
+                t.dim() == 1 and t.is_contiguous():
+            continue
+        _need(t, name, torch.int32, device, 1)
+        if t.shape[0] != n:
+            raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
 
 
 def _table(table: torch.Tensor, B: int, device):
     """Row stride and columns of a block table."""
-    _need(table, "table", torch.int32, device, 2, contiguous=False)
-    if table.shape[0] != B or table.stride(1) != 1:
+    if not (type(table) is torch.Tensor and table.dtype is torch.int32 and table.get_device() == device.index and
+            table.dim() == 2):
+        _need(table, "table", torch.int32, device, 2, contiguous=False)
+    rows, cols = table.shape
+    step, one = table.stride()
+    if rows != B or one != 1 and cols > 1:
         raise ValueError(f"table must be [{B}][max_pages] with contiguous rows")
-    return table.stride(0), table.shape[1]
+    return (step if B > 1 else cols), cols
+
+
+def _rows(t: torch.Tensor, name: str, dtype, device, dims: int):
+    """A tensor of this type and rank on the device, contiguous in its last dimension."""
+    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device.index and t.dim() == dims):
+        _need(t, name, dtype, device, dims, contiguous=False)
+    if t.stride(-1) != 1 and t.shape[-1] > 1:
+        raise ValueError(f"{name} must be contiguous over its last dimension")
 
 
 def _cache(kc: torch.Tensor, vc: torch.Tensor, k_scale, v_scale, device):
     """Element type of a pair of caches, and their strides of a page, a token and a head."""
-    if kc.dtype == torch.bfloat16:
-        kind = DSPARK_BF16
-    elif kc.dtype == torch.float8_e4m3fn:
-        kind = DSPARK_E4M3
-    else:
+    kind = _CACHE_TYPES.get(kc.dtype)
+    if kind is None:
         raise TypeError(f"the cache must be bf16 or float8_e4m3fn, got {kc.dtype}")
-    _need(kc, "kcache", None, device, 4, contiguous=False)
-    _need(vc, "vcache", kc.dtype, device, 4, contiguous=False)
-    sp, st, sh, sd = kc.stride()
-    if vc.shape != kc.shape or vc.stride() != (sp, st, sh, sd):
+    _rows(kc, "kcache", kc.dtype, device, 4)
+    _rows(vc, "vcache", kc.dtype, device, 4)
+    strides = kc.stride()
+    if vc.shape != kc.shape or vc.stride() != strides:
         raise ValueError("kcache and vcache must have one shape and one set of strides")
+    sp, st, sh, _ = strides
     n, page, heads, d = kc.shape
     if heads == 1:                     # steps that are never taken: torch leaves them arbitrary
         sh = d
     if n == 1:
         sp = max(page * st, heads * sh)
-    if sd != 1:
-        raise ValueError("the cache must be contiguous over a head's values")
     for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
         if t is not None:
             _need(t, name, torch.float32, device, 1)
-            _len(t, kc.shape[2], name)
+            _len(t, heads, name)
     return kind, sp, st, sh
 
 
@@ -593,7 +613,6 @@ class Context:
         arrays have n_rows entries (or those of ``out``).  Returns t_offsets
         [B + 1], row_req, row_pos, row_slot [n_rows] (int32)."""
         dev = self.device
-        _need(K, "K", torch.int32, dev, 1)
         B = K.shape[0]
         ts, cols = _table(table, B, dev)
         held_out = held if held_out is None else held_out
@@ -604,11 +623,9 @@ class Context:
             out = tuple(torch.empty((n,), dtype=torch.int32, device=dev) for n in (B + 1, n_rows, n_rows, n_rows))
         offs, req, pos, slot = out
         n_rows = slot.shape[0] if n_rows is None else n_rows
-        for t, n, name in ((length, B, "length"), (held, B, "held"), (held_out, B, "held_out"),
-                           (free_list, n_pages, "free_list"), (n_free, 1, "n_free"), (n_free_out, 1, "n_free_out"),
-                           (offs, B + 1, "t_offsets"), (req, n_rows, "row_req"), (pos, n_rows, "row_pos"),
-                           (slot, n_rows, "row_slot")):
-            _ints(t, n, name, dev)
+        _ints(dev, (K, B, "K"), (length, B, "length"), (held, B, "held"), (held_out, B, "held_out"),
+              (free_list, n_pages, "free_list"), (n_free, 1, "n_free"), (n_free_out, 1, "n_free_out"),
+              (offs, B + 1, "t_offsets"), (req, n_rows, "row_req"), (pos, n_rows, "row_pos"), (slot, n_rows, "row_slot"))
         self._rc(self.lib.dspark_pages_reserve(
             self._h, _stream(dev, stream), B, page_size, n_pages, K.data_ptr(), length.data_ptr(), table.data_ptr(),
             ts, cols, held.data_ptr(), held_out.data_ptr(), free_list.data_ptr(), n_free.data_ptr(),
@@ -623,18 +640,16 @@ class Context:
         length, held and n_free are updated in place unless their _out is
         given.  Returns the new lengths."""
         dev = self.device
-        _need(length, "length", torch.int32, dev, 1)
         B = length.shape[0]
         ts, cols = _table(table, B, dev)
         len_out = length if len_out is None else len_out
         held_out = held if held_out is None else held_out
         n_free_out = n_free if n_free_out is None else n_free_out
-        for t, n, name in ((len_out, B, "len_out"), (accept_len, B, "accept_len"), (held, B, "held"),
-                           (held_out, B, "held_out"), (free_list, n_pages, "free_list"), (n_free, 1, "n_free"),
-                           (n_free_out, 1, "n_free_out")):
-            _ints(t, n, name, dev)
+        _ints(dev, (length, B, "length"), (len_out, B, "len_out"), (accept_len, B, "accept_len"), (held, B, "held"),
+              (held_out, B, "held_out"), (free_list, n_pages, "free_list"), (n_free, 1, "n_free"),
+              (n_free_out, 1, "n_free_out"))
         if finished is not None:
-            _ints(finished, B, "finished", dev)
+            _ints(dev, (finished, B, "finished"))
         self._rc(self.lib.dspark_pages_commit(
             self._h, _stream(dev, stream), B, page_size, n_pages, length.data_ptr(), len_out.data_ptr(),
             accept_len.data_ptr(), _ptr(finished), table.data_ptr(), ts, cols, held.data_ptr(), held_out.data_ptr(),
@@ -650,14 +665,12 @@ class Context:
         dev = self.device
         kind, sp, st, sh = _cache(kcache, vcache, k_scale, v_scale, dev)
         n_pages, page_size, heads, d = kcache.shape
-        _need(k, "k", torch.bfloat16, dev, 3, contiguous=False)
-        _need(v, "v", torch.bfloat16, dev, 3, contiguous=False)
+        _rows(k, "k", torch.bfloat16, dev, 3)
+        _rows(v, "v", torch.bfloat16, dev, 3)
         n_rows = k.shape[0]
-        if tuple(k.shape) != (n_rows, heads, d) or tuple(v.shape) != (n_rows, heads, d):
+        if k.shape != (n_rows, heads, d) or v.shape != (n_rows, heads, d):
             raise ValueError("k and v must be [n_rows][heads][d] of the cache")
-        if k.stride(2) != 1 or v.stride(2) != 1:
-            raise ValueError("k and v must be contiguous over a head's values")
-        _ints(row_slot, n_rows, "row_slot", dev)
+        _ints(dev, (row_slot, n_rows, "row_slot"))
         self._rc(self.lib.dspark_cache_write(
             self._h, _stream(dev, stream), n_rows, heads, d, page_size, n_pages, k.data_ptr(), *_steps(k),
             v.data_ptr(), *_steps(v), row_slot.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), sp, st, sh, kind,
@@ -675,27 +688,27 @@ class Context:
         dev = self.device
         kind, sp, st, sh = _cache(kcache, vcache, k_scale, v_scale, dev)
         n_pages, page_size, heads, d = kcache.shape
-        _need(q, "q", torch.bfloat16, dev, 3, contiguous=False)
+        _rows(q, "q", torch.bfloat16, dev, 3)
         n_rows, heads_q, dq = q.shape
-        if dq != d or q.stride(2) != 1:
-            raise ValueError("q must be [n_rows][heads_q][d], contiguous over a head's values")
-        _need(length, "length", torch.int32, dev, 1)
+        if dq != d:
+            raise ValueError("q must be [n_rows][heads_q][d] with the cache's d")
         B = length.shape[0]
         ts, cols = _table(table, B, dev)
+        _ints(dev, (length, B, "length"))
         if K is not None:
-            _ints(K, B, "K", dev)
+            _ints(dev, (K, B, "K"))
         if t_offsets is not None:
-            _need(t_offsets, "t_offsets", torch.int32, dev, 1)
+            _rows(t_offsets, "t_offsets", torch.int32, dev, 1)
             if t_offsets.shape[0] < B:
                 raise ValueError(f"t_offsets must have at least {B} entries")
         if out is None:
             out = torch.zeros((n_rows, heads_q, d), dtype=torch.bfloat16, device=dev)
-        _need(out, "out", torch.bfloat16, dev, 3, contiguous=False)
-        if out.shape != q.shape or out.stride(2) != 1:
-            raise ValueError("out must have the shape of q and be contiguous over a head's values")
+        _rows(out, "out", torch.bfloat16, dev, 3)
+        if out.shape != q.shape:
+            raise ValueError("out must have the shape of q")
         if lse is not None:
             _need(lse, "lse", torch.float32, dev, 2)
-            if tuple(lse.shape) != (n_rows, heads_q):
+            if lse.shape != (n_rows, heads_q):
                 raise ValueError("lse must be [n_rows][heads_q]")
         self._rc(self.lib.dspark_attend(
             self._h, _stream(dev, stream), B, n_rows, gamma, heads_q, heads, d, q.data_ptr(), *_steps(q),
@@ -721,40 +734,31 @@ class Context:
         dev = self.device
         packed = t_offsets is not None
         dims = 2 if packed else 3
-        _need(logits, "logits", None, dev, dims, contiguous=False)
-        if logits.dtype == torch.bfloat16:
-            kind = DSPARK_BF16
-        elif logits.dtype == torch.float32:
-            kind = DSPARK_F32
-        else:
+        kind = _LOGIT_TYPES.get(logits.dtype)
+        if kind is None:
             raise TypeError(f"logits must be bf16 or float32, got {logits.dtype}")
+        _rows(logits, "logits", logits.dtype, dev, dims)
         if out is None:
             n, m = (1, logits.shape[0]) if packed else logits.shape[:2]
             wide = -(-logits.shape[-1] // 4) * 4
             out = torch.zeros((n, m, wide), dtype=torch.float32, device=dev)[:, :, :logits.shape[-1]]
             out = out[0] if packed else out
-        _need(out, "out", torch.float32, dev, dims, contiguous=False)
+        _rows(out, "out", torch.float32, dev, dims)
         V = logits.shape[-1]
         if out.shape != logits.shape:
             raise ValueError("out must have the shape of logits")
-        if V > 1 and (logits.stride(-1) != 1 or out.stride(-1) != 1):
-            raise ValueError("logits and out must be contiguous over the vocabulary")
         if packed:
             n_rows = logits.shape[0]
             _need(t_offsets, "t_offsets", torch.int32, dev, 1)
-            if K is None:
-                B = t_offsets.shape[0]
-            else:
-                _need(K, "K", torch.int32, dev, 1)
-                B = K.shape[0]
+            B = t_offsets.shape[0] if K is None else K.shape[0]
             if t_offsets.shape[0] < B:
                 raise ValueError(f"t_offsets must have at least {B} entries")
         else:
             B, n_rows = logits.shape[0], 0
             if logits.shape[1] < n_pos:
                 raise ValueError(f"logits have {logits.shape[1]} positions, n_pos is {n_pos}")
-            if K is not None:
-                _ints(K, B, "K", dev)
+        if K is not None:
+            _ints(dev, (K, B, "K"))
 
         def steps(t, width):
             """Strides of a request and of a row; a row that is the only one takes its width."""
@@ -765,22 +769,22 @@ class Context:
         wide = -(-V // 8) * 8
         hs = hm = ts = bs = bm = 0
         if hist is not None:
-            _need(hist, "hist", torch.int32, dev, 2, contiguous=False)
-            if hist.shape[0] != B or (hist.shape[1] > 1 and hist.stride(1) != 1):
-                raise ValueError(f"hist must be [{B}][hist_max] with contiguous rows")
+            _rows(hist, "hist", torch.int32, dev, 2)
+            if hist.shape[0] != B:
+                raise ValueError(f"hist must be [{B}][hist_max]")
             hm = hist.shape[1]
             hs = hist.stride(0) if B > 1 else hm
-            _ints(n_hist, B, "n_hist", dev)
+            _ints(dev, (n_hist, B, "n_hist"))
             if n_prompt is not None:
-                _ints(n_prompt, B, "n_prompt", dev)
+                _ints(dev, (n_prompt, B, "n_prompt"))
         if tokens is not None:
-            _need(tokens, "tokens", torch.int32, dev, 2, contiguous=False)
-            if tokens.shape[0] != B or tokens.shape[1] < n_pos - 1 or (tokens.shape[1] > 1 and tokens.stride(1) != 1):
-                raise ValueError(f"tokens must be [{B}][>= n_pos - 1] with contiguous rows")
+            _rows(tokens, "tokens", torch.int32, dev, 2)
+            if tokens.shape[0] != B or tokens.shape[1] < n_pos - 1:
+                raise ValueError(f"tokens must be [{B}][>= n_pos - 1]")
             ts = tokens.stride(0) if B > 1 else tokens.shape[1]
         for t, name in ((rep, "rep"), (freq, "freq"), (pres, "pres")):
             if t is not None:
-                _need(t, name, torch.float32, dev, 1)
+                _rows(t, name, torch.float32, dev, 1)
                 _len(t, B, name)
         ids = values = n_bias = None
         if bias is not None:
@@ -791,13 +795,12 @@ class Context:
                 raise ValueError(f"bias ids and values must be [{B}][n]")
             bs = bm = ids.shape[1]
             if n_bias is not None:
-                _ints(n_bias, B, "bias counts", dev)
+                _ints(dev, (n_bias, B, "bias counts"))
         mb = mk = 0
         if mask is not None:
-            _need(mask, "mask", torch.int32, dev, dims, contiguous=False)
+            _rows(mask, "mask", torch.int32, dev, dims)
             words = -(-V // 32)
-            if mask.shape[:-1] != logits.shape[:-1] or mask.shape[-1] < words or (
-                    mask.shape[-1] > 1 and mask.stride(-1) != 1):
+            if mask.shape[:-1] != logits.shape[:-1] or mask.shape[-1] < words:
                 raise ValueError(f"mask must have the rows of logits and {words} words in each")
             mb, mk = steps(mask, mask.shape[-1])
         lb, lk = steps(logits, wide)

@@ -177,13 +177,9 @@ struct dspark_ctx {
   // per-request counters of dspark_draft_markov_conf (zero between calls)
   unsigned int* cm_cnt = nullptr;
   size_t cm_n = 0;
-  // attention: pieces of tiles and what each stretch begins with, one size for
-  // every shape (allocated at the first call and kept, so that captured calls
-  // stay valid); resident workgroups per CU of each variant (-1 = not asked)
+  // attention: the tiles to join and their pieces, one size for every shape
+  // (allocated at the first call and kept, so that captured calls stay valid)
   unsigned char* attend_buf = nullptr;
-  int attend_wg_per_cu[3][3][2] = {{{-1, -1}, {-1, -1}, {-1, -1}},
-                                   {{-1, -1}, {-1, -1}, {-1, -1}},
-                                   {{-1, -1}, {-1, -1}, {-1, -1}}};
   // draft: running best (key, index) per (position, request), zero between calls
   unsigned long long* best = nullptr;
   size_t best_n = 0;
@@ -1200,6 +1196,7 @@ int check_cache(dspark_ctx* c, int heads, int d, int page_size, const void* kc, 
   const bool tok_major = c_head >= d && c_tok >= heads * c_head && c_page >= page_size * c_tok;
   const bool head_major = c_tok >= d && c_head >= page_size * c_tok && c_page >= heads * c_head;
   if (!tok_major && !head_major) return fail(c, DSPARK_EINVAL, "cache strides overlap");
+  if (c_tok > INT32_MAX / 32) return fail(c, DSPARK_EINVAL, "cache token stride too large");
   return DSPARK_OK;
 }
 
@@ -1890,30 +1887,19 @@ int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   const int mt = most <= 16 ? 1 : most <= 32 || d == 256 ? 2 : 4;
   const int64_t tiles = (most + 16 * mt - 1) / (16 * mt);
   const int64_t tokens = (int64_t)max_pages << sh;
-  if (tokens > INT32_MAX - 4096 || heads * tiles * ((tokens + 127) / 128) > INT32_MAX)
+  if (tokens > INT32_MAX - 4096 || heads * tiles * (tokens / 32 + 64) > INT32_MAX)
     return fail(c, DSPARK_EINVAL, "max_pages * page_size is too large");
   DeviceGuard dg(c->device);
   if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
-  constexpr size_t kHead = kAttendMaxGrid * sizeof(AttendPiece);
   if (!c->attend_buf) {
-    if (hipMalloc(&c->attend_buf, kHead + kAttendPartBytes) != hipSuccess) {
+    if (hipMalloc(&c->attend_buf, kAttendJoinBytes + kAttendPartBytes) != hipSuccess) {
       (void)hipGetLastError();
       c->attend_buf = nullptr;
-      return fail(c, DSPARK_ENOMEM, "allocation of %zu bytes failed", kHead + kAttendPartBytes);
+      return fail(c, DSPARK_ENOMEM, "allocation of %zu bytes failed", kAttendJoinBytes + kAttendPartBytes);
     }
   }
   const void* fn = attend_kernel(d, mt, e4m3);
-  int& wg = c->attend_wg_per_cu[d / 128][mt / 2][e4m3];
-  if (wg < 0) {
-    int nb = 0;
-    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&nb, fn, kAttendThreads, 0) != hipSuccess) {
-      (void)hipGetLastError();
-      nb = 0;
-    }
-    wg = std::max(1, nb);
-  }
-  const size_t piece = (size_t)16 * mt * (d + 2) * sizeof(float);
-  const int grid = (int)std::min<size_t>(std::min(kAttendMaxGrid, wg * c->cu_count), kAttendPartBytes / (2 * piece));
+  const int grid = std::min(kAttendMaxGrid, c->cu_count);
   AttendArgs a;
   memset(&a, 0, sizeof(a));
   const int64_t size = e4m3 ? 1 : 2;
@@ -1928,7 +1914,8 @@ int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   a.cols = max_pages;
   a.causal = causal != 0;
   a.rows = 16 * mt;
-  a.min_units = 1;
+  a.tile_cost = 1;
+  a.min_steps = 2;
   a.q = static_cast<const uint16_t*>(q);
   a.q_row = q_stride_row;
   a.q_head = q_stride_head;
@@ -1949,12 +1936,11 @@ int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   a.o_row = o_stride_row;
   a.o_head = o_stride_head;
   a.lse = lse;
-  a.pieces = reinterpret_cast<AttendPiece*>(c->attend_buf);
-  a.part = reinterpret_cast<float*>(c->attend_buf + kHead);
+  a.joins = reinterpret_cast<AttendJoin*>(c->attend_buf);
+  a.part = reinterpret_cast<float*>(c->attend_buf + kAttendJoinBytes);
   a.err = c->dev_err;
   if ((rc = klaunch(c, DSPARK_K_ATTEND, fn, dim3(grid), dim3(kAttendThreads), &a, stream))) return rc;
-  if (grid == 1) return DSPARK_OK;
-  return klaunch(c, DSPARK_K_ATTEND, attend_join_kernel(d), dim3(grid - 1, 4 * mt), dim3(kAttendThreads), &a, stream);
+  return klaunch(c, DSPARK_K_ATTEND, attend_join_kernel(d), dim3(grid, mt), dim3(kAttendThreads), &a, stream);
 }
 
 int dspark_constrain(dspark_ctx* c, hipStream_t stream, int B, int n_pos, int V, const void* logits,

@@ -11,28 +11,38 @@
 //
 // Work: a tile is the rows of one request that share a cache head (rows times
 // heads per group, 16 MT of them at a time, so that a key is read once for
-// all of them) over the request's tokens in units of 128.  All units of the
-// batch stand in one line, request by request, and every workgroup takes an
-// equal stretch of it, so that ragged lengths load the chip evenly without the
-// host knowing them; a tile that falls to several workgroups is joined from
-// its pieces by a second launch.
+// all of them) over the request's tokens in steps of 32.  All tiles of the
+// batch stand in one line, request by request, each as long as its steps and
+// what it costs besides them, and every wave takes an equal stretch of the
+// line, so that ragged lengths load the chip evenly without the host knowing
+// them.  The four waves of a workgroup have neighbouring stretches and join
+// what they share of a tile in LDS when they are done; what a workgroup shares
+// with its neighbours it leaves in memory, and a second launch adds the pieces
+// up in the order of their tokens.
 //
-// In a workgroup each of the four waves takes 32 tokens of a unit.  Scores
-// are formed transposed, S^T = K Q^T, and so is the product, O^T = V^T P^T:
-// then the accumulators of the first product (a lane: one query, tokens 4 g + i
-// of the two 16-token halves, g = lane / 16) are in place as the second's
-// operand, whose eight products per lane may be taken in any order of tokens as
-// long as the values come in the same order.  A lane loads its eight tokens'
-// values at D / 16 neighbouring places, whole cache lines per token, and
-// exchanges rows for columns within its own registers.  No key, value or score
-// passes through LDS.
+// One workgroup a CU, one wave a SIMD: its registers hold the next two steps'
+// keys and values in flight (64 to 128 KB a CU), which is what the memory's
+// latency asks for; with more waves the older ones of a SIMD are served first
+// and the younger ones finish alone (measured: two workgroups a CU 139 us
+// against 131 on 128 requests of 64 to 8192 tokens, 137 against 96 on equal
+// lengths of 1024).
+//
+// Scores are formed transposed, S^T = K Q^T, and so is the product, O^T =
+// V^T P^T: then the accumulators of the first product (a lane: one query,
+// tokens 4 g + i of the two 16-token halves, g = lane / 16) are in place as
+// the second's operand, whose eight products per lane may be taken in any
+// order of tokens as long as the values come in the same order.  A lane loads
+// its eight tokens' values at D / 16 neighbouring places, whole cache lines
+// per token, and exchanges rows for columns within its own registers.  No
+// key, value or score passes through LDS.
 #include "common.hpp"
 #include "internal.hpp"
 
 namespace dspark {
 namespace {
 
-constexpr int kUnit = 128;       // tokens of a unit: 4 waves of 32
+constexpr int kStep = 32;        // tokens of a step
+constexpr int kWaves = kAttendThreads / 64;
 
 __device__ __forceinline__ f32x4_t mfma(const uint4 a, const uint4 b, const f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
@@ -47,107 +57,98 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
+__device__ __forceinline__ uint4 load16(const unsigned char* p) {
+  typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
+  const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+  return make_uint4(v[0], v[1], v[2], v[3]);
+}
+
+// The bits of the infinite and NaN ones among the two bf16 or four e4m3
+// values of a word.
+__device__ __forceinline__ uint32_t odd_bf16(uint32_t x) {
+  return ((x & 0x7F80u) == 0x7F80u ? 0x0000FFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
+}
+__device__ __forceinline__ uint32_t odd_e4m3(uint32_t x) {
+  return ((((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+}
+
 // Two e4m3 values (the low or high half of w) as bf16: exact.
 template <bool HI>
 __device__ __forceinline__ uint32_t widen(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
 }
 
+typedef const __attribute__((address_space(4))) int32_t* uniform_ptr;   // scalar loads
+
 // The rows of request b: none where a length, row or count is out of range.
 struct Rows {
-  int n, len, row0;
+  int n, len, row0, bad;
 };
 
-__device__ __forceinline__ Rows request_rows(const AttendArgs& a, int b, bool report) {
+template <typename P>
+__device__ __forceinline__ Rows request_rows(const AttendArgs& a, P K, P len, P offs, int b) {
   Rows r;
-  int k = a.K ? a.K[b] : a.gamma;
-  r.len = a.len[b];
-  r.row0 = a.offs ? a.offs[b] : b * (a.gamma + 1);
-  int bad = 0;
+  int k = a.K ? K[b] : a.gamma;
+  r.len = len[b];
+  r.row0 = a.offs ? offs[b] : b * (a.gamma + 1);
+  r.bad = 0;
   if (k < -1 || k > a.gamma) {
-    bad = kErrK;
+    r.bad = kErrK;
     k = k < -1 ? -1 : a.gamma;
   }
   r.n = k + 1;
   if (r.n > 0 && (r.len < 0 || (int64_t)r.len + r.n > (int64_t)a.cols << a.page_shift)) {
-    bad |= kErrCache;
+    r.bad |= kErrCache;
     r.n = 0;
   }
   if (r.n > 0 && (r.row0 < 0 || (int64_t)r.row0 + r.n > a.n_rows)) {
-    bad |= kErrRow;
+    r.bad |= kErrRow;
     r.n = 0;
   }
-  if (bad && report) atomicOr(a.err, bad);
   return r;
 }
 
-template <int D, int MT, int E4M3>
-struct Tile {
-  static constexpr int kRows = 16 * MT;
-  static constexpr int KS = D / 32;                      // products of 32 values per score
-  static constexpr int DT = D / 16;                      // 16-wide blocks of a value row
-  static constexpr int KW = E4M3 ? KS / 2 : KS;          // 16-byte loads of a key per lane
-  static constexpr int VW = DT * (E4M3 ? 1 : 2) / 4;     // words of a value per lane
-  static constexpr int kSize = E4M3 ? 1 : 2;
-
+// Keys and values of a step as a lane has them loaded.
+template <int D, int E4M3>
+struct Loaded {
+  static constexpr int KW = E4M3 ? D / 64 : D / 32;      // 16-byte loads of a key per lane
+  static constexpr int VW = D / 16 * (E4M3 ? 1 : 2) / 4; // words of a value per lane
   uint4 k[2][KW];
   uint32_t v[8][VW];
-  uint4 q[MT][KS];
-  f32x4_t o[MT][DT];
-  float m[MT], l[MT];
-  int lim[MT];                                           // last token a query sees
-  int kid[2], vid[2];                                    // page ids of the next tile's tokens
 
-  // Page ids of the tile of 32 tokens at `base`, tokens past `last` taken as
-  // `last` (they are masked): the lane's two key tokens and two runs of four
-  // value tokens, which a page of 8 or more holds whole.
-  __device__ __forceinline__ void load_ids(const AttendArgs& a, const int32_t* table, int base, int last, int lane) {
+  // A lane's keys: token lane % 16 of either half, `kl` its place in a group.
+  __device__ __forceinline__ void load_k(const unsigned char* kc, const int64_t (&at)[4], unsigned kl, int lane) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      kid[s] = table[min(base + 16 * s + (lane & 15), last) >> a.page_shift];
-      vid[s] = table[min(base + 16 * s + 4 * (lane >> 4), last) >> a.page_shift];
+      const int64_t lo = at[2 * s], hi = at[2 * s + 1];
+      const unsigned char* p = kc + (lane & 8 ? hi : lo) + kl;
+#pragma unroll
+      for (int w = 0; w < KW; ++w) k[s][w] = load16(p + 64 * w);
     }
   }
 
-  __device__ __forceinline__ int64_t page_base(const AttendArgs& a, int id) {
-    if ((unsigned)id >= (unsigned)a.n_pages) {
-      atomicOr(a.err, kErrPage);
-      id = 0;
-    }
-    return (int64_t)id * a.c_page;
-  }
-
-  __device__ __forceinline__ void load_k(const AttendArgs& a, const unsigned char* kc, int base, int last, int lane) {
-    const int in_page = (1 << a.page_shift) - 1;
+  // A lane's values: tokens 4 g + i of either half, `vl` the first one's place in its group.
+  __device__ __forceinline__ void load_v(const unsigned char* vc, const int64_t (&at)[4], unsigned vl, int64_t c_tok,
+                                         int lane) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int t = min(base + 16 * s + (lane & 15), last);
-      const unsigned char* p = kc + page_base(a, kid[s]) + (int64_t)(t & in_page) * a.c_tok + 16 * (lane >> 4);
-#pragma unroll
-      for (int w = 0; w < KW; ++w) k[s][w] = *reinterpret_cast<const uint4*>(p + 64 * w);
-    }
-  }
-
-  __device__ __forceinline__ void load_v(const AttendArgs& a, const unsigned char* vc, int base, int last, int lane) {
-    const int in_page = (1 << a.page_shift) - 1;
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const unsigned char* p = vc + page_base(a, vid[s]) + 4 * VW * (lane & 15);
+      const int64_t lo = at[2 * s], hi = at[2 * s + 1];
+      const unsigned char* p = vc + (lane & 32 ? hi : lo) + vl;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int t = min(base + 16 * s + 4 * (lane >> 4) + i, last);
-        const unsigned char* pt = p + (int64_t)(t & in_page) * a.c_tok;
+        const unsigned char* pt = p + i * c_tok;
         uint32_t(&w)[VW] = v[4 * s + i];
         if constexpr (VW == 1) {
-          w[0] = *reinterpret_cast<const uint32_t*>(pt);
+          w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(pt));
         } else if constexpr (VW == 2) {
-          const uint2 x = *reinterpret_cast<const uint2*>(pt);
-          w[0] = x.x;
-          w[1] = x.y;
+          typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
+          const u32x2_t x = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pt));
+          w[0] = x[0];
+          w[1] = x[1];
         } else {
 #pragma unroll
           for (int c = 0; c < VW / 4; ++c) {
-            const uint4 x = reinterpret_cast<const uint4*>(pt)[c];
+            const uint4 x = load16(pt + 16 * c);
             w[4 * c] = x.x;
             w[4 * c + 1] = x.y;
             w[4 * c + 2] = x.z;
@@ -159,7 +160,7 @@ struct Tile {
   }
 
   // The key operand of product ks: 16 tokens (a lane: its token's values 32 ks
-  // + 8 g ..; e4m3: 64 (ks / 2) + 16 g + 8 (ks % 2) .., the order of q below).
+  // + 8 g ..; e4m3: 64 (ks / 2) + 16 g + 8 (ks % 2) .., the order of the queries too).
   __device__ __forceinline__ uint4 key(int s, int ks) const {
     if constexpr (!E4M3) return k[s][ks];
     const uint4 w = k[s][ks >> 1];
@@ -167,19 +168,19 @@ struct Tile {
     return make_uint4(widen<false>(lo), widen<true>(lo), widen<false>(hi), widen<true>(hi));
   }
 
-  // The value operands of blocks dt and dt + 1: rows d = DT r + dt of V^T (r =
-  // lane % 16), the lane's eight tokens in pairs.
+  // The value operands of blocks dt and dt + 1: rows d = D / 16 r + dt of V^T
+  // (r = lane % 16), the lane's eight tokens in pairs.
   __device__ __forceinline__ void values(int dt, uint4 (&f)[2]) const {
     uint32_t x[2][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (!E4M3) {
-        const uint32_t e = v[2 * j][dt / 2], o2 = v[2 * j + 1][dt / 2];
-        x[0][j] = __builtin_amdgcn_perm(o2, e, 0x05040100u);
-        x[1][j] = __builtin_amdgcn_perm(o2, e, 0x07060302u);
+        const uint32_t e = v[2 * j][dt / 2], o = v[2 * j + 1][dt / 2];
+        x[0][j] = __builtin_amdgcn_perm(o, e, 0x05040100u);
+        x[1][j] = __builtin_amdgcn_perm(o, e, 0x07060302u);
       } else {
-        const uint32_t e = v[2 * j][dt / 4], o2 = v[2 * j + 1][dt / 4];
-        const uint32_t w = __builtin_amdgcn_perm(o2, e, dt & 2 ? 0x07030602u : 0x05010400u);
+        const uint32_t e = v[2 * j][dt / 4], o = v[2 * j + 1][dt / 4];
+        const uint32_t w = __builtin_amdgcn_perm(o, e, dt & 2 ? 0x07030602u : 0x05010400u);
         x[0][j] = widen<false>(w);
         x[1][j] = widen<true>(w);
       }
@@ -188,61 +189,61 @@ struct Tile {
     f[1] = make_uint4(x[1][0], x[1][1], x[1][2], x[1][3]);
   }
 
-  // The bits of the infinite and NaN ones among the two bf16 or four e4m3
-  // values of a word.
-  static __device__ __forceinline__ uint32_t odd_bf16(uint32_t x) {
-    return ((x & 0x7F80u) == 0x7F80u ? 0x0000FFFFu : 0u) | ((x & 0x7F800000u) == 0x7F800000u ? 0xFFFF0000u : 0u);
-  }
-  static __device__ __forceinline__ uint32_t odd_e4m3(uint32_t x) {
-    return ((((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
-  }
-
-  __device__ __forceinline__ bool odd_values() const {
-    uint32_t any = 0;
+  // Takes infinite and NaN values out; whether there were any.
+  __device__ __forceinline__ uint32_t take_odd() {
+    uint32_t odd = 0;
 #pragma unroll
     for (int t = 0; t < 8; ++t)
 #pragma unroll
-      for (int w = 0; w < VW; ++w) any |= E4M3 ? odd_e4m3(v[t][w]) : odd_bf16(v[t][w]);
-    return any != 0;
-  }
-
-  __device__ __forceinline__ void add_odd_values(int base, int lane, const uint4 (&p)[MT]) {
-    const int g = lane >> 4;
-#pragma unroll
-    for (int dt = 0; dt < DT; dt += 2) {
-      uint4 f[2];
-      values(dt, f);
-#pragma unroll
-      for (int c = 0; c < 2; ++c)
-        f[c] = make_uint4(f[c].x & odd_bf16(f[c].x), f[c].y & odd_bf16(f[c].y), f[c].z & odd_bf16(f[c].z),
-                          f[c].w & odd_bf16(f[c].w));
-#pragma unroll 1
-      for (int t = 0; t < 32; ++t) {
-        const int e = (t & 3) + (t >> 4) * 4, gt = (t >> 2) & 3;
-        uint32_t keep[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) keep[j] = g == gt && e >> 1 == j ? (e & 1 ? 0xFFFF0000u : 0x0000FFFFu) : 0u;
-#pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint4 vf = make_uint4(f[c].x & keep[0], f[c].y & keep[1], f[c].z & keep[2], f[c].w & keep[3]);
-#pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            const uint4 pf = make_uint4(p[mt].x & keep[0], p[mt].y & keep[1], p[mt].z & keep[2], p[mt].w & keep[3]);
-            const f32x4_t x = mfma(vf, pf, f32x4_t{0.f, 0.f, 0.f, 0.f});
-            const bool seen = base + t <= lim[mt];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) o[mt][dt + c][i] += seen ? x[i] : 0.0f;
-          }
-        }
+      for (int w = 0; w < VW; ++w) {
+        const uint32_t x = E4M3 ? odd_e4m3(v[t][w]) : odd_bf16(v[t][w]);
+        odd |= x;
+        v[t][w] &= ~x;
       }
-    }
-#pragma unroll
-    for (int t = 0; t < 8; ++t)
-#pragma unroll
-      for (int w = 0; w < VW; ++w) v[t][w] &= ~(E4M3 ? odd_e4m3(v[t][w]) : odd_bf16(v[t][w]));
+    return odd;
   }
+};
 
-  __device__ __forceinline__ void start(const AttendArgs& a, const Rows& r, int h, int rt, int lane) {
+// Where the four groups of eight tokens of a step begin in a cache.  A page
+// holds whole groups; one behind the last token is taken as the last group,
+// and places of a group behind the last token are read and masked.  Page ids
+// are uniform: scalar loads, whose wait is none of the key and value loads'.
+struct Groups {
+  int id[4];
+  __device__ __forceinline__ static int first(int base, int j, int last) { return min(base + 8 * j, last & ~7); }
+  __device__ __forceinline__ void load(const AttendArgs& a, const int32_t* table, int base, int last) {
+    const uniform_ptr t = (uniform_ptr)(uintptr_t)table;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) id[j] = t[first(base, j, last) >> a.page_shift];
+  }
+  // Bytes from the cache's beginning, for the step at `base` whose ids are loaded.
+  __device__ __forceinline__ void place(const AttendArgs& a, int base, int last, int64_t (&at)[4]) const {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      int p = id[j];
+      if ((unsigned)p >= (unsigned)a.n_pages) {
+        atomicOr(a.err, kErrPage);
+        p = 0;
+      }
+      at[j] = (int64_t)p * a.c_page + (int64_t)(first(base, j, last) & ((1 << a.page_shift) - 1)) * a.c_tok;
+    }
+  }
+};
+
+template <int D, int MT, int E4M3>
+struct Tile {
+  using In = Loaded<D, E4M3>;
+  static constexpr int kRows = 16 * MT;
+  static constexpr int KS = D / 32;                      // products of 32 values per score
+  static constexpr int DT = D / 16;                      // 16-wide blocks of a value row
+
+  uint4 q[MT][KS];
+  f32x4_t o[MT][DT];
+  float m[MT], l[MT];
+  int lim[MT];                                           // last token a query sees
+  uint32_t odd;                                          // infinite or NaN values were taken out
+
+  __device__ __forceinline__ void load_q(const AttendArgs& a, const Rows& r, int h, int rt, int lane) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       const int row = rt * kRows + mt * 16 + (lane & 15);
@@ -255,6 +256,13 @@ struct Tile {
         q[mt][ks] = ok ? *reinterpret_cast<const uint4*>(p + d) : make_uint4(0, 0, 0, 0);
       }
       lim[mt] = a.causal ? r.len + i : r.len + r.n - 1;
+    }
+  }
+
+  __device__ __forceinline__ void reset() {
+    odd = 0;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
       m[mt] = -INFINITY;
       l[mt] = 0.0f;
 #pragma unroll
@@ -262,18 +270,18 @@ struct Tile {
     }
   }
 
-  // Scores, p and sums of the tile at `base`; `tail`: some query may not see
-  // some token of it.  `next` loads the following tile's keys once this one's
-  // are used, and then its values.
+  // Scores, p and sums of the 32 tokens at `base`, in `in`; `tail`: some query
+  // may not see some of them.  next_k and next_v load a later step's keys and
+  // values into it once these are used.
   template <typename NextK, typename NextV>
-  __device__ __forceinline__ void step(int base, bool tail, float sc, int lane, NextK next_k, NextV next_v) {
+  __device__ __forceinline__ void step(In& in, int base, bool tail, float sc, int lane, NextK next_k, NextV next_v) {
     const int g = lane >> 4;
     f32x4_t s[MT][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const uint4 kf = key(h, ks);
+        const uint4 kf = in.key(h, ks);
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
           s[mt][h] = mfma(kf, q[mt][ks], ks == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : s[mt][h]);
@@ -320,18 +328,18 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[4 * h + i] = fast_exp2(__builtin_fmaf(s[mt][h][i], sc, -ref));
       l[mt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-      // p as bf16 for the second product: half a unit of 2^-8 of each term, of
-      // either sign, below the rounding of the bf16 result
+      // p as bf16 for the second product: at most 2^-8 of each term, of either
+      // sign, about what the bf16 result is rounded by itself
       p[mt] = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
     }
     // a token that a query does not see must not reach it, but 0 times
-    // infinity or NaN is NaN: such values are taken out of the tile and added
-    // one token at a time where they are seen
-    if (tail && __any(odd_values())) add_odd_values(base, lane, p);
+    // infinity or NaN is NaN: such values are left out here and added to the
+    // results that see them at the end
+    if (tail) odd |= in.take_odd();
 #pragma unroll
     for (int dt = 0; dt < DT; dt += 2) {
       uint4 f[2];
-      values(dt, f);
+      in.values(dt, f);
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
@@ -341,31 +349,41 @@ struct Tile {
   }
 };
 
-// Workgroups of a variant that a CU is to hold (its registers are allotted
-// for them).
-template <int D, int MT>
-constexpr int kPerCu = D * MT <= 128 ? 3 : D * MT <= 256 && D < 256 ? 2 : 1;
+// Steps loaded ahead: two, or one where two and the sums pass the registers.
+template <int D, int MT, int E4M3>
+constexpr int kAhead = D * MT >= 512 && !E4M3 ? 1 : 2;
 
 template <int D, int MT, int E4M3>
-__global__ __launch_bounds__(kAttendThreads, (kPerCu<D, MT>)) void attend_impl(const AttendArgs a) {
+__global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArgs a) {
   using T = Tile<D, MT, E4M3>;
+  using In = Loaded<D, E4M3>;
   constexpr int kRows = T::kRows, DT = T::DT;
-  __shared__ float4 red[4][DT][64];
-  __shared__ float wm[4][kRows], wl[4][kRows];
-  __shared__ int64_t sums[kAttendThreads / 64];
-  __shared__ int start_b;
-  __shared__ int64_t start_off;
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  __shared__ int64_t sums[kWaves];
+  __shared__ Rows start_rows[kWaves];
+  __shared__ int start_b[kWaves], start_off[kWaves];
+  __shared__ f32x4_t share_o[kWaves - 1][MT * DT][64];    // what waves 1 .. 3 begin with of a tile
+  __shared__ float2 share_ml[kWaves - 1][kRows];
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // a lane's place in a group of eight tokens: its key's and its first value's
+  const unsigned kl = (unsigned)(lane & 7) * (unsigned)a.c_tok + 16 * (lane >> 4);
+  const unsigned vl = 4 * (lane >> 4 & 1) * (unsigned)a.c_tok + 4 * In::VW * (lane & 15);
 
-  // units of every request, and where this workgroup's stretch begins
+  // the line: what every request adds to it, and where the four stretches of
+  // this workgroup's waves begin
   const int per = (a.B + kAttendThreads - 1) / kAttendThreads;
   const int b0 = min(a.B, tid * per), b1 = min(a.B, b0 + per);
-  auto units = [&](const Rows& r) -> int {
-    if (r.n <= 0) return 0;
-    return a.Hkv * ((a.group * r.n + kRows - 1) / kRows) * ((r.len + r.n + kUnit - 1) / kUnit);
+  auto row_tiles = [&](const Rows& r) { return (a.group * r.n + kRows - 1) / kRows; };
+  auto steps = [&](const Rows& r) { return (r.len + r.n + kStep - 1) / kStep; };
+  auto length = [&](const Rows& r) -> int64_t {
+    return r.n <= 0 ? 0 : (int64_t)a.Hkv * row_tiles(r) * (steps(r) + a.tile_cost);
   };
   int64_t mine = 0;
-  for (int b = b0; b < b1; ++b) mine += units(request_rows(a, b, blockIdx.x == 0));
+  Rows r{0, 0, 0, 0};
+  for (int b = b0; b < b1; ++b) {
+    r = request_rows(a, a.K, a.len, a.offs, b);
+    if (r.bad && blockIdx.x == 0) atomicOr(a.err, r.bad);
+    mine += length(r);
+  }
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 64; o <<= 1) {
@@ -376,229 +394,288 @@ __global__ __launch_bounds__(kAttendThreads, (kPerCu<D, MT>)) void attend_impl(c
   __syncthreads();
   int64_t total = 0, before = incl - mine;
 #pragma unroll
-  for (int w = 0; w < kAttendThreads / 64; ++w) {
+  for (int w = 0; w < kWaves; ++w) {
     if (w < wave) before += sums[w];
     total += sums[w];
   }
-  int64_t chunk = (total + gridDim.x - 1) / gridDim.x;
-  if (chunk < a.min_units) chunk = a.min_units;
-  const int64_t u0 = blockIdx.x * chunk;
-  const int64_t u1 = u0 + chunk < total ? u0 + chunk : total;
-  if (u0 >= total) {
-    if (tid == 0) {
-      AttendPiece d;
-      d.t0 = 0;
-      a.pieces[blockIdx.x] = d;
-    }
+  const int64_t workers = (int64_t)gridDim.x * kWaves;
+  const int64_t chunk = max((int64_t)a.tile_cost + a.min_steps, (total + workers - 1) / workers);
+  const int64_t group_chunk = kWaves * chunk, group_u0 = blockIdx.x * group_chunk;
+  if (group_u0 >= total) {
+    if (tid == 0) a.joins[blockIdx.x].n = 0;
     return;
   }
-  if (u0 >= before && u0 < before + mine) {
+  for (int w = 0; w < kWaves; ++w) {
+    const int64_t u0 = group_u0 + w * chunk;
+    if (u0 < before || u0 >= before + mine) continue;
     int64_t base = before;
-    for (int b = b0; b < b1; ++b) {
-      const int n = units(request_rows(a, b, false));
-      if (u0 < base + n) {
-        start_b = b;
-        start_off = u0 - base;
-        break;
+    int b = b0;
+    if (per > 1)                                         // else r is the request still
+      for (;; ++b) {
+        r = request_rows(a, a.K, a.len, a.offs, b);
+        const int64_t n = length(r);
+        if (u0 < base + n) break;
+        base += n;
       }
-      base += n;
+    start_b[w] = b;
+    start_off[w] = (int)(u0 - base);
+    start_rows[w] = r;
+  }
+  __syncthreads();
+  auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
+  const int64_t u0 = group_u0 + wave * chunk, u1 = min(total, u0 + chunk);
+  const uniform_ptr uK = (uniform_ptr)(uintptr_t)a.K, ulen = (uniform_ptr)(uintptr_t)a.len,
+                    uoffs = (uniform_ptr)(uintptr_t)a.offs;
+  T t;
+  // the tile at hand: rows, head, row tile, steps, and where they begin in the line
+  Rows now{0, 0, 0, 0};
+  int h = 0, rt = 0, n_s = 0;
+  int64_t real0 = 0;
+
+  // A lane: query lane % 16 of each block, values DT (4 g + i) + dt.
+  auto write = [&]() {
+    const float vs = E4M3 && a.v_scale ? a.v_scale[h] : 1.0f;
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      const int grow = rt * kRows + mt * 16 + (lane & 15);
+      if (grow >= a.group * now.n) continue;
+      const int i = grow / a.group, hh = grow - i * a.group;
+      const float inv = vs / t.l[mt];
+      uint16_t* op = a.out + (int64_t)(now.row0 + i) * a.o_row + (int64_t)(h * a.group + hh) * a.o_head +
+                     4 * DT * (lane >> 4);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        uint32_t w[DT / 2];
+#pragma unroll
+        for (int c = 0; c < DT / 2; ++c) w[c] = pack_bf16(t.o[mt][2 * c][j] * inv, t.o[mt][2 * c + 1][j] * inv);
+        if constexpr (DT == 4) {
+          reinterpret_cast<uint2*>(op)[j] = make_uint2(w[0], w[1]);
+        } else {
+#pragma unroll
+          for (int c = 0; c < DT / 8; ++c)
+            reinterpret_cast<uint4*>(op + j * DT)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
+        }
+      }
+      if (a.lse && lane < 16)
+        a.lse[(int64_t)(now.row0 + i) * a.Hq + h * a.group + hh] = (t.m[mt] + fast_log2(t.l[mt])) * kLn2;
+    }
+  };
+  // A workgroup leaves at most two pieces in memory: what it begins with and what it ends with.
+  auto leave = [&]() {
+    float* part = a.part + (int64_t)(2 * blockIdx.x + (group_u0 < real0 - a.tile_cost ? 1 : 0)) * (kRows * (D + 2));
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      if (lane < 16) *reinterpret_cast<float2*>(part + 2 * (mt * 16 + lane)) = make_float2(t.m[mt], t.l[mt]);
+      f32x4_t* pp = reinterpret_cast<f32x4_t*>(part + 2 * kRows) + mt * DT * 64 + lane;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) pp[dt * 64] = t.o[mt][dt];
+    }
+  };
+
+  bool owner = false;                                    // the tile at hand goes on in the next wave
+  if (u0 < total) {
+    int b = uniform(start_b[wave]);
+    r = Rows{uniform(start_rows[wave].n), uniform(start_rows[wave].len), uniform(start_rows[wave].row0), 0};
+    int off = uniform(start_off[wave]);                  // place in request b's part of the line (below 2^31)
+    for (int64_t u = u0; u < u1;) {
+      while (r.n <= 0) r = request_rows(a, uK, ulen, uoffs, ++b);   // u < u1 <= total: one follows
+      now = r;
+      n_s = steps(r);
+      const int L = r.len + r.n, n_rt = row_tiles(r), size = n_s + a.tile_cost;
+      const int seg = off / size, x0 = off - seg * size;
+      const int x1 = (int)min((int64_t)size, x0 + (u1 - u));
+      h = seg / n_rt;
+      rt = seg - h * n_rt;
+      const int s0 = max(0, x0 - a.tile_cost), s1 = x1 - a.tile_cost;   // this wave's steps of the tile
+      real0 = u - x0 + a.tile_cost;
+      const int32_t* table = a.table + b * a.tstride;
+      if (u == group_u0 && lane == 0) {
+        // of the workgroups whose stretches begin within a tile's steps the
+        // first has it joined: its predecessor's piece, its own ..
+        AttendJoin j{0, 0, 0, 0, 0, 0};
+        if (s0 > 0 && group_u0 - group_chunk <= real0) {
+          j.row0 = now.row0;
+          j.rows = a.group * now.n - rt * kRows;
+          j.h = h;
+          j.rt = rt;
+          j.n = (int)((real0 + n_s - 1) / group_chunk) - (int)blockIdx.x + 2;
+          j.slot = 2 * ((int)blockIdx.x - 1) + (group_u0 - group_chunk < real0 - a.tile_cost ? 1 : 0);
+        }
+        a.joins[blockIdx.x] = j;
+      }
+      u += x1 - x0;
+      off += x1 - x0;
+      if (off == a.Hkv * n_rt * size) {
+        off = 0;
+        ++b;
+        if (u < u1) r = request_rows(a, uK, ulen, uoffs, b);
+      }
+      if (s1 <= 0) continue;                             // none of the tile's steps falls to this stretch
+
+      t.load_q(a, now, h, rt, lane);
+      t.reset();
+      const float sc = a.scale2 * (E4M3 && a.k_scale ? a.k_scale[h] : 1.0f);
+      const unsigned char *kc = a.kc + (int64_t)h * a.c_head, *vc = a.vc + (int64_t)h * a.c_head;
+      const int full = a.causal ? now.len : L - 1;       // tokens up to `full` are seen by every row
+      const int end = min(s1 * kStep, L), last = end - 1;
+      // steps behind the last one are the last tokens once more: loads without a branch
+      constexpr int N = kAhead<D, MT, E4M3>;
+      In in[N];
+      Groups ids;
+      int64_t at[4];
+      int base = s0 * kStep;
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        ids.load(a, table, base + i * kStep, last);
+        ids.place(a, base + i * kStep, last, at);
+        in[i].load_k(kc, at, kl, lane);
+        in[i].load_v(vc, at, vl, a.c_tok, lane);
+      }
+      ids.load(a, table, base + N * kStep, last);
+      for (;;) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          t.step(
+              in[i], base, base + kStep - 1 > full, sc, lane,
+              [&]() {
+                ids.place(a, base + N * kStep, last, at);
+                ids.load(a, table, base + (N + 1) * kStep, last);
+                in[i].load_k(kc, at, kl, lane);
+              },
+              [&]() { in[i].load_v(vc, at, vl, a.c_tok, lane); });
+          base += kStep;
+          if (base >= end) goto done;
+        }
+      }
+    done:
+      if (__any(t.odd != 0)) {
+        // the values left out above, to the rows that see them: only steps that
+        // reach past `full` leave any out
+        for (int tk = max(s0 * kStep, (full + 1) & ~(kStep - 1)); tk < end; ++tk) {
+          const int id = table[tk >> a.page_shift];
+          const unsigned char* p = vc + (int64_t)((unsigned)id < (unsigned)a.n_pages ? id : 0) * a.c_page +
+                                   (int64_t)(tk & ((1 << a.page_shift) - 1)) * a.c_tok;
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int dt = 0; dt < DT; ++dt) {
+              const int d = DT * (4 * (lane >> 4) + i) + dt;
+              const uint32_t x = E4M3 ? widen<false>(p[d]) & 0xFFFFu : reinterpret_cast<const uint16_t*>(p)[d];
+              const float y = (x & 0x7F80u) == 0x7F80u ? __uint_as_float(x << 16) : 0.0f;
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+                if (tk <= t.lim[mt]) t.o[mt][dt][i] += y;
+            }
+        }
+      }
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        t.l[mt] += shfl_xor(t.l[mt], 16);
+        t.l[mt] += shfl_xor(t.l[mt], 32);
+      }
+      owner = s1 < n_s;                                  // the stretch ends within the tile
+      if (s0 > 0 && wave > 0) {
+        // begun by an earlier wave of this workgroup, which joins it
+        owner = false;
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          if (lane < 16) share_ml[wave - 1][mt * 16 + lane] = make_float2(t.m[mt], t.l[mt]);
+#pragma unroll
+          for (int dt = 0; dt < DT; ++dt) share_o[wave - 1][mt * DT + dt][lane] = t.o[mt][dt];
+        }
+      } else if (!owner) {
+        if (s0 == 0) write();
+        else leave();
+      }
     }
   }
   __syncthreads();
-  int b = start_b, off = (int)start_off;
-  int slot = 0;
-  bool first = true;
-  for (int64_t u = u0; u < u1;) {
-    Rows r = request_rows(a, b, false);
-    while (r.n <= 0) r = request_rows(a, ++b, false);    // u < u1 <= total: one follows
-    const int L = r.len + r.n;
-    const int n_rt = (a.group * r.n + kRows - 1) / kRows, n_t = (L + kUnit - 1) / kUnit;
-    const int seg = off / n_t, t0 = off - seg * n_t;
-    const int t1 = (int)(u1 - u < n_t - t0 ? t0 + (u1 - u) : n_t);
-    const int h = seg / n_rt, rt = seg - h * n_rt;
-    const bool whole = t0 == 0 && t1 == n_t;
-    if (first && tid == 0) {
-      AttendPiece d;
-      d.b = b;
-      d.h = h;
-      d.rt = rt;
-      d.n_t = n_t;
-      d.t0 = t0;
-      d.unit0 = u - t0;
-      d.chunk = chunk;
-      a.pieces[blockIdx.x] = d;
-    }
-
-    // this wave's tiles of 32 tokens: every fourth
-    T t;
-    t.start(a, r, h, rt, lane);
-    const float sc = a.scale2 * (E4M3 && a.k_scale ? a.k_scale[h] : 1.0f);
-    const int32_t* table = a.table + b * a.tstride;
-    const unsigned char* kc = a.kc + (int64_t)h * a.c_head;
-    const unsigned char* vc = a.vc + (int64_t)h * a.c_head;
-    const int full = a.causal ? r.len : L - 1;           // tokens up to `full` are seen by every row
-    int base = (t0 * 4 + wave) * 32;
-    const int end = min(t1 * kUnit, L), last = end - 1;
-    if (base < end) {
-      t.load_ids(a, table, base, last, lane);
-      t.load_k(a, kc, base, last, lane);
-      t.load_v(a, vc, base, last, lane);
-      t.load_ids(a, table, base + kUnit, last, lane);
-      // the tile after the last one is token `last` over and over: loads
-      // without a branch, of one cache line a lane group
-      for (; base < end; base += kUnit)
-        t.step(
-            base, base + 31 > full, sc, lane, [&]() { t.load_k(a, kc, base + kUnit, last, lane); },
-            [&]() {
-              t.load_v(a, vc, base + kUnit, last, lane);
-              t.load_ids(a, table, base + 2 * kUnit, last, lane);
-            });
-    }
-
-    // the four waves' sums, 16 queries at a time
-    __syncthreads();
+  if (!owner) return;
+  // the pieces of the waves after this one that the tile reaches
+  const int64_t last_u = real0 + n_s - 1;
+  const int to = (int)min((int64_t)kWaves - 1, (last_u - group_u0) / chunk);
+  for (int w = wave + 1; w <= to; ++w) {
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      float l = t.l[mt];
-      l += shfl_xor(l, 16);
-      l += shfl_xor(l, 32);
-      if (lane < 16) {
-        wm[wave][mt * 16 + lane] = t.m[mt];
-        wl[wave][mt * 16 + lane] = l;
-      }
-    }
-    const float vs = E4M3 && a.v_scale ? a.v_scale[h] : 1.0f;
-    float* part = a.part + ((int64_t)blockIdx.x * 2 + slot) * (kRows * (D + 2));
-    // thread: query tid / 16, values DT (tid % 16) ..
-    const int qi = tid >> 4, rr = tid & 15;
+      const float2 ml = share_ml[w - 1][mt * 16 + (lane & 15)];
+      const float mn = fmaxf(t.m[mt], ml.x);
+      const float f = t.m[mt] == -INFINITY ? 0.0f : fast_exp2(t.m[mt] - mn);
+      const float g = ml.x == -INFINITY ? 0.0f : fast_exp2(ml.x - mn);
+      t.m[mt] = mn;
+      t.l[mt] = t.l[mt] * f + ml.y * g;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      if (mt > 0) __syncthreads();
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-        red[wave][dt][lane] = make_float4(t.o[mt][dt][0], t.o[mt][dt][1], t.o[mt][dt][2], t.o[mt][dt][3]);
-      __syncthreads();
-      const int row = mt * 16 + qi;
-      float M = wm[0][row];
-#pragma unroll
-      for (int w = 1; w < 4; ++w) M = fmaxf(M, wm[w][row]);
-      float f[4], lsum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        f[w] = wm[w][row] == -INFINITY ? 0.0f : fast_exp2(wm[w][row] - M);
-        lsum += f[w] * wl[w][row];
-      }
-      float acc[DT];
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        float x = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float* y = reinterpret_cast<const float*>(&red[w][dt][(rr >> 2) * 16 + qi]);
-          x += f[w] * y[rr & 3];
-        }
-        acc[dt] = x;
-      }
-      const int grow = rt * kRows + row;
-      if (grow < a.group * r.n) {
-        if (whole) {
-          const int i = grow / a.group, hh = grow - i * a.group;
-          const float inv = vs / lsum;
-          uint16_t* op = a.out + (int64_t)(r.row0 + i) * a.o_row + (int64_t)(h * a.group + hh) * a.o_head + DT * rr;
-          uint32_t w[DT / 2];
-#pragma unroll
-          for (int c = 0; c < DT / 2; ++c) w[c] = pack_bf16(acc[2 * c] * inv, acc[2 * c + 1] * inv);
-          if constexpr (DT == 4) {
-            *reinterpret_cast<uint2*>(op) = make_uint2(w[0], w[1]);
-          } else {
-#pragma unroll
-            for (int c = 0; c < DT / 8; ++c)
-              reinterpret_cast<uint4*>(op)[c] = make_uint4(w[4 * c], w[4 * c + 1], w[4 * c + 2], w[4 * c + 3]);
-          }
-          if (a.lse && rr == 0)
-            a.lse[(int64_t)(r.row0 + i) * a.Hq + h * a.group + hh] = (M + fast_log2(lsum)) * kLn2;
-        } else {
-          if (rr == 0) {
-            part[row] = M;
-            part[kRows + row] = lsum;
-          }
-          float4* pp = reinterpret_cast<float4*>(part + 2 * kRows + row * D + DT * rr);
-#pragma unroll
-          for (int c = 0; c < DT / 4; ++c)
-            pp[c] = make_float4(acc[4 * c], acc[4 * c + 1], acc[4 * c + 2], acc[4 * c + 3]);
-        }
-      }
-    }
-    __syncthreads();
-    u += t1 - t0;
-    off += t1 - t0;
-    slot = 1;
-    first = false;
-    if (off == a.Hkv * n_rt * n_t) {
-      ++b;
-      off = 0;
+      for (int dt = 0; dt < DT; ++dt) t.o[mt][dt] = t.o[mt][dt] * f + share_o[w - 1][mt * DT + dt][lane] * g;
     }
   }
+  if (real0 >= group_u0 && last_u < group_u0 + group_chunk) write();
+  else leave();
 }
 
-// Joins the pieces of one tile: those of workgroups w - 1, w, .. where w is
-// the first whose stretch begins inside the tile.  A wave per row; pieces are
-// added in the order of their tokens.
+// Adds up the pieces of the tiles that several workgroups share: a workgroup for
+// 16 rows, a wave of it for a quarter of their values.
 template <int D>
 __global__ __launch_bounds__(kAttendThreads) void attend_join_impl(const AttendArgs a) {
-  const int rows = a.rows;
-  const int w = blockIdx.x + 1;
-  const AttendPiece d = a.pieces[w];
-  if (d.t0 == 0 || d.unit0 < (w - 1) * d.chunk) return;
-  const Rows r = request_rows(a, d.b, false);
-  const int lane = threadIdx.x & 63;
-  const int row = blockIdx.y * (kAttendThreads / 64) + (threadIdx.x >> 6);
-  const int grow = d.rt * rows + row;
-  if (grow >= a.group * r.n) return;
-  const int n = (int)((d.unit0 + d.n_t - 1) / d.chunk) - (w - 1) + 1;
-  const int size = rows * (D + 2);
-  // piece j: workgroup w - 1 + j; the first may be the second of its workgroup
-  const int skip = d.unit0 == (w - 1) * d.chunk ? 0 : 1;
-  auto piece = [&](int j) { return a.part + ((int64_t)(w - 1 + j) * 2 + (j == 0 ? skip : 0)) * size; };
-  float M = -INFINITY;
-  for (int j = lane; j < n; j += 64) M = fmaxf(M, piece(j)[row]);
+  constexpr int DT = D / 16, kV = DT / 4;
+  const AttendJoin d = a.joins[blockIdx.x];
+  const int lane = threadIdx.x & 63, mt = blockIdx.y, rows = a.rows;
+  if (d.n == 0 || mt * 16 >= d.rows) return;
+  const int row = mt * 16 + (lane & 15), dt0 = (threadIdx.x >> 6) * kV, size = rows * (D + 2);
+  float M = -INFINITY, L = 0.0f;
+  f32x4_t acc[kV];
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) M = fmaxf(M, shfl_xor(M, o));
-  float L = 0.0f, acc[D / 64];
+  for (int c = 0; c < kV; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+  constexpr int kPieces = 8;
+  for (int j0 = 0; j0 < d.n; j0 += kPieces) {
+    float2 ml[kPieces];
+    f32x4_t y[kPieces][kV];
 #pragma unroll
-  for (int c = 0; c < D / 64; ++c) acc[c] = 0.0f;
-  for (int j0 = 0; j0 < n; j0 += 64) {
-    float f = 0.0f;
-    if (j0 + lane < n) {
-      const float* p = piece(j0 + lane);
-      f = p[row] == -INFINITY ? 0.0f : fast_exp2(p[row] - M);
-      L += f * p[rows + row];
+    for (int j = 0; j < kPieces; ++j) {
+      // the first piece stands alone, the others at the beginnings of the stretches after it
+      const int i = min(j0 + j, d.n - 1);
+      const float* p = a.part + (int64_t)(i == 0 ? d.slot : (d.slot & ~1) + 2 * i) * size;
+      ml[j] = *reinterpret_cast<const float2*>(p + 2 * row);
+#pragma unroll
+      for (int c = 0; c < kV; ++c)
+        y[j][c] = reinterpret_cast<const f32x4_t*>(p + 2 * rows)[(mt * DT + dt0 + c) * 64 + lane];
     }
-    const int m = min(64, n - j0);
-#pragma unroll 4
-    for (int j = 0; j < m; ++j) {
-      const float fj = __shfl(f, j, 64);
-      const float* p = piece(j0 + j) + 2 * rows + row * D;
+    float mn = M;
 #pragma unroll
-      for (int c = 0; c < D / 64; ++c) {
-        const float y = p[(D / 64) * lane + c];
-        acc[c] += fj * y;
-      }
+    for (int j = 0; j < kPieces; ++j) mn = fmaxf(mn, ml[j].x);
+    if (j0 > 0) {
+      const float f = M == -INFINITY ? 0.0f : fast_exp2(M - mn);
+      L *= f;
+#pragma unroll
+      for (int c = 0; c < kV; ++c) acc[c] *= f;
+    }
+    M = mn;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const bool there = j0 + j < d.n;
+      const float f = ml[j].x == -INFINITY ? 0.0f : fast_exp2(ml[j].x - M);
+      L += there ? f * ml[j].y : 0.0f;
+#pragma unroll
+      for (int c = 0; c < kV; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[c][i] += there ? y[j][c][i] * f : 0.0f;
     }
   }
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) L += shfl_xor(L, o);
-  const int i = grow / a.group, hh = grow - i * a.group;
+  if (row >= d.rows) return;
+  const int grow = d.rt * rows + row, q = grow / a.group, hh = grow - q * a.group;
   const float inv = (a.v_scale ? a.v_scale[d.h] : 1.0f) / L;
-  uint16_t* op = a.out + (int64_t)(r.row0 + i) * a.o_row + (int64_t)(d.h * a.group + hh) * a.o_head;
-  if constexpr (D == 64) {
-    op[lane] = (uint16_t)pack_bf16(acc[0] * inv, 0.0f);
-  } else {
+  uint16_t* op = a.out + (int64_t)(d.row0 + q) * a.o_row + (int64_t)(d.h * a.group + hh) * a.o_head +
+                 4 * DT * (lane >> 4) + dt0;
 #pragma unroll
-    for (int c = 0; c < D / 128; ++c)
-      reinterpret_cast<uint32_t*>(op)[(D / 128) * lane + c] = pack_bf16(acc[2 * c] * inv, acc[2 * c + 1] * inv);
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (kV == 1) {
+      op[i * DT] = (uint16_t)pack_bf16(acc[0][i] * inv, 0.0f);
+    } else {
+#pragma unroll
+      for (int c = 0; c < kV; c += 2)
+        *reinterpret_cast<uint32_t*>(op + i * DT + c) = pack_bf16(acc[c][i] * inv, acc[c + 1][i] * inv);
+    }
   }
-  if (a.lse && lane == 0) a.lse[(int64_t)(r.row0 + i) * a.Hq + d.h * a.group + hh] = (M + fast_log2(L)) * kLn2;
+  if (a.lse && threadIdx.x < 16)
+    a.lse[(int64_t)(d.row0 + q) * a.Hq + d.h * a.group + hh] = (M + fast_log2(L)) * kLn2;
 }
 
 template <int D, int MT>

@@ -113,9 +113,8 @@ __global__ __launch_bounds__(kConstrainThreads) void constrain_impl(const Constr
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u) {
         const int i = i0 + u * kConstrainThreads;
-        if (i >= len) break;
         if (report && (unsigned)t[u] >= (unsigned)a.V) atomicOr(a.err, kErrToken);
-        if (t[u] >= v0 && t[u] < v1) {
+        if (i < len && t[u] >= v0 && t[u] < v1) {
           if (i < prompt) atomicOr(&count[t[u] - v0], kPrompt);
           else atomicAdd(&count[t[u] - v0], 1u);
         }

@@ -276,18 +276,18 @@ constexpr int kCacheThreads = 256;
 const void* cache_write_kernel(int e4m3);
 
 // Attention of packed rows over the paged cache (attend.hip).
-// What a workgroup's stretch of units begins with: the tile (request, cache
-// head, row tile), its units, the unit of the tile it begins at (0: at the
-// tile's start, or no stretch), and the tile's first unit in the batch's line.
-struct AttendPiece {
-  int b, h, rt, n_t, t0;
-  int64_t unit0, chunk;
+// A tile to be joined: its request's first row, the rows from its first one
+// on, cache head and row tile, and its n pieces, the first at `slot`; n = 0:
+// none.
+struct AttendJoin {
+  int row0, rows, h, rt, n, slot;
 };
 
 struct AttendArgs {
   int B, n_rows, gamma, Hq, Hkv, group, page_shift, n_pages, cols, causal;
   int rows;                      // rows of a tile: 16 mt
-  int min_units;                 // units per workgroup at least
+  int tile_cost;                 // what a tile costs besides its steps, in steps
+  int min_steps;                 // steps of a wave's stretch at least
   const uint16_t* q;             // bf16
   int64_t q_row, q_head;
   const unsigned char* kc;       // caches, strides in bytes
@@ -304,13 +304,14 @@ struct AttendArgs {
   uint16_t* out;                 // bf16
   int64_t o_row, o_head;
   float* lse;                    // [n_rows][Hq], nullable
-  AttendPiece* pieces;           // [grid]
-  float* part;                   // [grid][2]: m [rows], sum [rows], unscaled result [rows][d]
+  AttendJoin* joins;             // [grid]
+  float* part;                   // [grid][2]: (m, sum) [rows], unscaled result [rows][d] in lane order
   int32_t* err;
 };
 constexpr int kAttendThreads = 256;
-constexpr int kAttendMaxGrid = 2048;
-constexpr size_t kAttendPartBytes = (size_t)48 << 20;
+constexpr int kAttendMaxGrid = 512;    // workgroups: one per CU
+constexpr size_t kAttendJoinBytes = kAttendMaxGrid * sizeof(AttendJoin);
+constexpr size_t kAttendPartBytes = kAttendMaxGrid * 2 * 8320 * sizeof(float);   // 16 mt (d + 2) <= 64 * 130
 // mt: 16-row blocks of a tile (1, 2; 4 where d < 256)
 const void* attend_kernel(int d, int mt, int e4m3);
 const void* attend_join_kernel(int d);
