@@ -1915,7 +1915,7 @@ int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   a.causal = causal != 0;
   a.rows = 16 * mt;
   a.tile_cost = 1;
-  a.min_steps = 2;
+  a.min_steps = 1;
   a.q = static_cast<const uint16_t*>(q);
   a.q_row = q_stride_row;
   a.q_head = q_stride_head;

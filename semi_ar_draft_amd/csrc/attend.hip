@@ -288,6 +288,7 @@ struct Tile {
       }
     next_k();
     if (tail) {
+      asm volatile("");                                  // a branch: few steps take it
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
@@ -296,13 +297,20 @@ struct Tile {
           for (int i = 0; i < 4; ++i)
             if (base + 16 * h + 4 * g + i > lim[mt]) s[mt][h][i] = -INFINITY;
     }
+    // exponents against the maximum so far (0 where nothing was seen yet: then
+    // every p of a masked token is 2^-inf = 0 too)
     float top[MT];
     bool grows = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+      const float ref = m[mt] == -INFINITY ? 0.0f : m[mt];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[mt][h][i] = __builtin_fmaf(s[mt][h][i], sc, -ref);
       float x = fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3]));
       x = fmaxf(x, fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
-      top[mt] = x * sc;
+      top[mt] = x + ref;
       grows |= top[mt] > m[mt] + 8.0f;
     }
     if (__any(grows)) {
@@ -312,8 +320,13 @@ struct Tile {
         x = fmaxf(x, shfl_xor(x, 32));
         const float mn = fmaxf(m[mt], x);
         const float f = mn == m[mt] ? 1.0f : fast_exp2(m[mt] - mn);
+        const float up = (m[mt] == -INFINITY ? 0.0f : m[mt]) - (mn == -INFINITY ? 0.0f : mn);
         m[mt] = mn;
         l[mt] *= f;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) s[mt][h][i] += up;
 #pragma unroll
         for (int dt = 0; dt < DT; ++dt) o[mt][dt] *= f;
       }
@@ -321,12 +334,11 @@ struct Tile {
     uint4 p[MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const float ref = m[mt] == -INFINITY ? 0.0f : m[mt];   // nothing seen yet: every p is 2^-inf = 0
       float e[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[4 * h + i] = fast_exp2(__builtin_fmaf(s[mt][h][i], sc, -ref));
+        for (int i = 0; i < 4; ++i) e[4 * h + i] = fast_exp2(s[mt][h][i]);
       l[mt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       // p as bf16 for the second product: at most 2^-8 of each term, of either
       // sign, about what the bf16 result is rounded by itself
@@ -352,6 +364,15 @@ struct Tile {
 // Steps loaded ahead: two, or one where two and the sums pass the registers.
 template <int D, int MT, int E4M3>
 constexpr int kAhead = D * MT >= 512 && !E4M3 ? 1 : 2;
+
+// A wave's steps s0 .. s1 - 1 of a tile: the rows of request r at cache head h, row tile rt.
+struct Piece {
+  Rows r;
+  int h, rt, n_s, s0, s1;        // n_s: steps of the whole tile
+  int64_t real0;                 // where they begin in the line
+  const int32_t* table;          // the request's pages
+  __device__ __forceinline__ int last() const { return min(s1 * kStep, r.len + r.n) - 1; }
+};
 
 template <int D, int MT, int E4M3>
 __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArgs a) {
@@ -427,21 +448,18 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
   const uniform_ptr uK = (uniform_ptr)(uintptr_t)a.K, ulen = (uniform_ptr)(uintptr_t)a.len,
                     uoffs = (uniform_ptr)(uintptr_t)a.offs;
   T t;
-  // the tile at hand: rows, head, row tile, steps, and where they begin in the line
-  Rows now{0, 0, 0, 0};
-  int h = 0, rt = 0, n_s = 0;
-  int64_t real0 = 0;
+  Piece now;                                             // the piece at hand
 
   // A lane: query lane % 16 of each block, values DT (4 g + i) + dt.
   auto write = [&]() {
-    const float vs = E4M3 && a.v_scale ? a.v_scale[h] : 1.0f;
+    const float vs = E4M3 && a.v_scale ? a.v_scale[now.h] : 1.0f;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const int grow = rt * kRows + mt * 16 + (lane & 15);
-      if (grow >= a.group * now.n) continue;
+      const int grow = now.rt * kRows + mt * 16 + (lane & 15);
+      if (grow >= a.group * now.r.n) continue;
       const int i = grow / a.group, hh = grow - i * a.group;
       const float inv = vs / t.l[mt];
-      uint16_t* op = a.out + (int64_t)(now.row0 + i) * a.o_row + (int64_t)(h * a.group + hh) * a.o_head +
+      uint16_t* op = a.out + (int64_t)(now.r.row0 + i) * a.o_row + (int64_t)(now.h * a.group + hh) * a.o_head +
                      4 * DT * (lane >> 4);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -457,12 +475,12 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
         }
       }
       if (a.lse && lane < 16)
-        a.lse[(int64_t)(now.row0 + i) * a.Hq + h * a.group + hh] = (t.m[mt] + fast_log2(t.l[mt])) * kLn2;
+        a.lse[(int64_t)(now.r.row0 + i) * a.Hq + now.h * a.group + hh] = (t.m[mt] + fast_log2(t.l[mt])) * kLn2;
     }
   };
   // A workgroup leaves at most two pieces in memory: what it begins with and what it ends with.
   auto leave = [&]() {
-    float* part = a.part + (int64_t)(2 * blockIdx.x + (group_u0 < real0 - a.tile_cost ? 1 : 0)) * (kRows * (D + 2));
+    float* part = a.part + (int64_t)(2 * blockIdx.x + (group_u0 < now.real0 - a.tile_cost ? 1 : 0)) * (kRows * (D + 2));
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (lane < 16) *reinterpret_cast<float2*>(part + 2 * (mt * 16 + lane)) = make_float2(t.m[mt], t.l[mt]);
@@ -477,83 +495,110 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
     int b = uniform(start_b[wave]);
     r = Rows{uniform(start_rows[wave].n), uniform(start_rows[wave].len), uniform(start_rows[wave].row0), 0};
     int off = uniform(start_off[wave]);                  // place in request b's part of the line (below 2^31)
-    for (int64_t u = u0; u < u1;) {
-      while (r.n <= 0) r = request_rows(a, uK, ulen, uoffs, ++b);   // u < u1 <= total: one follows
-      now = r;
-      n_s = steps(r);
-      const int L = r.len + r.n, n_rt = row_tiles(r), size = n_s + a.tile_cost;
-      const int seg = off / size, x0 = off - seg * size;
-      const int x1 = (int)min((int64_t)size, x0 + (u1 - u));
-      h = seg / n_rt;
-      rt = seg - h * n_rt;
-      const int s0 = max(0, x0 - a.tile_cost), s1 = x1 - a.tile_cost;   // this wave's steps of the tile
-      real0 = u - x0 + a.tile_cost;
-      const int32_t* table = a.table + b * a.tstride;
-      if (u == group_u0 && lane == 0) {
-        // of the workgroups whose stretches begin within a tile's steps the
-        // first has it joined: its predecessor's piece, its own ..
-        AttendJoin j{0, 0, 0, 0, 0, 0};
-        if (s0 > 0 && group_u0 - group_chunk <= real0) {
-          j.row0 = now.row0;
-          j.rows = a.group * now.n - rt * kRows;
-          j.h = h;
-          j.rt = rt;
-          j.n = (int)((real0 + n_s - 1) / group_chunk) - (int)blockIdx.x + 2;
-          j.slot = 2 * ((int)blockIdx.x - 1) + (group_u0 - group_chunk < real0 - a.tile_cost ? 1 : 0);
+    int64_t u = u0;
+    // the stretch's next piece, if it has one
+    auto take = [&](Piece& p) {
+      while (u < u1) {
+        while (r.n <= 0) r = request_rows(a, uK, ulen, uoffs, ++b);   // u < u1 <= total: one follows
+        const int n_rt = row_tiles(r), size = steps(r) + a.tile_cost;
+        const int seg = off / size, x0 = off - seg * size;
+        const int x1 = (int)min((int64_t)size, x0 + (u1 - u));
+        p.r = r;
+        p.n_s = size - a.tile_cost;
+        p.h = seg / n_rt;
+        p.rt = seg - p.h * n_rt;
+        p.s0 = max(0, x0 - a.tile_cost);
+        p.s1 = x1 - a.tile_cost;
+        p.real0 = u - x0 + a.tile_cost;
+        p.table = a.table + b * a.tstride;
+        if (u == group_u0 && lane == 0) {
+          // of the workgroups whose stretches begin within a tile's steps the
+          // first has it joined: its predecessor's piece, its own ..
+          AttendJoin j{0, 0, 0, 0, 0, 0};
+          if (p.s0 > 0 && group_u0 - group_chunk <= p.real0) {
+            j.row0 = r.row0;
+            j.rows = a.group * r.n - p.rt * kRows;
+            j.h = p.h;
+            j.rt = p.rt;
+            j.n = (int)((p.real0 + p.n_s - 1) / group_chunk) - (int)blockIdx.x + 2;
+            j.slot = 2 * ((int)blockIdx.x - 1) + (group_u0 - group_chunk < p.real0 - a.tile_cost ? 1 : 0);
+          }
+          a.joins[blockIdx.x] = j;
         }
-        a.joins[blockIdx.x] = j;
+        u += x1 - x0;
+        off += x1 - x0;
+        if (off == a.Hkv * n_rt * size) {
+          off = 0;
+          ++b;
+          if (u < u1) r = request_rows(a, uK, ulen, uoffs, b);
+        }
+        if (p.s1 > 0) return true;                       // else none of the tile's steps falls to this stretch
       }
-      u += x1 - x0;
-      off += x1 - x0;
-      if (off == a.Hkv * n_rt * size) {
-        off = 0;
-        ++b;
-        if (u < u1) r = request_rows(a, uK, ulen, uoffs, b);
-      }
-      if (s1 <= 0) continue;                             // none of the tile's steps falls to this stretch
-
-      t.load_q(a, now, h, rt, lane);
-      t.reset();
-      const float sc = a.scale2 * (E4M3 && a.k_scale ? a.k_scale[h] : 1.0f);
-      const unsigned char *kc = a.kc + (int64_t)h * a.c_head, *vc = a.vc + (int64_t)h * a.c_head;
-      const int full = a.causal ? now.len : L - 1;       // tokens up to `full` are seen by every row
-      const int end = min(s1 * kStep, L), last = end - 1;
-      // steps behind the last one are the last tokens once more: loads without a branch
-      constexpr int N = kAhead<D, MT, E4M3>;
-      In in[N];
-      Groups ids;
-      int64_t at[4];
-      int base = s0 * kStep;
+      return false;
+    };
+    constexpr int N = kAhead<D, MT, E4M3>;
+    In in[N];
+    Groups ids[N + 1];
+    int64_t at[4];
+    // a piece's first steps: page ids, then queries, keys and values
+    auto ask = [&](const Piece& p) {
+#pragma unroll
+      for (int i = 0; i <= N; ++i) ids[i].load(a, p.table, (p.s0 + i) * kStep, p.last());
+    };
+    auto begin = [&](const Piece& p) {
+      const unsigned char *kc = a.kc + (int64_t)p.h * a.c_head, *vc = a.vc + (int64_t)p.h * a.c_head;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        ids.load(a, table, base + i * kStep, last);
-        ids.place(a, base + i * kStep, last, at);
+        ids[i].place(a, (p.s0 + i) * kStep, p.last(), at);
         in[i].load_k(kc, at, kl, lane);
+        if (i == 0) t.load_q(a, p.r, p.h, p.rt, lane);
         in[i].load_v(vc, at, vl, a.c_tok, lane);
       }
-      ids.load(a, table, base + N * kStep, last);
+    };
+    bool have = take(now);
+    if (have) {
+      ask(now);
+      begin(now);
+    }
+    while (have) {
+      Piece next = now;
+      have = take(next);
+      t.reset();
+      const int L = now.r.len + now.r.n, h = now.h;
+      const float sc = a.scale2 * (E4M3 && a.k_scale ? a.k_scale[h] : 1.0f);
+      const unsigned char *kc = a.kc + (int64_t)h * a.c_head, *vc = a.vc + (int64_t)h * a.c_head;
+      const int full = a.causal ? now.r.len : L - 1;     // tokens up to `full` are seen by every row
+      const int last = now.last();
+      Groups id = ids[N];
+      if (have) ask(next);
+      int base = now.s0 * kStep;
       for (;;) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           t.step(
               in[i], base, base + kStep - 1 > full, sc, lane,
               [&]() {
-                ids.place(a, base + N * kStep, last, at);
-                ids.load(a, table, base + (N + 1) * kStep, last);
+                // (with 64 rows the branch costs more register copies than the loads: those are
+                // the last tokens once more)
+                if (MT < 4 && base + N * kStep > last) return;
+                id.place(a, base + N * kStep, last, at);
+                id.load(a, now.table, base + (N + 1) * kStep, last);
                 in[i].load_k(kc, at, kl, lane);
               },
-              [&]() { in[i].load_v(vc, at, vl, a.c_tok, lane); });
+              [&]() {
+                if (MT == 4 || base + N * kStep <= last) in[i].load_v(vc, at, vl, a.c_tok, lane);
+              });
           base += kStep;
-          if (base >= end) goto done;
+          if (base > last) goto done;
         }
       }
     done:
       if (__any(t.odd != 0)) {
         // the values left out above, to the rows that see them: only steps that
         // reach past `full` leave any out
-        for (int tk = max(s0 * kStep, (full + 1) & ~(kStep - 1)); tk < end; ++tk) {
-          const int id = table[tk >> a.page_shift];
-          const unsigned char* p = vc + (int64_t)((unsigned)id < (unsigned)a.n_pages ? id : 0) * a.c_page +
+        for (int tk = max(now.s0 * kStep, (full + 1) & ~(kStep - 1)); tk <= last; ++tk) {
+          const int page = now.table[tk >> a.page_shift];
+          const unsigned char* p = vc + (int64_t)((unsigned)page < (unsigned)a.n_pages ? page : 0) * a.c_page +
                                    (int64_t)(tk & ((1 << a.page_shift) - 1)) * a.c_tok;
 #pragma unroll
           for (int i = 0; i < 4; ++i)
@@ -568,13 +613,14 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
             }
         }
       }
+      if (have) begin(next);                             // under way while this piece is finished
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         t.l[mt] += shfl_xor(t.l[mt], 16);
         t.l[mt] += shfl_xor(t.l[mt], 32);
       }
-      owner = s1 < n_s;                                  // the stretch ends within the tile
-      if (s0 > 0 && wave > 0) {
+      owner = now.s1 < now.n_s;                          // the stretch ends within the tile
+      if (now.s0 > 0 && wave > 0) {
         // begun by an earlier wave of this workgroup, which joins it
         owner = false;
 #pragma unroll
@@ -584,15 +630,16 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
           for (int dt = 0; dt < DT; ++dt) share_o[wave - 1][mt * DT + dt][lane] = t.o[mt][dt];
         }
       } else if (!owner) {
-        if (s0 == 0) write();
+        if (now.s0 == 0) write();
         else leave();
       }
+      if (have) now = next;
     }
   }
   __syncthreads();
   if (!owner) return;
   // the pieces of the waves after this one that the tile reaches
-  const int64_t last_u = real0 + n_s - 1;
+  const int64_t last_u = now.real0 + now.n_s - 1;
   const int to = (int)min((int64_t)kWaves - 1, (last_u - group_u0) / chunk);
   for (int w = wave + 1; w <= to; ++w) {
 #pragma unroll
@@ -607,7 +654,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
       for (int dt = 0; dt < DT; ++dt) t.o[mt][dt] = t.o[mt][dt] * f + share_o[w - 1][mt * DT + dt][lane] * g;
     }
   }
-  if (real0 >= group_u0 && last_u < group_u0 + group_chunk) write();
+  if (now.real0 >= group_u0 && last_u < group_u0 + group_chunk) write();
   else leave();
 }
 

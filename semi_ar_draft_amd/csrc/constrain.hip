@@ -27,11 +27,18 @@ constexpr uint32_t kPrompt = 0x80000000u, kSpecial = 0x40000000u, kCount = 0x3FF
 template <int BF16>
 __device__ __forceinline__ float4 load4(const void* p, int64_t i) {
   if constexpr (BF16) {
-    const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + i);
-    return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                       __uint_as_float(w.y & 0xFFFF0000u));
+    typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
+    const u32x2_t w =
+        __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(static_cast<const uint16_t*>(p) + i));
+    return make_float4(__uint_as_float(w[0] << 16), __uint_as_float(w[0] & 0xFFFF0000u), __uint_as_float(w[1] << 16),
+                       __uint_as_float(w[1] & 0xFFFF0000u));
   }
-  return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+  const f32x4_t w = __builtin_nontemporal_load(reinterpret_cast<const f32x4_t*>(static_cast<const float*>(p) + i));
+  return make_float4(w[0], w[1], w[2], w[3]);
+}
+
+__device__ __forceinline__ void store4(float* p, const float (&y)[4]) {
+  __builtin_nontemporal_store(f32x4_t{y[0], y[1], y[2], y[3]}, reinterpret_cast<f32x4_t*>(p));
 }
 
 template <int BF16>
@@ -188,14 +195,13 @@ __global__ __launch_bounds__(kConstrainThreads) void constrain_impl(const Constr
 #pragma unroll
         for (int u = 0; u < kGroup; ++u) {
           const int i = i0 + u;
-          if (i >= n) break;
           float y[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             y[e] = any ? value(y[e], w[e], i, v + e) : at_least_masked(y[e]);
             y[e] = bits[u] >> e & 1u ? y[e] : kMasked;
           }
-          *reinterpret_cast<float4*>(a.out + out_row(i) + v) = make_float4(y[0], y[1], y[2], y[3]);
+          if (i < n) store4(a.out + out_row(i) + v, y);
         }
       }
     } else {
