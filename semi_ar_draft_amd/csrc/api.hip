@@ -2016,8 +2016,10 @@ int dspark_constrain(dspark_ctx* c, hipStream_t stream, int B, int n_pos, int V,
   a.mask_b = mask_stride_b;
   a.mask_k = mask_stride_k;
   a.err = c->dev_err;
+  a.in_place = logits == out;
   // the largest slice that leaves four workgroups a CU (each reads the
-  // request's whole history)
+  // request's whole history; 1024 bf16 rows of 151936: 175 us in slices of
+  // 2048, 166 of 4096, 170 of 8192; with histories of 32768 185, 168, 170)
   int slice = kConstrainMaxSlice;
   while (slice > 1024 && (int64_t)B * ((V + slice - 1) / slice) < 4L * c->cu_count) slice /= 2;
   a.slice = slice;

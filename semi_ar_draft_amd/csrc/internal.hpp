@@ -320,6 +320,7 @@ const void* attend_join_kernel(int d);
 // stride_k, or packed rows offs[b] + i at stride_k.
 struct ConstrainArgs {
   int B, n_pos, V, slice, n_rows;
+  int in_place;                  // out is in
   const int32_t* offs;           // nullable
   const int32_t* K;              // rows - 1 of each request; nullable: n_pos rows
   const void* in;                // bf16 or float
@@ -345,8 +346,8 @@ struct ConstrainArgs {
   int64_t mask_b, mask_k;
   int32_t* err;
 };
-constexpr int kConstrainThreads = 256;
-constexpr int kConstrainMaxSlice = 8192;
+constexpr int kConstrainThreads = 512;
+constexpr int kConstrainMaxSlice = 4096;
 const void* constrain_kernel(int bf16);
 
 // Kernel lookup (host stubs usable with hipLaunchKernel and graph nodes).
