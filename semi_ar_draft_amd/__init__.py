@@ -9,6 +9,7 @@ fallback: if the library is missing, every call raises.
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 from typing import Optional
 
@@ -29,14 +30,13 @@ EXPORTS = (
     "dspark_pages_reserve", "dspark_pages_commit", "dspark_cache_write", "dspark_attend", "dspark_constrain",
     "dspark_timing_enable", "dspark_timing_read",
 )
-_LOGIT_TYPES = {torch.bfloat16: DSPARK_BF16, torch.float32: DSPARK_F32}
-_CACHE_TYPES = {torch.bfloat16: DSPARK_BF16, torch.float8_e4m3fn: DSPARK_E4M3}
 KERNEL_CLASSES = ("draft_sweep", "draft_combine", "confidence", "survival", "schedule",
                   "verify_rows", "verify_decide", "resid_sweep", "resid_combine", "gru", "diag", "sts_fit",
                   "draft_chain", "verify_chain", "conf_merge", "pages", "cache", "attend",
                   "constrain")
 
 _lib = None
+_native_module = None
 _vp, _i32, _i64, _u64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
 
 
@@ -176,70 +176,17 @@ def _logits3(t: torch.Tensor, name: str, device):
     return t.stride(0), t.stride(1)
 
 
-def _ints(device: torch.device, *vectors):
-    """Contiguous int32 vectors on the device, given as (tensor, entries, name).
-
-    The calls over a paged cache take ten of them at a few microseconds a
-    call, so what is right is told from four attributes; what is not goes
-    through the full checks for its message."""
-    index = device.index
-    for t, n, name in vectors:
-        if type(t) is torch.Tensor and t.numel() == n and t.dtype is torch.int32 and t.get_device() == index and \
-                t.dim() == 1 and t.is_contiguous():
-            continue
-        _need(t, name, torch.int32, device, 1)
-        if t.shape[0] != n:
-            raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
-
-
-def _table(table: torch.Tensor, B: int, device):
-    """Row stride and columns of a block table."""
-    if not (type(table) is torch.Tensor and table.dtype is torch.int32 and table.get_device() == device.index and
-            table.dim() == 2):
-        _need(table, "table", torch.int32, device, 2, contiguous=False)
-    rows, cols = table.shape
-    step, one = table.stride()
-    if rows != B or one != 1 and cols > 1:
-        raise ValueError(f"table must be [{B}][max_pages] with contiguous rows")
-    return (step if B > 1 else cols), cols
-
-
-def _rows(t: torch.Tensor, name: str, dtype, device, dims: int):
-    """A tensor of this type and rank on the device, contiguous in its last dimension."""
-    if not (type(t) is torch.Tensor and t.dtype is dtype and t.get_device() == device.index and t.dim() == dims):
-        _need(t, name, dtype, device, dims, contiguous=False)
-    if t.stride(-1) != 1 and t.shape[-1] > 1:
-        raise ValueError(f"{name} must be contiguous over its last dimension")
-
-
-def _cache(kc: torch.Tensor, vc: torch.Tensor, k_scale, v_scale, device):
-    """Element type of a pair of caches, and their strides of a page, a token and a head."""
-    kind = _CACHE_TYPES.get(kc.dtype)
-    if kind is None:
-        raise TypeError(f"the cache must be bf16 or float8_e4m3fn, got {kc.dtype}")
-    _rows(kc, "kcache", kc.dtype, device, 4)
-    _rows(vc, "vcache", kc.dtype, device, 4)
-    strides = kc.stride()
-    if vc.shape != kc.shape or vc.stride() != strides:
-        raise ValueError("kcache and vcache must have one shape and one set of strides")
-    sp, st, sh, _ = strides
-    n, page, heads, d = kc.shape
-    if heads == 1:                     # steps that are never taken: torch leaves them arbitrary
-        sh = d
-    if n == 1:
-        sp = max(page * st, heads * sh)
-    for t, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if t is not None:
-            _need(t, name, torch.float32, device, 1)
-            _len(t, heads, name)
-    return kind, sp, st, sh
-
-
-def _steps(t: torch.Tensor):
-    """Strides of the two leading dimensions, 0 for one that has a single entry."""
-    a, b, _ = t.stride()
-    n, m, _ = t.shape
-    return (a if n > 1 else 0), (b if m > 1 else 0)
+def _compiled():
+    """The compiled part of the binding (the calls over a paged cache, the logit constraints)."""
+    global _native_module
+    if _native_module is None:
+        load_library()
+        try:
+            module = importlib.import_module(__name__ + "._native")
+        except ImportError as e:
+            raise RuntimeError("the binding's compiled part is not built; run `python -m semi_ar_draft_amd.build`") from e
+        _native_module = module
+    return _native_module
 
 
 class Context:
@@ -253,6 +200,7 @@ class Context:
         if rc != DSPARK_OK:
             raise DSparkError(rc, f"dspark_create(device={device}) failed")
         self._h = h
+        self._native = _compiled()
 
     def close(self):
         if getattr(self, "_h", None):
@@ -613,23 +561,15 @@ class Context:
         arrays have n_rows entries (or those of ``out``).  Returns t_offsets
         [B + 1], row_req, row_pos, row_slot [n_rows] (int32)."""
         dev = self.device
-        B = K.shape[0]
-        ts, cols = _table(table, B, dev)
-        held_out = held if held_out is None else held_out
-        n_free_out = n_free if n_free_out is None else n_free_out
         if out is None:
             if n_rows is None:
                 raise ValueError("n_rows is needed where out is not given")
-            out = tuple(torch.empty((n,), dtype=torch.int32, device=dev) for n in (B + 1, n_rows, n_rows, n_rows))
+            out = tuple(torch.empty((n,), dtype=torch.int32, device=dev) for n in (K.shape[0] + 1, n_rows, n_rows, n_rows))
         offs, req, pos, slot = out
-        n_rows = slot.shape[0] if n_rows is None else n_rows
-        _ints(dev, (K, B, "K"), (length, B, "length"), (held, B, "held"), (held_out, B, "held_out"),
-              (free_list, n_pages, "free_list"), (n_free, 1, "n_free"), (n_free_out, 1, "n_free_out"),
-              (offs, B + 1, "t_offsets"), (req, n_rows, "row_req"), (pos, n_rows, "row_pos"), (slot, n_rows, "row_slot"))
-        self._rc(self.lib.dspark_pages_reserve(
-            self._h, _stream(dev, stream), B, page_size, n_pages, K.data_ptr(), length.data_ptr(), table.data_ptr(),
-            ts, cols, held.data_ptr(), held_out.data_ptr(), free_list.data_ptr(), n_free.data_ptr(),
-            n_free_out.data_ptr(), n_rows, offs.data_ptr(), req.data_ptr(), pos.data_ptr(), slot.data_ptr()))
+        self._rc(self._native.pages_reserve(
+            self._h.value, dev.index, _stream(dev, stream), page_size, n_pages, slot.shape[0] if n_rows is None else n_rows,
+            K, length, table, held, held if held_out is None else held_out, free_list, n_free,
+            n_free if n_free_out is None else n_free_out, offs, req, pos, slot))
         return offs, req, pos, slot
 
     # -- dspark_pages_commit ----------------------------------------------------------
@@ -640,20 +580,11 @@ class Context:
         length, held and n_free are updated in place unless their _out is
         given.  Returns the new lengths."""
         dev = self.device
-        B = length.shape[0]
-        ts, cols = _table(table, B, dev)
         len_out = length if len_out is None else len_out
-        held_out = held if held_out is None else held_out
-        n_free_out = n_free if n_free_out is None else n_free_out
-        _ints(dev, (length, B, "length"), (len_out, B, "len_out"), (accept_len, B, "accept_len"), (held, B, "held"),
-              (held_out, B, "held_out"), (free_list, n_pages, "free_list"), (n_free, 1, "n_free"),
-              (n_free_out, 1, "n_free_out"))
-        if finished is not None:
-            _ints(dev, (finished, B, "finished"))
-        self._rc(self.lib.dspark_pages_commit(
-            self._h, _stream(dev, stream), B, page_size, n_pages, length.data_ptr(), len_out.data_ptr(),
-            accept_len.data_ptr(), _ptr(finished), table.data_ptr(), ts, cols, held.data_ptr(), held_out.data_ptr(),
-            free_list.data_ptr(), n_free.data_ptr(), n_free_out.data_ptr()))
+        self._rc(self._native.pages_commit(
+            self._h.value, dev.index, _stream(dev, stream), page_size, n_pages, length, len_out, accept_len, finished,
+            table, held, held if held_out is None else held_out, free_list, n_free,
+            n_free if n_free_out is None else n_free_out))
         return len_out
 
     # -- dspark_cache_write -----------------------------------------------------------
@@ -662,19 +593,8 @@ class Context:
         ([n_pages][page_size][heads][d], bf16 or float8_e4m3fn with a scale per
         head; any order of pages, tokens and heads in memory that the strides
         describe)."""
-        dev = self.device
-        kind, sp, st, sh = _cache(kcache, vcache, k_scale, v_scale, dev)
-        n_pages, page_size, heads, d = kcache.shape
-        _rows(k, "k", torch.bfloat16, dev, 3)
-        _rows(v, "v", torch.bfloat16, dev, 3)
-        n_rows = k.shape[0]
-        if k.shape != (n_rows, heads, d) or v.shape != (n_rows, heads, d):
-            raise ValueError("k and v must be [n_rows][heads][d] of the cache")
-        _ints(dev, (row_slot, n_rows, "row_slot"))
-        self._rc(self.lib.dspark_cache_write(
-            self._h, _stream(dev, stream), n_rows, heads, d, page_size, n_pages, k.data_ptr(), *_steps(k),
-            v.data_ptr(), *_steps(v), row_slot.data_ptr(), kcache.data_ptr(), vcache.data_ptr(), sp, st, sh, kind,
-            _ptr(k_scale), _ptr(v_scale)))
+        self._rc(self._native.cache_write(self._h.value, self.device.index, _stream(self.device, stream), kcache, vcache,
+                                          k_scale, v_scale, k, v, row_slot))
 
     # -- dspark_attend ----------------------------------------------------------------
     def attend(self, q, kcache, vcache, table, length, gamma: int, K=None, t_offsets=None, causal: bool = True,
@@ -686,35 +606,11 @@ class Context:
         shape; rows of no request are left as they are); ``lse``: a float32
         [n_rows][heads_q] tensor to fill with the log-sum-exps."""
         dev = self.device
-        kind, sp, st, sh = _cache(kcache, vcache, k_scale, v_scale, dev)
-        n_pages, page_size, heads, d = kcache.shape
-        _rows(q, "q", torch.bfloat16, dev, 3)
-        n_rows, heads_q, dq = q.shape
-        if dq != d:
-            raise ValueError("q must be [n_rows][heads_q][d] with the cache's d")
-        B = length.shape[0]
-        ts, cols = _table(table, B, dev)
-        _ints(dev, (length, B, "length"))
-        if K is not None:
-            _ints(dev, (K, B, "K"))
-        if t_offsets is not None:
-            _rows(t_offsets, "t_offsets", torch.int32, dev, 1)
-            if t_offsets.shape[0] < B:
-                raise ValueError(f"t_offsets must have at least {B} entries")
         if out is None:
-            out = torch.zeros((n_rows, heads_q, d), dtype=torch.bfloat16, device=dev)
-        _rows(out, "out", torch.bfloat16, dev, 3)
-        if out.shape != q.shape:
-            raise ValueError("out must have the shape of q")
-        if lse is not None:
-            _need(lse, "lse", torch.float32, dev, 2)
-            if lse.shape != (n_rows, heads_q):
-                raise ValueError("lse must be [n_rows][heads_q]")
-        self._rc(self.lib.dspark_attend(
-            self._h, _stream(dev, stream), B, n_rows, gamma, heads_q, heads, d, q.data_ptr(), *_steps(q),
-            kcache.data_ptr(), vcache.data_ptr(), sp, st, sh, kind, _ptr(k_scale), _ptr(v_scale), page_size, n_pages,
-            table.data_ptr(), ts, cols, length.data_ptr(), _ptr(K), _ptr(t_offsets), 1 if causal else 0,
-            d ** -0.5 if scale is None else float(scale), out.data_ptr(), *_steps(out), _ptr(lse)))
+            out = torch.zeros(q.shape, dtype=torch.bfloat16, device=dev)
+        self._rc(self._native.attend(
+            self._h.value, dev.index, _stream(dev, stream), kcache, vcache, k_scale, v_scale, q, length, table, gamma, K,
+            t_offsets, causal, q.shape[-1] ** -0.5 if scale is None else scale, out, lse))
         return out
 
     # -- dspark_constrain -------------------------------------------------------------
@@ -732,83 +628,13 @@ class Context:
         themselves.  Returns out; rows of no request are left as they are (a
         new out holds zeros there)."""
         dev = self.device
-        packed = t_offsets is not None
-        dims = 2 if packed else 3
-        kind = _LOGIT_TYPES.get(logits.dtype)
-        if kind is None:
-            raise TypeError(f"logits must be bf16 or float32, got {logits.dtype}")
-        _rows(logits, "logits", logits.dtype, dev, dims)
         if out is None:
-            n, m = (1, logits.shape[0]) if packed else logits.shape[:2]
-            wide = -(-logits.shape[-1] // 4) * 4
-            out = torch.zeros((n, m, wide), dtype=torch.float32, device=dev)[:, :, :logits.shape[-1]]
-            out = out[0] if packed else out
-        _rows(out, "out", torch.float32, dev, dims)
-        V = logits.shape[-1]
-        if out.shape != logits.shape:
-            raise ValueError("out must have the shape of logits")
-        if packed:
-            n_rows = logits.shape[0]
-            _need(t_offsets, "t_offsets", torch.int32, dev, 1)
-            B = t_offsets.shape[0] if K is None else K.shape[0]
-            if t_offsets.shape[0] < B:
-                raise ValueError(f"t_offsets must have at least {B} entries")
-        else:
-            B, n_rows = logits.shape[0], 0
-            if logits.shape[1] < n_pos:
-                raise ValueError(f"logits have {logits.shape[1]} positions, n_pos is {n_pos}")
-        if K is not None:
-            _ints(dev, (K, B, "K"))
-
-        def steps(t, width):
-            """Strides of a request and of a row; a row that is the only one takes its width."""
-            if packed:
-                return 0, t.stride(0) if t.shape[0] > 1 else width
-            return t.stride(0) if B > 1 else 0, t.stride(1) if t.shape[1] > 1 else width
-
-        wide = -(-V // 8) * 8
-        hs = hm = ts = bs = bm = 0
-        if hist is not None:
-            _rows(hist, "hist", torch.int32, dev, 2)
-            if hist.shape[0] != B:
-                raise ValueError(f"hist must be [{B}][hist_max]")
-            hm = hist.shape[1]
-            hs = hist.stride(0) if B > 1 else hm
-            _ints(dev, (n_hist, B, "n_hist"))
-            if n_prompt is not None:
-                _ints(dev, (n_prompt, B, "n_prompt"))
-        if tokens is not None:
-            _rows(tokens, "tokens", torch.int32, dev, 2)
-            if tokens.shape[0] != B or tokens.shape[1] < n_pos - 1:
-                raise ValueError(f"tokens must be [{B}][>= n_pos - 1]")
-            ts = tokens.stride(0) if B > 1 else tokens.shape[1]
-        for t, name in ((rep, "rep"), (freq, "freq"), (pres, "pres")):
-            if t is not None:
-                _rows(t, name, torch.float32, dev, 1)
-                _len(t, B, name)
-        ids = values = n_bias = None
-        if bias is not None:
-            ids, values, n_bias = bias
-            _need(ids, "bias ids", torch.int32, dev, 2)
-            _need(values, "bias values", torch.float32, dev, 2)
-            if ids.shape[0] != B or values.shape != ids.shape:
-                raise ValueError(f"bias ids and values must be [{B}][n]")
-            bs = bm = ids.shape[1]
-            if n_bias is not None:
-                _ints(dev, (n_bias, B, "bias counts"))
-        mb = mk = 0
-        if mask is not None:
-            _rows(mask, "mask", torch.int32, dev, dims)
-            words = -(-V // 32)
-            if mask.shape[:-1] != logits.shape[:-1] or mask.shape[-1] < words:
-                raise ValueError(f"mask must have the rows of logits and {words} words in each")
-            mb, mk = steps(mask, mask.shape[-1])
-        lb, lk = steps(logits, wide)
-        ob, ok = steps(out, wide)
-        self._rc(self.lib.dspark_constrain(
-            self._h, _stream(dev, stream), B, n_pos, V, logits.data_ptr(), kind, lb, lk, _ptr(t_offsets), _ptr(K),
-            n_rows, _ptr(hist), hs, hm, _ptr(n_hist), _ptr(n_prompt), _ptr(tokens), ts, _ptr(rep), _ptr(freq),
-            _ptr(pres), _ptr(ids), _ptr(values), bs, bm, _ptr(n_bias), _ptr(mask), mb, mk, out.data_ptr(), ob, ok))
+            V = logits.shape[-1]
+            out = torch.zeros((*logits.shape[:-1], -(-V // 4) * 4), dtype=torch.float32, device=dev)[..., :V]
+        ids, values, n_bias = (None, None, None) if bias is None else bias
+        self._rc(self._native.constrain(
+            self._h.value, dev.index, _stream(dev, stream), logits, out, n_pos, K, t_offsets, hist, n_hist, n_prompt, tokens,
+            rep, freq, pres, ids, values, n_bias, mask))
         return out
 
     # -- dspark_sts_fit ---------------------------------------------------------------
