@@ -5,8 +5,8 @@
 // end, an offset and a marker per row).  Integer work on a few numbers per
 // request, bound by latency: one launch each, in which every workgroup scans
 // the requests for itself (12 bytes a request, from the caches) and then
-// writes its own share of the rows or pages, so that no workgroup waits for
-// another.  Arrays that may be updated in place (held, n_free, len) are
+// writes its own share of the rows or pages, one a thread, so that no workgroup
+// waits for another and a row costs one search in LDS and one load behind it.  Arrays that may be updated in place (held, n_free, len) are
 // written by the last workgroup to finish, after every other has read them.
 #include "common.hpp"
 #include "internal.hpp"
@@ -14,56 +14,51 @@
 namespace dspark {
 namespace {
 
-// Exclusive scan over the requests of two counts at once (rows and pages),
-// both below 2^31 in total or the result is not used: every thread sums its
-// run of consecutive requests, the workgroup scans the sums.  `n` and `x`
-// hold the counts on entry and their exclusive prefixes on return, entry B
-// the totals.  Returns false (to every thread) if a total passes 2^31 - 1.
-__device__ __forceinline__ bool scan_requests(int B, int32_t* n, int32_t* x, int64_t (*red)[2]) {
+// Exclusive scan over the requests of N counts at once, each below 2^31 in
+// total or the result is not used: every thread sums its run of consecutive
+// requests, the workgroup scans the sums.  x holds the counts on entry and
+// their exclusive prefixes on return, entry B the totals.  Returns false (to
+// every thread) if a total passes 2^31 - 1.
+template <int N>
+__device__ __forceinline__ bool scan_requests(int B, int32_t* const (&x)[N], int64_t (*red)[N]) {
   const int per = (B + kPagesThreads - 1) / kPagesThreads;
   const int b0 = min(B, (int)threadIdx.x * per), b1 = min(B, b0 + per);
-  int64_t sn = 0, sx = 0;
-  for (int b = b0; b < b1; ++b) {
-    sn += n[b];
-    sx += x[b];
-  }
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  int64_t in = sn, ix = sx;
+  int64_t sum[N], incl[N];
 #pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t un = __shfl_up(in, o, 64), ux = __shfl_up(ix, o, 64);
-    if (lane >= o) {
-      in += un;
-      ix += ux;
+  for (int k = 0; k < N; ++k) {
+    sum[k] = 0;
+    for (int b = b0; b < b1; ++b) sum[k] += x[k][b];
+    incl[k] = sum[k];
+  }
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      const int64_t u = __shfl_up(incl[k], o, 64);
+      if (lane >= o) incl[k] += u;
     }
-  }
-  if (lane == 63) {
-    red[w][0] = in;
-    red[w][1] = ix;
-  }
+  if (lane == 63)
+#pragma unroll
+    for (int k = 0; k < N; ++k) red[w][k] = incl[k];
   __syncthreads();
-  int64_t bn = 0, bx = 0, tn = 0, tx = 0;
+  bool ok = true;
 #pragma unroll
-  for (int i = 0; i < kPagesThreads / 64; ++i) {
-    if (i < w) {
-      bn += red[i][0];
-      bx += red[i][1];
+  for (int k = 0; k < N; ++k) {
+    int64_t at = incl[k] - sum[k], total = 0;
+#pragma unroll
+    for (int i = 0; i < kPagesThreads / 64; ++i) {
+      if (i < w) at += red[i][k];
+      total += red[i][k];
     }
-    tn += red[i][0];
-    tx += red[i][1];
-  }
-  const bool ok = tn <= INT32_MAX && tx <= INT32_MAX;
-  int64_t pn = bn + in - sn, px = bx + ix - sx;
-  for (int b = b0; b < b1; ++b) {
-    const int32_t cn = n[b], cx = x[b];
-    n[b] = (int32_t)pn;
-    x[b] = (int32_t)px;
-    pn += cn;
-    px += cx;
-  }
-  if (threadIdx.x == 0) {
-    n[B] = ok ? (int32_t)tn : 0;
-    x[B] = ok ? (int32_t)tx : 0;
+    for (int b = b0; b < b1; ++b) {
+      const int32_t c = x[k][b];
+      x[k][b] = (int32_t)at;
+      at += c;
+    }
+    const bool fits = total <= INT32_MAX;
+    ok = ok && fits;
+    if (threadIdx.x == 0) x[k][B] = fits ? (int32_t)total : 0;
   }
   __syncthreads();
   return ok;
@@ -81,14 +76,19 @@ __device__ __forceinline__ int owner(const int32_t* first, int B, int i) {
   return lo;
 }
 
-// True in every thread of the last workgroup of the launch to come here.
+// True in every thread of the last workgroup of the launch to come here.  The
+// others' loads have returned (their values are used before), and nothing they
+// stored is read, so that the count needs no fence.
 __device__ __forceinline__ bool last_workgroup(unsigned int* done, int* flag) {
+  if (gridDim.x == 1) {
+    __syncthreads();
+    return true;
+  }
   __syncthreads();
   if (threadIdx.x == 0) {
-    __threadfence();
-    const unsigned int n = atomicAdd(done, 1u);
+    const unsigned int n = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     *flag = n == gridDim.x - 1;
-    if (*flag) atomicExch(done, 0u);
+    if (*flag) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
   return *flag != 0;
@@ -99,7 +99,7 @@ __device__ __forceinline__ bool last_workgroup(unsigned int* done, int* flag) {
 // A row's slot needs no table entry of this launch: a page past held[b] is
 // looked up in the free list.
 __global__ __launch_bounds__(kPagesThreads) void pages_reserve_impl(const PagesArgs a) {
-  __shared__ int32_t n[kPagesMaxB + 1], x[kPagesMaxB + 1];
+  __shared__ int32_t n[kPagesMaxB + 1], x[kPagesMaxB + 1], lens[kPagesMaxB], helds[kPagesMaxB];
   __shared__ int64_t red[kPagesThreads / 64][2];
   __shared__ int bad, flag;
   if (threadIdx.x == 0) bad = 0;
@@ -110,12 +110,14 @@ __global__ __launch_bounds__(kPagesThreads) void pages_reserve_impl(const PagesA
     const int64_t need = ((int64_t)len + k + page) >> a.page_shift;
     const bool ok = k >= -1 && len >= 0 && held >= 0 && held <= a.cols && need <= a.cols;
     if (!ok) bad = 1;
+    lens[b] = len;
+    helds[b] = held;
     n[b] = ok ? k + 1 : 0;
     x[b] = ok && need > held ? (int32_t)(need - held) : 0;
   }
   const int32_t n_free = *a.n_free;
   __syncthreads();
-  const bool fits = scan_requests(a.B, n, x, red);
+  const bool fits = scan_requests<2>(a.B, {n, x}, red);
   const int32_t total = n[a.B], extra = x[a.B];
   const bool in_pool = n_free >= 0 && n_free <= a.n_pages && extra <= n_free;
   const bool refused = bad || !fits || total > a.n_rows || !in_pool;
@@ -128,8 +130,8 @@ __global__ __launch_bounds__(kPagesThreads) void pages_reserve_impl(const PagesA
     int req = -1, pos = -1, slot = -1;
     if (!refused && i < total) {
       req = owner(n, a.B, i);
-      const int32_t held = a.held[req];
-      pos = a.len[req] + i - n[req];
+      const int32_t held = helds[req];
+      pos = lens[req] + i - n[req];
       const int p = pos >> a.page_shift;
       const int32_t id =
           p < held ? a.table[req * a.tstride + p] : a.free_list[n_free - 1 - x[req] - (p - held)];
@@ -146,20 +148,20 @@ __global__ __launch_bounds__(kPagesThreads) void pages_reserve_impl(const PagesA
   if (!refused)
     for (int i = blockIdx.x * kPagesThreads + threadIdx.x; i < extra; i += stride) {
       const int b = owner(x, a.B, i);
-      a.table[b * a.tstride + a.held[b] + (i - x[b])] = a.free_list[n_free - 1 - i];
+      a.table[b * a.tstride + helds[b] + (i - x[b])] = a.free_list[n_free - 1 - i];
     }
   for (int b = blockIdx.x * kPagesThreads + threadIdx.x; b <= a.B; b += stride) a.offs[b] = refused ? 0 : n[b];
   if (!last_workgroup(a.done, &flag)) return;
   for (int b = threadIdx.x; b < a.B; b += kPagesThreads)
-    a.held_out[b] = a.held[b] + (refused ? 0 : x[b + 1] - x[b]);
+    a.held_out[b] = helds[b] + (refused ? 0 : x[b + 1] - x[b]);
   if (threadIdx.x == 0) *a.n_free_out = refused ? n_free : n_free - extra;
 }
 
 // Pages keep .. held - 1 of every request, pushed in request order and by
 // ascending place.
 __global__ __launch_bounds__(kPagesThreads) void pages_commit_impl(const PagesArgs a) {
-  __shared__ int32_t keep[kPagesMaxB + 1], x[kPagesMaxB + 1];
-  __shared__ int64_t red[kPagesThreads / 64][2];
+  __shared__ int32_t x[kPagesMaxB + 1], helds[kPagesMaxB];
+  __shared__ int64_t red[kPagesThreads / 64][1];
   __shared__ int bad, flag;
   if (threadIdx.x == 0) bad = 0;
   __syncthreads();
@@ -172,12 +174,12 @@ __global__ __launch_bounds__(kPagesThreads) void pages_commit_impl(const PagesAr
     const int64_t k = (new_len(b) + page - 1) >> a.page_shift;
     const bool ok = acc >= -1 && len >= 0 && held >= 0 && held <= a.cols && k <= held;
     if (!ok) bad = 1;
-    keep[b] = 0;
+    helds[b] = held;
     x[b] = ok ? held - (int32_t)k : 0;
   }
   const int32_t n_free = *a.n_free;
   __syncthreads();
-  const bool fits = scan_requests(a.B, keep, x, red);
+  const bool fits = scan_requests<1>(a.B, {x}, red);
   const int32_t given = x[a.B];
   const bool in_pool = n_free >= 0 && n_free <= a.n_pages && given <= a.n_pages - n_free;
   const bool refused = bad || !fits || !in_pool;
@@ -186,11 +188,11 @@ __global__ __launch_bounds__(kPagesThreads) void pages_commit_impl(const PagesAr
   if (!refused)
     for (int i = blockIdx.x * kPagesThreads + threadIdx.x; i < given; i += gridDim.x * kPagesThreads) {
       const int b = owner(x, a.B, i);
-      a.free_list[n_free + i] = a.table[b * a.tstride + a.held[b] - (x[b + 1] - i)];
+      a.free_list[n_free + i] = a.table[b * a.tstride + helds[b] - (x[b + 1] - i)];
     }
   if (!last_workgroup(a.done, &flag)) return;
   for (int b = threadIdx.x; b < a.B; b += kPagesThreads) {
-    const int32_t len = a.len[b], held = a.held[b];
+    const int32_t len = a.len[b], held = helds[b];
     a.len_out[b] = refused ? len : (int32_t)new_len(b);
     a.held_out[b] = refused ? held : held - (x[b + 1] - x[b]);
   }
