@@ -574,10 +574,12 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
  *     l1  = seen ? (l > 0 ? l / rep[b] : l * rep[b]) : l
  *     l2  = l1 - freq[b] * c - (c > 0 ? pres[b] : 0) + (sum of v's biases)
  *     out = allowed(v) ? max(l2, DSPARK_MASKED) : DSPARK_MASKED
- * in float32.  DSPARK_MASKED is finite, so that the rows can be drafted and
- * verified from as they are (-infinity would make a log-sum-exp NaN): logits
- * of -infinity or the type's lowest value become DSPARK_MASKED too; NaN
- * stays.  A row whose mask allows nothing is DSPARK_MASKED throughout.
+ * in float32.  The rows can be drafted and verified from as they are: masked
+ * entries weigh nothing there.  Logits of -infinity or the type's lowest value
+ * become DSPARK_MASKED too; NaN stays.  A row whose mask allows nothing is
+ * DSPARK_MASKED throughout; a draft or a verification that samples from such a
+ * row has nothing to choose from, raises the device error flag and emits
+ * token 0.
  *
  * logits: dtype BF16 or F32, V entries a row (any V), rows 16-byte aligned.
  * out: float, the same rows; F32 logits may be constrained in place (out =

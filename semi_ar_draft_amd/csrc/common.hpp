@@ -121,6 +121,19 @@ struct SoftmaxState {
   float s;   // sum of exp2(y2 - m)
 };
 
+// Where a lane's running maximum of y2 begins.  2^(y2 - m) is formed as a fused
+// multiply-add of the logit, so against a maximum m that is itself a rounded
+// product it is off by up to 2^(|m| 2^-24): nothing for logits, 2^(8e22) for a
+// lane that has met masked entries alone (DSPARK_MASKED).  A maximum never
+// below -2^28 keeps that at 2^16 at most; what lies below weighs 0.
+constexpr float kLowMax = -0x1.0p28f;
+
+// ln sum exp of a row's state; +infinity where no entry counted (every
+// probability formed with it is then 0).
+__device__ __forceinline__ float row_lse_of(float m, float s) {
+  return s == 0.0f ? INFINITY : (m + fast_log2(s)) * kLn2;
+}
+
 __device__ __forceinline__ void softmax_merge(float& m, float& s, float m2, float s2) {
   float mn = fmaxf(m, m2);
   float a = (m == mn) ? s : s * fast_exp2(m - mn);

@@ -96,7 +96,7 @@ struct LaneState {
 };
 
 __device__ __forceinline__ void lane_init(LaneState& st) {
-  st.m = -INFINITY;
+  st.m = kLowMax;
   st.s = 0.0f;
   st.key = -INFINITY;
   st.idx = 0x7fffffff;

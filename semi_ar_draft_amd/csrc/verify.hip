@@ -156,7 +156,7 @@ __device__ __forceinline__ void row_task(const VerifyArgs& a, int b, int k, int 
   const int nv4 = a.V >> 2;
   const int c0 = chunk * kRowsThreads * kRowsPer;
   const int c1 = min(nv4, c0 + kRowsThreads * kRowsPer);
-  RowState st{-INFINITY, 0.f, -INFINITY, 0x7fffffff};
+  RowState st{kLowMax, 0.f, -INFINITY, 0x7fffffff};
   if (a.greedy) {
     row_chunk<1>(st, p, c0, c1, a.s2, 0, 0);
   } else if (bonus) {
@@ -233,7 +233,7 @@ __device__ __forceinline__ void decide_request(const VerifyArgs& a, int b, int l
       RowState o{shfl_xor(st.m, mask), shfl_xor(st.s, mask), shfl_xor(st.key, mask), shfl_xor(st.idx, mask)};
       row_merge(st, o);
     }
-    const float lse_r = (st.m + fast_log2(st.s)) * kLn2;   // ln sum exp(t / T)
+    const float lse_r = row_lse_of(st.m, st.s);   // ln sum exp(t / T)
     // lane g0 + i takes the statistics of row g0 + i (held by lane 8 i)
     const int src = ((lane - g0) & 7) * 8;
     const float l2 = __shfl(lse_r, src, 64);
@@ -384,7 +384,7 @@ __device__ __forceinline__ void chain_task(const VerifyArgs& a, int b, int k, in
     xt = a.tokens[(int64_t)b * a.gamma + k - 1];
     if ((unsigned)xt >= (unsigned)a.V) xt = 0;             // the decision reports it and tests x = 0
   }
-  RowState st{-INFINITY, 0.f, -INFINITY, 0x7fffffff};
+  RowState st{kLowMax, 0.f, -INFINITY, 0x7fffffff};
   if (a.greedy) {
     row_fold_all<1>(st, x, c0, c1, a.s2, 0, 0);
   } else if (k == kb + 1) {
@@ -485,7 +485,7 @@ __device__ void chain_decide(const VerifyArgs& a, int b, int k, int lane, unsign
       RowState o{shfl_xor(st.m, mask), shfl_xor(st.s, mask), shfl_xor(st.key, mask), shfl_xor(st.idx, mask)};
       row_merge(st, o);
     }
-    const float lse_r = __shfl((st.m + fast_log2(st.s)) * kLn2, 0, 64);
+    const float lse_r = __shfl(row_lse_of(st.m, st.s), 0, 64);
     const int star = __shfl(st.idx, 0, 64);
     bool rej = false;
     if (test) {                                            // uniform over the wave
@@ -685,7 +685,7 @@ __global__ __launch_bounds__(64) void rows_lse_impl(const VerifyArgs a) {
     row_merge(st, RowState{q.x, q.y, q.z, a.pi[base + c]});
   }
   wave_row_reduce(st);
-  if (threadIdx.x == 0) a.row_lse[(int64_t)b * a.gamma + k - 1] = (st.m + fast_log2(st.s)) * kLn2;
+  if (threadIdx.x == 0) a.row_lse[(int64_t)b * a.gamma + k - 1] = row_lse_of(st.m, st.s);
 }
 
 }  // namespace
