@@ -559,7 +559,8 @@ class Context:
         int32 [n_pages]; n_free: int32 [1].  held and n_free are updated in
         place unless held_out and n_free_out are given; table is.  The row
         arrays have n_rows entries (or those of ``out``).  Returns t_offsets
-        [B + 1], row_req, row_pos, row_slot [n_rows] (int32)."""
+        [B + 1] (verify_packed takes its first B), row_req, row_pos, row_slot
+        [n_rows] (int32)."""
         dev = self.device
         if out is None:
             if n_rows is None:
