@@ -1193,10 +1193,11 @@ int check_cache(dspark_ctx* c, int heads, int d, int page_size, const void* kc, 
   const int64_t step = kv_dtype == DSPARK_E4M3 ? 16 : 8;
   if (!aligned16(kc) || !aligned16(vc) || c_page % step || c_tok % step || c_head % step)
     return fail(c, DSPARK_EINVAL, "the caches must be 16-byte aligned, their strides multiples of 16 bytes");
+  if (c_tok > INT32_MAX / 32 || c_head > INT64_MAX >> 16 || c_page > INT64_MAX >> 16)
+    return fail(c, DSPARK_EINVAL, "cache strides too large");
   const bool tok_major = c_head >= d && c_tok >= heads * c_head && c_page >= page_size * c_tok;
   const bool head_major = c_tok >= d && c_head >= page_size * c_tok && c_page >= heads * c_head;
   if (!tok_major && !head_major) return fail(c, DSPARK_EINVAL, "cache strides overlap");
-  if (c_tok > INT32_MAX / 32) return fail(c, DSPARK_EINVAL, "cache token stride too large");
   return DSPARK_OK;
 }
 
@@ -1916,8 +1917,6 @@ int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   a.cols = max_pages;
   a.causal = causal != 0;
   a.rows = 16 * mt;
-  a.tile_cost = 1;
-  a.min_steps = 1;
   a.q = static_cast<const uint16_t*>(q);
   a.q_row = q_stride_row;
   a.q_head = q_stride_head;

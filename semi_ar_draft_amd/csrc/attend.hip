@@ -43,6 +43,12 @@ namespace {
 
 constexpr int kStep = 32;        // tokens of a step
 constexpr int kWaves = kAttendThreads / 64;
+// What a tile costs besides its steps, in steps, and the steps of a wave's
+// stretch at least.  128 requests of 64 to 8192 tokens: 117 us with a cost of
+// 1, 119 with 2, 123 with 4; one row of one request of up to 1200 tokens: 14.2 us
+// with at least 1 step, 16.1 with 2 (a wave's first step waits for its loads,
+// the second is nearly free, but so is the wave that would take it).
+constexpr int kTileCost = 1, kMinSteps = 1;
 
 __device__ __forceinline__ f32x4_t mfma(const uint4 a, const uint4 b, const f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
@@ -287,6 +293,17 @@ struct Tile {
           s[mt][h] = mfma(kf, q[mt][ks], ks == 0 ? f32x4_t{0.f, 0.f, 0.f, 0.f} : s[mt][h]);
       }
     next_k();
+    // exponents against the maximum so far (0 where nothing was seen yet: then
+    // every p of a masked token is 2^-inf = 0 too)
+    float ref[MT], top[MT];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      ref[mt] = m[mt] == -INFINITY ? 0.0f : m[mt];
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[mt][h][i] = __builtin_fmaf(s[mt][h][i], sc, -ref[mt]);
+    }
     if (tail) {
       asm volatile("");                                  // a branch: few steps take it
 #pragma unroll
@@ -297,20 +314,12 @@ struct Tile {
           for (int i = 0; i < 4; ++i)
             if (base + 16 * h + 4 * g + i > lim[mt]) s[mt][h][i] = -INFINITY;
     }
-    // exponents against the maximum so far (0 where nothing was seen yet: then
-    // every p of a masked token is 2^-inf = 0 too)
-    float top[MT];
     bool grows = false;
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      const float ref = m[mt] == -INFINITY ? 0.0f : m[mt];
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) s[mt][h][i] = __builtin_fmaf(s[mt][h][i], sc, -ref);
       float x = fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3]));
       x = fmaxf(x, fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
-      top[mt] = x + ref;
+      top[mt] = x + ref[mt];
       grows |= top[mt] > m[mt] + 8.0f;
     }
     if (__any(grows)) {
@@ -396,7 +405,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
   auto row_tiles = [&](const Rows& r) { return (a.group * r.n + kRows - 1) / kRows; };
   auto steps = [&](const Rows& r) { return (r.len + r.n + kStep - 1) / kStep; };
   auto length = [&](const Rows& r) -> int64_t {
-    return r.n <= 0 ? 0 : (int64_t)a.Hkv * row_tiles(r) * (steps(r) + a.tile_cost);
+    return r.n <= 0 ? 0 : (int64_t)a.Hkv * row_tiles(r) * (steps(r) + kTileCost);
   };
   int64_t mine = 0;
   Rows r{0, 0, 0, 0};
@@ -420,7 +429,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
     total += sums[w];
   }
   const int64_t workers = (int64_t)gridDim.x * kWaves;
-  const int64_t chunk = max((int64_t)a.tile_cost + a.min_steps, (total + workers - 1) / workers);
+  const int64_t chunk = max((int64_t)kTileCost + kMinSteps, (total + workers - 1) / workers);
   const int64_t group_chunk = kWaves * chunk, group_u0 = blockIdx.x * group_chunk;
   if (group_u0 >= total) {
     if (tid == 0) a.joins[blockIdx.x].n = 0;
@@ -480,7 +489,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
   };
   // A workgroup leaves at most two pieces in memory: what it begins with and what it ends with.
   auto leave = [&]() {
-    float* part = a.part + (int64_t)(2 * blockIdx.x + (group_u0 < now.real0 - a.tile_cost ? 1 : 0)) * (kRows * (D + 2));
+    float* part = a.part + (int64_t)(2 * blockIdx.x + (group_u0 < now.real0 - kTileCost ? 1 : 0)) * (kRows * (D + 2));
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (lane < 16) *reinterpret_cast<float2*>(part + 2 * (mt * 16 + lane)) = make_float2(t.m[mt], t.l[mt]);
@@ -500,16 +509,16 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
     auto take = [&](Piece& p) {
       while (u < u1) {
         while (r.n <= 0) r = request_rows(a, uK, ulen, uoffs, ++b);   // u < u1 <= total: one follows
-        const int n_rt = row_tiles(r), size = steps(r) + a.tile_cost;
+        const int n_rt = row_tiles(r), size = steps(r) + kTileCost;
         const int seg = off / size, x0 = off - seg * size;
         const int x1 = (int)min((int64_t)size, x0 + (u1 - u));
         p.r = r;
-        p.n_s = size - a.tile_cost;
+        p.n_s = size - kTileCost;
         p.h = seg / n_rt;
         p.rt = seg - p.h * n_rt;
-        p.s0 = max(0, x0 - a.tile_cost);
-        p.s1 = x1 - a.tile_cost;
-        p.real0 = u - x0 + a.tile_cost;
+        p.s0 = max(0, x0 - kTileCost);
+        p.s1 = x1 - kTileCost;
+        p.real0 = u - x0 + kTileCost;
         p.table = a.table + b * a.tstride;
         if (u == group_u0 && lane == 0) {
           // of the workgroups whose stretches begin within a tile's steps the
@@ -521,7 +530,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
             j.h = p.h;
             j.rt = p.rt;
             j.n = (int)((p.real0 + p.n_s - 1) / group_chunk) - (int)blockIdx.x + 2;
-            j.slot = 2 * ((int)blockIdx.x - 1) + (group_u0 - group_chunk < p.real0 - a.tile_cost ? 1 : 0);
+            j.slot = 2 * ((int)blockIdx.x - 1) + (group_u0 - group_chunk < p.real0 - kTileCost ? 1 : 0);
           }
           a.joins[blockIdx.x] = j;
         }

@@ -286,8 +286,6 @@ struct AttendJoin {
 struct AttendArgs {
   int B, n_rows, gamma, Hq, Hkv, group, page_shift, n_pages, cols, causal;
   int rows;                      // rows of a tile: 16 mt
-  int tile_cost;                 // what a tile costs besides its steps, in steps
-  int min_steps;                 // steps of a wave's stretch at least
   const uint16_t* q;             // bf16
   int64_t q_row, q_head;
   const unsigned char* kc;       // caches, strides in bytes
