@@ -620,7 +620,7 @@ class Context:
         """Penalties, biases and grammar masks: float32 rows for draft and verify.
 
         logits (bf16 or float32): [B][>= n_pos][V], or with t_offsets (int32
-        [>= B]) packed rows [n_rows][V], request b's K[b] + 1 from t_offsets[b]
+        [>= B]; [B] where K is None) packed rows [n_rows][V], request b's K[b] + 1 from t_offsets[b]
         on.  hist int32 [B][hist_max] with n_hist (and n_prompt) int32 [B];
         tokens int32 [B][>= n_pos - 1], the drafts; rep, freq, pres float32
         [B]; bias = (ids int32 [B][n], ascending, values float32 [B][n],

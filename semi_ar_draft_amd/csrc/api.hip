@@ -1883,6 +1883,8 @@ int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   const bool head_major = (n_rows == 1 || o_stride_row >= d) &&
                           (heads_q == 1 || o_stride_head >= (n_rows == 1 ? d : n_rows * o_stride_row));
   if (!row_major && !head_major) return fail(c, DSPARK_EINVAL, "out strides overlap");
+  // (several workgroups may read a row of q while one of them writes its result)
+  if (out == q) return fail(c, DSPARK_EINVAL, "out may not be q");
   if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(c, DSPARK_EINVAL, "scale must be positive and finite");
   // the fewest 16-row blocks that hold a request's rows of one cache head, up
   // to 64 rows (d = 256: 32): a tile reads its keys once for all of them
@@ -1975,6 +1977,9 @@ int dspark_constrain(dspark_ctx* c, hipStream_t stream, int B, int n_pos, int V,
   };
   if (!apart(l_stride_b, l_stride_k, V) || !apart(o_stride_b, o_stride_k, V))
     return fail(c, DSPARK_EINVAL, "logit strides overlap rows of %d values", V);
+  if (logits == out &&
+      (bf16 || l_stride_k != o_stride_k || (!t_offsets && l_stride_b != o_stride_b)))
+    return fail(c, DSPARK_EINVAL, "in place only for float32 logits with equal strides");
   if (mask && !apart(mask_stride_b, mask_stride_k, (V + 31) / 32))
     return fail(c, DSPARK_EINVAL, "mask strides overlap rows of %d words", (V + 31) / 32);
   if (hist && (hist_max < 0 || hist_max >= (1 << 29) || hist_stride < hist_max))
