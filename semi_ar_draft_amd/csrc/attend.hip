@@ -379,6 +379,8 @@ struct Tile {
 };
 
 // Steps loaded ahead: two, or one where two and the sums pass the registers.
+// (More of the small steps cost more at a piece's beginning than they hide: three
+// 24.0, four 26.5 us against 23.4 on 48 draft blocks with heads of 64.)
 template <int D, int MT, int E4M3>
 constexpr int kAhead = D * MT >= 512 && !E4M3 ? 1 : 2;
 
