@@ -6,8 +6,8 @@
 //     o = sum_t p_t v_t / sum_t p_t,   p_t = 2^(s_t - m),
 //     s_t = (scale log2 e k_scale) q . k_t,
 // over the tokens t it sees, in one pass with a running m (a row's sums are
-// rescaled only when some score passes m by more than 8, so p_t stays below
-// 2^8 and the products keep their bits).
+// rescaled only when some score passes m by more than 8, so p_t stays within
+// 2^8 of the largest and the products keep their bits).
 //
 // Work: a tile is the rows of one request that share a cache head (rows times
 // heads per group, 16 MT of them at a time, so that a key is read once for
@@ -63,6 +63,20 @@ __device__ __forceinline__ f32x4_t mfma(const uint4 a, const uint4 b, const f32x
                                                  0, 0);
 }
 
+__device__ __forceinline__ f32x4_t mfma_f16(const uint4 a, const uint4 b, const f32x4_t c) {
+  typedef __attribute__((ext_vector_type(8))) _Float16 f16x8_t;
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, a), __builtin_bit_cast(f16x8_t, b), c, 0, 0,
+                                                0);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  typedef __attribute__((ext_vector_type(2))) _Float16 f16x2_t;
+  f16x2_t r;
+  r[0] = (_Float16)lo;                                   // to nearest even
+  r[1] = (_Float16)hi;
+  return __builtin_bit_cast(uint32_t, r);
+}
+
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
   bf16x2_t r;
@@ -86,10 +100,14 @@ __device__ __forceinline__ uint32_t odd_e4m3(uint32_t x) {
   return ((((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
 }
 
-// Two e4m3 values (the low or high half of w) as bf16: exact.
+// Two e4m3 values (the low or high half of w) as bf16 or f16: exact.
 template <bool HI>
 __device__ __forceinline__ uint32_t widen(uint32_t w) {
   return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, HI));
+}
+template <bool HI>
+__device__ __forceinline__ uint32_t widen_f16(uint32_t w) {
+  return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, HI));
 }
 
 typedef const __attribute__((address_space(4))) int32_t* uniform_ptr;   // scalar loads
@@ -182,8 +200,8 @@ struct Loaded {
     return make_uint4(widen<false>(lo), widen<true>(lo), widen<false>(hi), widen<true>(hi));
   }
 
-  // The value operands of blocks dt and dt + 1: rows d = D / 16 r + dt of V^T
-  // (r = lane % 16), the lane's eight tokens in pairs.
+  // The value operands of blocks dt and dt + 1, bf16 or (e4m3) f16: rows d =
+  // D / 16 r + dt of V^T (r = lane % 16), the lane's eight tokens in pairs.
   __device__ __forceinline__ void values(int dt, uint4 (&f)[2]) const {
     uint32_t x[2][4];
 #pragma unroll
@@ -195,8 +213,8 @@ struct Loaded {
       } else {
         const uint32_t e = v[2 * j][dt / 4], o = v[2 * j + 1][dt / 4];
         const uint32_t w = __builtin_amdgcn_perm(o, e, dt & 2 ? 0x07030602u : 0x05010400u);
-        x[0][j] = widen<false>(w);
-        x[1][j] = widen<true>(w);
+        x[0][j] = widen_f16<false>(w);
+        x[1][j] = widen_f16<true>(w);
       }
     }
     f[0] = make_uint4(x[0][0], x[0][1], x[0][2], x[0][3]);
@@ -250,6 +268,10 @@ struct Tile {
   static constexpr int kRows = 16 * MT;
   static constexpr int KS = D / 32;                      // products of 32 values per score
   static constexpr int DT = D / 16;                      // 16-wide blocks of a value row
+  // m stands this far below the row's maximum (in the exponent) when it is set.  The weights of an e4m3 cache
+  // are f16 in the second product: a row's largest lies between 2^7 and 2^15, below 65504, and what f16 cannot
+  // hold of the small ones is 2^-32 of it.
+  static constexpr float kHead = E4M3 ? 7.0f : 0.0f;
 
   uint4 q[MT][KS];
   f32x4_t o[MT][DT];
@@ -328,14 +350,14 @@ struct Tile {
       float x = fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3]));
       x = fmaxf(x, fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
       top[mt] = x + ref[mt];
-      grows |= top[mt] > m[mt] + 8.0f;
+      grows |= top[mt] > m[mt] + (8.0f + kHead);
     }
     if (__any(grows)) {
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
         float x = fmaxf(top[mt], shfl_xor(top[mt], 16));
         x = fmaxf(x, shfl_xor(x, 32));
-        const float mn = fmaxf(m[mt], x);
+        const float mn = fmaxf(m[mt], x - kHead);
         const float f = mn == m[mt] ? 1.0f : fast_exp2(m[mt] - mn);
         const float up = (m[mt] == -INFINITY ? 0.0f : m[mt]) - (mn == -INFINITY ? 0.0f : mn);
         m[mt] = mn;
@@ -348,7 +370,13 @@ struct Tile {
         for (int dt = 0; dt < DT; ++dt) o[mt][dt] *= f;
       }
     }
-    uint4 p[MT];
+    // The weights of the second product.  bf16 values: a weight is the sum of
+    // two bf16 numbers, its leading 8 bits and the rest to nearest, off by
+    // 2^-15 of it at most (rounded to one, 2^-8 of it, they cost as much as the
+    // rounding of the result does).  e4m3 values are exact in f16, whose 11
+    // bits leave 2^-11 of a weight, far below the rounding of the values that
+    // such a cache holds.
+    uint4 p[MT], rest[E4M3 ? 1 : MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       float e[8];
@@ -357,9 +385,19 @@ struct Tile {
 #pragma unroll
         for (int i = 0; i < 4; ++i) e[4 * h + i] = fast_exp2(s[mt][h][i]);
       l[mt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
-      // p as bf16 for the second product: at most 2^-8 of each term, of either
-      // sign, about what the bf16 result is rounded by itself
-      p[mt] = make_uint4(pack_bf16(e[0], e[1]), pack_bf16(e[2], e[3]), pack_bf16(e[4], e[5]), pack_bf16(e[6], e[7]));
+      uint32_t w[4], x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (E4M3) {
+          w[j] = pack_f16(e[2 * j], e[2 * j + 1]);
+        } else {
+          const uint32_t a = __float_as_uint(e[2 * j]), b = __float_as_uint(e[2 * j + 1]);
+          w[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);
+          x[j] = pack_bf16(e[2 * j] - __uint_as_float(a & 0xFFFF0000u), e[2 * j + 1] - __uint_as_float(b & 0xFFFF0000u));
+        }
+      }
+      p[mt] = make_uint4(w[0], w[1], w[2], w[3]);
+      if constexpr (!E4M3) rest[mt] = make_uint4(x[0], x[1], x[2], x[3]);
     }
     // a token that a query does not see must not reach it, but 0 times
     // infinity or NaN is NaN: such values are left out here and added to the
@@ -372,7 +410,14 @@ struct Tile {
 #pragma unroll
       for (int c = 0; c < 2; ++c)
 #pragma unroll
-        for (int mt = 0; mt < MT; ++mt) o[mt][dt + c] = mfma(f[c], p[mt], o[mt][dt + c]);
+        for (int mt = 0; mt < MT; ++mt) {
+          if constexpr (E4M3) {
+            o[mt][dt + c] = mfma_f16(f[c], p[mt], o[mt][dt + c]);
+          } else {
+            o[mt][dt + c] = mfma(f[c], p[mt], o[mt][dt + c]);
+            o[mt][dt + c] = mfma(f[c], rest[mt], o[mt][dt + c]);
+          }
+        }
     }
     next_v();
   }
