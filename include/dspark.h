@@ -28,6 +28,10 @@
  *    loop (DSPARK_GRAPH=1) is meant for capture.
  *  - Row-major layouts; strides are in elements.  Logit rows (U, target) are
  *    contiguous over the vocabulary and 16-byte aligned.
+ *  - A logit below -1e29 (dspark_constrain writes -1e30 for a masked entry)
+ *    weighs nothing in drafts, verifications and acceptance probabilities,
+ *    and no more does -infinity.  A sampled row without any other entry
+ *    raises the device error flag and gives token 0.
  *  - Tokens and request ids are 32-bit.  Request ids are read as unsigned.
  *  - Random numbers come from a counter-based hash keyed on
  *    (seed, request id, 1-based position, purpose): SplitMix64's output
@@ -577,8 +581,7 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
  *     l2  = l1 - freq[b] * c - (c > 0 ? pres[b] : 0) + (sum of v's biases)
  *     out = allowed(v) ? max(l2, DSPARK_MASKED) : DSPARK_MASKED
  * in float32.  The rows can be drafted and verified from as they are: masked
- * entries weigh nothing there (nor does any logit below -1.8e8 times the
- * temperature).  Logits of -infinity or the type's lowest value
+ * entries weigh nothing there.  Logits of -infinity or the type's lowest value
  * become DSPARK_MASKED too; NaN stays.  A row whose mask allows nothing is
  * DSPARK_MASKED throughout; a draft or a verification that samples from such a
  * row has nothing to choose from, raises the device error flag and emits

@@ -121,12 +121,14 @@ struct SoftmaxState {
   float s;   // sum of exp2(y2 - m)
 };
 
-// Where a lane's running maximum of y2 begins.  2^(y2 - m) is formed as a fused
-// multiply-add of the logit, so against a maximum m that is itself a rounded
-// product it is off by up to 2^(|m| 2^-24): nothing for logits, 2^(8e22) for a
-// lane that has met masked entries alone (DSPARK_MASKED).  A maximum never
-// below -2^28 keeps that at 2^16 at most; what lies below weighs 0.
-constexpr float kLowMax = -0x1.0p28f;
+// Where a lane's running maximum of y2 = s2 l begins: the place of a logit of
+// -1e29.  2^(y2 - m) is formed as a fused multiply-add of the logit, so against
+// a maximum m that is itself a rounded product it is off by up to 2^(|m|
+// 2^-24): nothing for logits, 2^(8e22) for a lane that has met masked entries
+// alone (DSPARK_MASKED, -1e30).  Against this one they weigh 0, and rows of any
+// other logits are what a beginning of -infinity makes them.  It is finite at
+// every temperature, or entries of -infinity would weigh 2^NaN.
+__device__ __forceinline__ float low_max(float s2) { return fmaxf(kMasked * 0.1f * s2, -1.0e38f); }
 
 // ln sum exp of a row's state; +infinity where no entry counted (every
 // probability formed with it is then 0).

@@ -95,8 +95,8 @@ struct LaneState {
   float pb, ebf;
 };
 
-__device__ __forceinline__ void lane_init(LaneState& st) {
-  st.m = kLowMax;
+__device__ __forceinline__ void lane_init(LaneState& st, float s2) {
+  st.m = low_max(s2);
   st.s = 0.0f;
   st.key = -INFINITY;
   st.idx = 0x7fffffff;
@@ -570,8 +570,8 @@ __global__ __launch_bounds__(256) void sweep_private_impl(const SweepArgs a) {
     if (!__any(w.ok[0] || w.ok[1])) return;
   }
   LaneState st[2];
-  lane_init(st[0]);
-  lane_init(st[1]);
+  lane_init(st[0], a.s2);
+  lane_init(st[1], a.s2);
   const int t0 = (int)((int64_t)a.n_tiles * vc / a.n_vc);
   const int t1 = (int)((int64_t)a.n_tiles * (vc + 1) / a.n_vc);
   const WT* __restrict__ W2 = static_cast<const WT*>(a.W2);
@@ -755,8 +755,8 @@ __global__ __launch_bounds__(256) void sweep_shared_impl(const SweepArgs a) {
     if (!__syncthreads_or(wave_active)) return;          // uniform over the block
   }
   LaneState st[2];
-  lane_init(st[0]);
-  lane_init(st[1]);
+  lane_init(st[0], a.s2);
+  lane_init(st[1], a.s2);
   // chunk boundaries on whole steps; only the last chunk may end mid-step
   const int n_steps = (a.n_tiles + NT - 1) / NT;
   const int t0 = min(NT * (int)((int64_t)n_steps * vc / a.n_vc), a.n_tiles);
@@ -981,7 +981,7 @@ __global__ __launch_bounds__(64 * NW) void draft_chain_impl(const SweepArgs a0) 
     const bool wave_active = __any(any_ok);
     LaneState st[NBW];
 #pragma unroll
-    for (int nb = 0; nb < NBW; ++nb) lane_init(st[nb]);
+    for (int nb = 0; nb < NBW; ++nb) lane_init(st[nb], a.s2);
     const int t0 = min(NT * (int)((int64_t)n_steps * vc / a.n_vc), a.n_tiles);
     const int t1 = min(NT * (int)((int64_t)n_steps * (vc + 1) / a.n_vc), a.n_tiles);
 
@@ -1305,7 +1305,7 @@ void draft_persist_impl(const SweepArgs a) {
       for (int s = 0; s < NS; ++s)
         Hf[s] = *reinterpret_cast<const FragT*>(hbuf + (nb * 16 + j) * 512 + (((4 * s + q) ^ j) * 16));
       LaneState st;
-      lane_init(st);
+      lane_init(st, a.s2);
 #pragma unroll
       for (int p = 0; p < NP; ++p) {
         if (p >= np) break;                              // uniform over the wave

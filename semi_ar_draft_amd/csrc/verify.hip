@@ -156,7 +156,7 @@ __device__ __forceinline__ void row_task(const VerifyArgs& a, int b, int k, int 
   const int nv4 = a.V >> 2;
   const int c0 = chunk * kRowsThreads * kRowsPer;
   const int c1 = min(nv4, c0 + kRowsThreads * kRowsPer);
-  RowState st{kLowMax, 0.f, -INFINITY, 0x7fffffff};
+  RowState st{low_max(a.s2), 0.f, -INFINITY, 0x7fffffff};
   if (a.greedy) {
     row_chunk<1>(st, p, c0, c1, a.s2, 0, 0);
   } else if (bonus) {
@@ -384,7 +384,7 @@ __device__ __forceinline__ void chain_task(const VerifyArgs& a, int b, int k, in
     xt = a.tokens[(int64_t)b * a.gamma + k - 1];
     if ((unsigned)xt >= (unsigned)a.V) xt = 0;             // the decision reports it and tests x = 0
   }
-  RowState st{kLowMax, 0.f, -INFINITY, 0x7fffffff};
+  RowState st{low_max(a.s2), 0.f, -INFINITY, 0x7fffffff};
   if (a.greedy) {
     row_fold_all<1>(st, x, c0, c1, a.s2, 0, 0);
   } else if (k == kb + 1) {
