@@ -31,7 +31,9 @@
  *  - A logit below -1e29 (dspark_constrain writes -1e30 for a masked entry)
  *    weighs nothing in drafts, verifications and acceptance probabilities,
  *    and no more does -infinity.  A sampled row without any other entry
- *    raises the device error flag and gives token 0.
+ *    raises the device error flag and gives token 0; a draft row of that kind
+ *    has lse = -infinity (an empty sum), and verification and acceptance
+ *    probabilities take each of its probabilities as 0.
  *  - Tokens and request ids are 32-bit.  Request ids are read as unsigned.
  *  - Random numbers come from a counter-based hash keyed on
  *    (seed, request id, 1-based position, purpose): SplitMix64's output

@@ -234,6 +234,11 @@ __device__ __forceinline__ void epilogue(LaneState& st, const f32x4_t z, const f
   }
 }
 
+// The draft's log-normaliser as probabilities are formed with it.  A row that
+// allows nothing has ln 0 = -infinity; every probability of it is 0, which
+// exp(y - lse) is with +infinity.
+__device__ __forceinline__ float draft_norm(float lse) { return lse == -INFINITY ? INFINITY : lse; }
+
 // End of a residual range: the keys log2 r_b - log2 E_b (and for p_t).
 __device__ __forceinline__ void resolve_resid(LaneState& st) {
   if (st.sb > 0.0f) st.key = fast_log2(st.sb) - fast_log2(st.eb);
@@ -353,11 +358,11 @@ struct WaveRows {
             given[nb] = a.tokens[(int64_t)b * a.gamma + k - 2];
         }
         if constexpr (MODE == kModeResidual) {
-          ld[nb] = a.lse[(int64_t)b * a.gamma + k - 1];
+          ld[nb] = draft_norm(a.lse[(int64_t)b * a.gamma + k - 1]);
           lt[nb] = a.resid_lt[b];
         }
         if constexpr (MODE == kModeAlpha) {
-          ld[nb] = a.lse[(int64_t)b * a.gamma + k - 1];
+          ld[nb] = draft_norm(a.lse[(int64_t)b * a.gamma + k - 1]);
           lt[nb] = a.resid_lt[(int64_t)b * a.gamma + k - 1];   // target log-normaliser of row (b, k)
         }
       }
