@@ -8,6 +8,7 @@ fallback: if the library is missing, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib
 import os
@@ -141,6 +142,11 @@ def _stream(device: torch.device, stream) -> int:
         # the current stream's handle without a Stream object around it
         return torch._C._cuda_getCurrentRawStream(device.index)
     return stream.cuda_stream
+
+
+def _on(stream):
+    """New tensors and their fills belong to the stream of the call that writes them."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
 
 
 def _wdtype(w: torch.Tensor) -> int:
@@ -565,7 +571,9 @@ class Context:
         if out is None:
             if n_rows is None:
                 raise ValueError("n_rows is needed where out is not given")
-            out = tuple(torch.empty((n,), dtype=torch.int32, device=dev) for n in (K.shape[0] + 1, n_rows, n_rows, n_rows))
+            with _on(stream):
+                out = tuple(torch.empty((n,), dtype=torch.int32, device=dev)
+                            for n in (K.shape[0] + 1, n_rows, n_rows, n_rows))
         offs, req, pos, slot = out
         self._rc(self._native.pages_reserve(
             self._h.value, dev.index, _stream(dev, stream), page_size, n_pages, slot.shape[0] if n_rows is None else n_rows,
@@ -608,7 +616,8 @@ class Context:
         [n_rows][heads_q] tensor to fill with the log-sum-exps."""
         dev = self.device
         if out is None:
-            out = torch.zeros(q.shape, dtype=torch.bfloat16, device=dev)
+            with _on(stream):
+                out = torch.zeros(q.shape, dtype=torch.bfloat16, device=dev)
         self._rc(self._native.attend(
             self._h.value, dev.index, _stream(dev, stream), kcache, vcache, k_scale, v_scale, q, length, table, gamma, K,
             t_offsets, causal, q.shape[-1] ** -0.5 if scale is None else scale, out, lse))
@@ -631,7 +640,8 @@ class Context:
         dev = self.device
         if out is None:
             V = logits.shape[-1]
-            out = torch.zeros((*logits.shape[:-1], -(-V // 4) * 4), dtype=torch.float32, device=dev)[..., :V]
+            with _on(stream):
+                out = torch.zeros((*logits.shape[:-1], -(-V // 4) * 4), dtype=torch.float32, device=dev)[..., :V]
         ids, values, n_bias = (None, None, None) if bias is None else bias
         self._rc(self._native.constrain(
             self._h.value, dev.index, _stream(dev, stream), logits, out, n_pos, K, t_offsets, hist, n_hist, n_prompt, tokens,
