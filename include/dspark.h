@@ -479,8 +479,9 @@ int dspark_verify_packed(dspark_ctx* ctx, hipStream_t stream,
  * row_slot: int32 [n_rows]; -1 for entries behind the last row);
  * held_out int32 [B] and n_free_out int32 [1], which may be held and n_free.
  * K may exceed 32 here (a prompt's rows).  If the pool, the table rows
- * (max_pages) or n_rows cannot hold the batch, or a K, length or count is
- * invalid, nothing is taken: the device error flag is raised, t_offsets are 0,
+ * (max_pages) or n_rows cannot hold the batch, a K, length or count is
+ * invalid, or a request holds too few pages for the len[b] tokens that it has,
+ * nothing is taken: the device error flag is raised, t_offsets are 0,
  * the row arrays -1, held_out = held, n_free_out = n_free.  A page id outside
  * [0, n_pages) is flagged and its rows get slot -1.
  *

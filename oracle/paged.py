@@ -25,9 +25,9 @@ def pages_reserve(K, length, table, held, free_list, n_free, page_size, n_rows):
     table, held = np.array(table), np.array(held)
     top, offs, rows = int(n_free), [0], []
     for b in range(len(K)):
-        if K[b] < -1 or length[b] < 0 or not 0 <= held[b] <= table.shape[1]:
+        if K[b] < -1 or length[b] < 0 or not 0 <= held[b] <= table.shape[1] or held[b] * page_size < length[b]:
             return None
-        while K[b] >= 0 and held[b] * page_size < length[b] + K[b] + 1 or held[b] * page_size < length[b]:
+        while held[b] * page_size < length[b] + K[b] + 1:
             if top == 0 or held[b] == table.shape[1]:
                 return None
             top -= 1

@@ -111,7 +111,9 @@ __global__ __launch_bounds__(kPagesThreads) void pages_reserve_impl(const PagesA
   for (int b = threadIdx.x; b < a.B; b += kPagesThreads) {
     const int32_t k = a.K[b], len = a.len[b], held = a.held[b];
     const int64_t need = ((int64_t)len + k + page) >> a.page_shift;
-    const bool ok = k >= -1 && len >= 0 && held >= 0 && held <= a.cols && need <= a.cols;
+    // (pages taken now for tokens that are cached already would hold none of them)
+    const bool ok = k >= -1 && len >= 0 && held >= 0 && held <= a.cols && need <= a.cols &&
+                    len <= (int64_t)held << a.page_shift;
     if (!ok) bad = 1;
     lens[b] = len;
     helds[b] = held;
