@@ -493,8 +493,9 @@ int dspark_verify_packed(dspark_ctx* ctx, hipStream_t stream,
  * checked to be >= -1, len_out[b] = 0 and every page goes back.  len_out and held_out may
  * be len and held, n_free_out may be n_free.  Table entries of pages given
  * back are left as they are.  If a length or count is invalid, a request
- * holds too few pages for its length, or the pool would overflow, nothing
- * changes (len_out = len, ...) and the error flag is raised.
+ * holds too few pages for its length, a page to be given back is outside [0,
+ * n_pages), or the pool would overflow, nothing changes (len_out = len, ...;
+ * entries of free_list behind its top may) and the error flag is raised.
  *
  * One launch each (timing class DSPARK_K_PAGES), no workspace.  Errors:
  * DSPARK_EINVAL for shapes, limits and null pointers. */

@@ -43,8 +43,8 @@ def pages_reserve(K, length, table, held, free_list, n_free, page_size, n_rows):
     return np.array(offs), req, pos, slot, table, held, top
 
 
-def pages_commit(length, accept_len, table, held, free_list, n_free, page_size, finished=None):
-    """(length, held, free_list, n_free), or None where an argument is invalid."""
+def pages_commit(length, accept_len, table, held, free_list, n_free, page_size, finished=None, n_pages=None):
+    """(length, held, free_list, n_free), or None where an argument is invalid (page ids too, where n_pages is given)."""
     length, held, free = np.array(length), np.array(held), list(free_list)
     top = int(n_free)
     for b in range(len(length)):
@@ -55,7 +55,7 @@ def pages_commit(length, accept_len, table, held, free_list, n_free, page_size, 
         if keep > held[b]:
             return None
         for p in range(keep, held[b]):
-            if top == len(free):
+            if top == len(free) or n_pages is not None and not 0 <= table[b][p] < n_pages:
                 return None
             free[top] = table[b][p]
             top += 1

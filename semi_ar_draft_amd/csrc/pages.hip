@@ -81,16 +81,16 @@ __device__ __forceinline__ int owner(const int32_t* first, int B, int i) {
 
 // True in every thread of the last workgroup of the launch to come here.  The
 // others' loads have returned (their values are used before), and nothing they
-// stored is read, so that the count needs no fence.
-__device__ __forceinline__ bool last_workgroup(unsigned int* done, int* flag) {
-  if (gridDim.x == 1) {
-    __syncthreads();
-    return true;
-  }
+// stored is read, so that the count needs no fence.  *bad (LDS) counts in its
+// upper half: nonzero in the last workgroup if it was in any.
+__device__ __forceinline__ bool last_workgroup(unsigned int* done, int* flag, int* bad) {
   __syncthreads();
+  if (gridDim.x == 1) return true;
   if (threadIdx.x == 0) {
-    const unsigned int n = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    *flag = n == gridDim.x - 1;
+    const unsigned int mine = 1u + (*bad ? 0x10000u : 0u);   // fewer than 2^16 workgroups
+    const unsigned int n = __hip_atomic_fetch_add(done, mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) + mine;
+    *flag = (n & 0xFFFFu) == gridDim.x;
+    *bad = n >> 16;
     if (*flag) __hip_atomic_store(done, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
   __syncthreads();
@@ -156,19 +156,20 @@ __global__ __launch_bounds__(kPagesThreads) void pages_reserve_impl(const PagesA
       a.table[b * a.tstride + helds[b] + (i - x[b])] = a.free_list[n_free - 1 - i];
     }
   for (int b = blockIdx.x * kPagesThreads + threadIdx.x; b <= a.B; b += stride) a.offs[b] = refused ? 0 : n[b];
-  if (!last_workgroup(a.done, &flag)) return;
+  if (!last_workgroup(a.done, &flag, &bad)) return;
   for (int b = threadIdx.x; b < a.B; b += kPagesThreads)
     a.held_out[b] = helds[b] + (refused ? 0 : x[b + 1] - x[b]);
   if (threadIdx.x == 0) *a.n_free_out = refused ? n_free : n_free - extra;
 }
 
 // Pages keep .. held - 1 of every request, pushed in request order and by
-// ascending place.
+// ascending place.  What a workgroup pushes stands behind the stack's top until
+// the last one raises it, which it does if every id is a page's.
 __global__ __launch_bounds__(kPagesThreads) void pages_commit_impl(const PagesArgs a) {
   __shared__ int32_t x[kPagesMaxB + 1], helds[kPagesMaxB];
   __shared__ int64_t red[kPagesThreads / 64][1];
-  __shared__ int bad, flag;
-  if (threadIdx.x == 0) bad = 0;
+  __shared__ int bad, bad_id, flag;
+  if (threadIdx.x == 0) bad = bad_id = 0;
   __syncthreads();
   const int64_t page = (int64_t)1 << a.page_shift;
   auto new_len = [&](int b) -> int64_t {
@@ -187,15 +188,21 @@ __global__ __launch_bounds__(kPagesThreads) void pages_commit_impl(const PagesAr
   const bool fits = scan_requests<1>(a.B, {x}, red);
   const int32_t given = x[a.B];
   const bool in_pool = n_free >= 0 && n_free <= a.n_pages && given <= a.n_pages - n_free;
-  const bool refused = bad || !fits || !in_pool;
+  bool refused = bad || !fits || !in_pool;
   if (refused && blockIdx.x == 0 && threadIdx.x == 0)
     atomicOr(a.err, (bad || !fits ? kErrCache : 0) | (in_pool ? 0 : kErrPool));
   if (!refused)
     for (int i = blockIdx.x * kPagesThreads + threadIdx.x; i < given; i += gridDim.x * kPagesThreads) {
       const int b = owner(x, a.B, i);
-      a.free_list[n_free + i] = a.table[b * a.tstride + helds[b] - (x[b + 1] - i)];
+      const int32_t id = a.table[b * a.tstride + helds[b] - (x[b + 1] - i)];
+      if ((unsigned)id >= (unsigned)a.n_pages) {
+        atomicOr(a.err, kErrPage);
+        bad_id = 1;
+      }
+      a.free_list[n_free + i] = id;
     }
-  if (!last_workgroup(a.done, &flag)) return;
+  if (!last_workgroup(a.done, &flag, &bad_id)) return;
+  refused = refused || bad_id != 0;
   for (int b = threadIdx.x; b < a.B; b += kPagesThreads) {
     const int32_t len = a.len[b], held = helds[b];
     a.len_out[b] = refused ? len : (int32_t)new_len(b);
