@@ -1753,7 +1753,7 @@ int dspark_pages_reserve(dspark_ctx* c, hipStream_t stream, int B, int page_size
   a.done = c->pages_done;
   a.err = c->dev_err;
   // a row a thread, up to a workgroup per CU
-  const int grid = std::max(1, std::min(c->cu_count, (n_rows + kPagesThreads - 1) / kPagesThreads));
+  const int grid = std::max(1, std::min(c->cu_count, (n_rows - 1) / kPagesThreads + 1));
   return klaunch(c, DSPARK_K_PAGES, pages_reserve_kernel(), dim3(grid), dim3(kPagesThreads), &a, stream);
 }
 

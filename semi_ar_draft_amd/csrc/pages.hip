@@ -129,9 +129,10 @@ __global__ __launch_bounds__(kPagesThreads) void pages_reserve_impl(const PagesA
   if (refused && blockIdx.x == 0 && threadIdx.x == 0)
     atomicOr(a.err, (bad || !fits || total > a.n_rows ? kErrCache : 0) | (in_pool ? 0 : kErrPool));
 
-  // the packed rows
-  const int stride = gridDim.x * kPagesThreads;
-  for (int i = blockIdx.x * kPagesThreads + threadIdx.x; i < a.n_rows; i += stride) {
+  // the packed rows (unsigned: the step behind the last row may pass 2^31)
+  const unsigned stride = gridDim.x * kPagesThreads;
+  for (unsigned u = blockIdx.x * kPagesThreads + threadIdx.x; u < (unsigned)a.n_rows; u += stride) {
+    const int i = (int)u;
     int req = -1, pos = -1, slot = -1;
     if (!refused && i < total) {
       req = owner(n, a.B, i);
@@ -151,11 +152,11 @@ __global__ __launch_bounds__(kPagesThreads) void pages_reserve_impl(const PagesA
   }
   // the new table entries (none if refused), and the offsets
   if (!refused)
-    for (int i = blockIdx.x * kPagesThreads + threadIdx.x; i < extra; i += stride) {
+    for (int i = blockIdx.x * kPagesThreads + threadIdx.x; i < extra; i += (int)stride) {
       const int b = owner(x, a.B, i);
       a.table[b * a.tstride + helds[b] + (i - x[b])] = a.free_list[n_free - 1 - i];
     }
-  for (int b = blockIdx.x * kPagesThreads + threadIdx.x; b <= a.B; b += stride) a.offs[b] = refused ? 0 : n[b];
+  for (int b = blockIdx.x * kPagesThreads + threadIdx.x; b <= a.B; b += (int)stride) a.offs[b] = refused ? 0 : n[b];
   if (!last_workgroup(a.done, &flag, &bad)) return;
   for (int b = threadIdx.x; b < a.B; b += kPagesThreads)
     a.held_out[b] = helds[b] + (refused ? 0 : x[b + 1] - x[b]);
