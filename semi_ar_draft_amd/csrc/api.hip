@@ -25,7 +25,7 @@ using namespace dspark;
 // chained-draft counters and release flags, the running-best slot groups and
 // the chunk partials, at fixed offsets.  One copy per GPU the library runs
 // on, held until the process ends; every call on that GPU shares it.
-constexpr size_t kScratchChainOff = 0;                        // 65 counter words
+constexpr size_t kScratchChainOff = 0;                        // kChainFirst + kChainCounters words
 constexpr size_t kScratchFlagsOff = 64 << 10;                 // kChainMaxGrid lines of 128 bytes
 constexpr size_t kScratchBestOff = kScratchFlagsOff + (size_t)kChainMaxGrid * 128;
 constexpr size_t kScratchBestBytes = 1 << 20;                 // B * gamma * 16 slots of 8 bytes
@@ -97,7 +97,7 @@ struct dspark_ctx {
   void* ws = nullptr;
   size_t ws_bytes = 0;
   int32_t* dev_err = nullptr;
-  unsigned int* pages_done = nullptr;   // finished workgroups of a page call (inside dev_err's block, zero between calls)
+  unsigned int* pages_done = nullptr;   // finished workgroups of a page call (DeviceWords, as dev_err, bar and chain)
   bool use_graph = false;
   int sweep_waves_per_cu = 8;     // occupancy target of the vocabulary sweeps
   // whole-draft kernel (Markov head, bf16, r = 256): used up to persist_max_b
@@ -116,12 +116,12 @@ struct dspark_ctx {
   // per-position sweeps instead)
   long coop_refused = 0;
   int bar_test = 0;               // failure injection (tests): barriers time out
-  unsigned int* bar = nullptr;    // its grid barrier counter (inside dev_err's block)
+  unsigned int* bar = nullptr;    // its grid barrier counter
   // chained draft kernel (Markov head, bf16, r in {128, 256}, one request quad
   // of three or four 32-row groups): every position in one launch; its ticket
-  // and per-position counters (inside dev_err's block, 33 words)
+  // and per-position counters
   bool use_chain = true;
-  unsigned int* chain = nullptr;  // 65 words: tickets, then per-position counters from word 32
+  unsigned int* chain = nullptr;  // tickets, then per-position counters
   unsigned int* chain_flags = nullptr;   // one 128-byte line per workgroup (kChainMaxGrid)
   int chain_wg_per_cu = -1;       // resident workgroups per CU (-1 = not yet asked)
   // shape of the chained draft: waves per workgroup, request rows per wave
@@ -1222,14 +1222,16 @@ int dspark_create(dspark_ctx** out, int device) {
   hipDeviceProp_t prop;
   if (hipGetDeviceProperties(&prop, device) == hipSuccess && prop.multiProcessorCount > 0)
     c->cu_count = prop.multiProcessorCount;
-  if (hipMalloc(&c->dev_err, 1024) != hipSuccess || hipMemset(c->dev_err, 0, 1024) != hipSuccess) {
+  if (hipMalloc(&c->dev_err, sizeof(DeviceWords)) != hipSuccess ||
+      hipMemset(c->dev_err, 0, sizeof(DeviceWords)) != hipSuccess) {
     (void)hipGetLastError();
     delete c;
     return DSPARK_EHIP;
   }
-  c->bar = reinterpret_cast<unsigned int*>(reinterpret_cast<char*>(c->dev_err) + 128);
-  c->chain = reinterpret_cast<unsigned int*>(reinterpret_cast<char*>(c->dev_err) + 512);
-  c->pages_done = reinterpret_cast<unsigned int*>(reinterpret_cast<char*>(c->dev_err) + 896);
+  DeviceWords* words = reinterpret_cast<DeviceWords*>(c->dev_err);   // addresses in it; the host reads none
+  c->bar = &words->bar;
+  c->chain = words->chain;
+  c->pages_done = &words->pages_done;
   if (hipMalloc(&c->chain_flags, (size_t)kChainMaxGrid * 128) != hipSuccess ||
       hipMemset(c->chain_flags, 0, (size_t)kChainMaxGrid * 128) != hipSuccess) {
     (void)hipGetLastError();

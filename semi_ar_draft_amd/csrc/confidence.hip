@@ -186,8 +186,8 @@ __global__ __launch_bounds__(kConfMergeThreads) void conf_merge_impl(const ConfM
     s_tok = idx;
   }
   if (m.bar && b == 0 && k == 1 && threadIdx.x == 0) *m.bar = 0u;   // grid barrier of the whole-draft kernel
-  if (m.chain && b == 0 && k == 1 && threadIdx.x < 97)   // chained draft counters
-    m.chain[threadIdx.x == 0 ? 0 : 31 + threadIdx.x] = 0u;
+  if (m.chain && b == 0 && k == 1 && threadIdx.x <= kChainCounters)   // chained draft counters
+    m.chain[threadIdx.x == 0 ? 0 : kChainFirst - 1 + threadIdx.x] = 0u;
   if (m.best && threadIdx.x < kBestGroups) {   // read above, before this barrier
     unsigned long long* slot = m.best + ((int64_t)(k - 1) * kBestGroups + threadIdx.x) * m.B + b;
     __hip_atomic_store(slot, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);

@@ -1095,7 +1095,7 @@ __global__ __launch_bounds__(64 * NW) void draft_chain_impl(const SweepArgs a0) 
     if (wid == 0) {
       unsigned before = 0;
       if (lane == 0)
-        before = __hip_atomic_fetch_add(a0.chain + 32 + kg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        before = __hip_atomic_fetch_add(a0.chain + kChainFirst + kg, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       before = __shfl(before, 0, 64);
       if (before == (unsigned)per_kg - 1u) {
         // the last item of (k, g): release every workgroup's wait on group g
@@ -1392,8 +1392,8 @@ __global__ __launch_bounds__(kCombineThreads) void combine_draft_impl(const Comb
     a.ytok[o] = a.greedy ? p.key : p.zb;   // sampling partials carry y itself
   }
   if (a.bar && b == 0 && k == 1 && threadIdx.x == 0) *a.bar = 0u;   // grid barrier of the whole-draft kernel
-  if (a.chain && b == 0 && k == 1 && threadIdx.x < 97)   // chained draft counters
-    a.chain[threadIdx.x == 0 ? 0 : 31 + threadIdx.x] = 0u;
+  if (a.chain && b == 0 && k == 1 && threadIdx.x <= kChainCounters)   // chained draft counters
+    a.chain[threadIdx.x == 0 ? 0 : kChainFirst - 1 + threadIdx.x] = 0u;
   if (a.best && threadIdx.x < kBestGroups) {
     unsigned long long* slot = a.best + ((int64_t)(k - 1) * kBestGroups + threadIdx.x) * a.B + b;
     __hip_atomic_store(slot, 0ull, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
