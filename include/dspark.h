@@ -113,10 +113,14 @@ int dspark_check(dspark_ctx* ctx, hipStream_t stream);
  * the whole-draft kernel, the default for small batches, is bracketed by events
  * recorded on the stream around it instead, which include that gap), and
  * the draft loop is
- * launched kernel by kernel even where a graph was requested.  dspark_timing_read waits
- * for the recorded events, writes per-kernel-class totals (milliseconds) and
- * launch counts into arrays of DSPARK_K_COUNT entries, and forgets them.
- * Errors: DSPARK_EINVAL for null arguments, DSPARK_EHIP if an event fails. */
+ * launched kernel by kernel even where a graph was requested.
+ * dspark_timing_read_classes waits for the recorded events, writes the totals
+ * (milliseconds) and launch counts of the first n kernel classes (1 ..
+ * DSPARK_K_COUNT) into arrays of n entries, and forgets all of them.
+ * dspark_timing_read is the same call with n = 15, DSPARK_K_CONF_MERGE the last:
+ * its arrays never grow, however many classes a later library has.
+ * Errors: DSPARK_EINVAL for null arguments and n, DSPARK_EHIP if an event
+ * fails. */
 enum {
   DSPARK_K_DRAFT_SWEEP = 0,    /* MFMA bias + vocabulary sweep of one position (or of
                                   every position: the whole-draft kernel) */
@@ -142,6 +146,7 @@ enum {
 };
 int dspark_timing_enable(dspark_ctx* ctx, int enable);
 int dspark_timing_read(dspark_ctx* ctx, double* ms, int* launches);
+int dspark_timing_read_classes(dspark_ctx* ctx, int n, double* ms, int* launches);
 
 /* Semi-autoregressive draft with the Markov head.
  *

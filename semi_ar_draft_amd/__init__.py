@@ -29,7 +29,7 @@ EXPORTS = (
     "dspark_confidence", "dspark_schedule", "dspark_schedule_async", "dspark_verify",
     "dspark_verify_packed", "dspark_accept_prob", "dspark_sts_fit", "dspark_stream_read",
     "dspark_pages_reserve", "dspark_pages_commit", "dspark_cache_write", "dspark_attend", "dspark_constrain",
-    "dspark_timing_enable", "dspark_timing_read",
+    "dspark_timing_enable", "dspark_timing_read", "dspark_timing_read_classes",
 )
 KERNEL_CLASSES = ("draft_sweep", "draft_combine", "confidence", "survival", "schedule",
                   "verify_rows", "verify_decide", "resid_sweep", "resid_combine", "gru", "diag", "sts_fit",
@@ -70,6 +70,8 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.dspark_timing_enable.argtypes = [_vp, _i32]
     lib.dspark_timing_read.restype = _i32
     lib.dspark_timing_read.argtypes = [_vp, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i32)]
+    lib.dspark_timing_read_classes.restype = _i32
+    lib.dspark_timing_read_classes.argtypes = [_vp, _i32, ctypes.POINTER(ctypes.c_double), ctypes.POINTER(_i32)]
     lib.dspark_draft_markov.restype = _i32
     lib.dspark_draft_markov.argtypes = [
         _vp, _vp, _i32, _i32, _i32, _i32, _i32,
@@ -242,7 +244,7 @@ class Context:
         n = len(KERNEL_CLASSES)
         ms = (ctypes.c_double * n)()
         cnt = (_i32 * n)()
-        self._rc(self.lib.dspark_timing_read(self._h, ms, cnt))
+        self._rc(self.lib.dspark_timing_read_classes(self._h, n, ms, cnt))
         return {name: (ms[i], cnt[i]) for i, name in enumerate(KERNEL_CLASSES)}
 
     # -- dspark_draft_markov ------------------------------------------------
