@@ -151,8 +151,9 @@ struct Cache {
     else raise(PyExc_TypeError, "the cache must be bf16 or float8_e4m3fn, got %s", c10::toString(st));
     const T* vc = a.rows("vcache", st, 4);
     if (kc->dim() != 4) raise(PyExc_ValueError, "kcache must have 4 dims, got %lld", (long long)kc->dim());
-    if (kc->sizes() != vc->sizes() || kc->strides() != vc->strides())
-      raise(PyExc_ValueError, "kcache and vcache must have one shape and one set of strides");
+    bool alike = kc->sizes() == vc->sizes();
+    for (int i = 0; i < 4; ++i) alike = alike && step(*kc, i) == step(*vc, i);
+    if (!alike) raise(PyExc_ValueError, "kcache and vcache must have one shape and one set of strides");
     if (kc->stride(3) != 1) raise(PyExc_ValueError, "the cache must be contiguous over a head's values");
     n_pages = to_int("n_pages", kc->size(0));
     page = to_int("page_size", kc->size(1));
