@@ -607,7 +607,7 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
  * hist: int32 [B][hist_stride], n_hist (0 .. hist_max), n_prompt int32 [B]
  * (n_prompt NULL: no prompt); hist NULL: no history.  tokens: int32 [B]
  * [tok_stride], the drafts (>= n_pos - 1 a request), or NULL: drafts do not
- * count (a draft's own rows).  rep (positive, finite; else flagged and 1),
+ * count (a draft's own rows).  rep (positive, normal, finite; else flagged and 1),
  * freq, pres: float [B], or NULL for 1, 0, 0.  bias_ids, bias_values:
  * [B][bias_stride], of which the first n_bias[b] (NULL: bias_max) count; ids
  * ascend (else flagged), equal ids add up in order.  mask: int32 words, bit v

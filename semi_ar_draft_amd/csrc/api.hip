@@ -1406,7 +1406,7 @@ int dspark_check(dspark_ctx* c, hipStream_t stream) {
                 (flag & kErrSlot) ? " cache slot out of range" : "",
                 (flag & kErrHist) ? " history or bias length out of range" : "",
                 (flag & kErrBias) ? " bias ids not ascending" : "",
-                (flag & kErrPenalty) ? " repetition penalty not positive and finite" : "");
+                (flag & kErrPenalty) ? " repetition penalty not positive, normal and finite" : "");
   }
   c->err.clear();
   return DSPARK_OK;

@@ -50,7 +50,8 @@ struct Penalty {
 
 __device__ __forceinline__ float penalised(float x, uint32_t word, const Penalty& p) {
   const float c = (float)(word & kCount);
-  // x / rep: the reciprocal's product and its remainder, within a unit of the last place
+  // x / rep: the reciprocal's product and its remainder, within a unit of the
+  // last place (1.5 where x is subnormal); rep is normal
   const float q = x * p.inv;
   const float d = __builtin_fmaf(__builtin_fmaf(-q, p.rep, x), p.inv, q);
   const float y = x > 0.0f ? (d == d ? d : q) : x * p.rep;
@@ -140,7 +141,7 @@ __global__ __launch_bounds__(kConstrainThreads) void constrain_impl(const Constr
     if (report && (unsigned)drafted[tid] >= (unsigned)a.V) atomicOr(a.err, kErrToken);
   }
   const float rep = a.rep ? a.rep[b] : 1.0f;
-  const bool rep_ok = rep > 0.0f && rep < INFINITY;
+  const bool rep_ok = rep >= 0x1p-126f && rep < INFINITY;   // (a subnormal one's reciprocal is infinite)
   if (!rep_ok && report && tid == 0) atomicOr(a.err, kErrPenalty);
   Penalty pen;
   pen.rep = rep_ok ? rep : 1.0f;
