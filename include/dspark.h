@@ -614,8 +614,8 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
  * % 32 of word v / 32 set where v is allowed, placed like the rows with its
  * own strides (in words); NULL: all allowed.  Token ids outside [0, V) are
  * flagged and ignored.
- * 1 <= n_pos <= 33, B <= 65535.  One launch (timing class
- * DSPARK_K_CONSTRAIN), no workspace.  Errors: DSPARK_EINVAL. */
+ * 1 <= n_pos <= 33, B <= 65535, V <= 2^29, hist_max and bias_max < 2^29.
+ * One launch (timing class DSPARK_K_CONSTRAIN), no workspace.  Errors: DSPARK_EINVAL. */
 #define DSPARK_MASKED (-1.0e30f)
 int dspark_constrain(dspark_ctx* ctx, hipStream_t stream, int B, int n_pos, int V,
                      const void* logits, dspark_dtype dtype, int64_t l_stride_b, int64_t l_stride_k,

@@ -1996,8 +1996,8 @@ int dspark_constrain(dspark_ctx* c, hipStream_t stream, int B, int n_pos, int V,
   if (hist && (hist_max < 0 || hist_max >= (1 << 29) || hist_stride < hist_max))
     return fail(c, DSPARK_EINVAL, "hist_max must be in 0..2^29 - 1 and at most hist_stride");
   if (tokens && tok_stride < n_pos - 1) return fail(c, DSPARK_EINVAL, "tokens must hold n_pos - 1 entries a request");
-  if (bias_ids && (bias_max < 0 || bias_stride < bias_max))
-    return fail(c, DSPARK_EINVAL, "bias_max must be >= 0 and at most bias_stride");
+  if (bias_ids && (bias_max < 0 || bias_max >= (1 << 29) || bias_stride < bias_max))
+    return fail(c, DSPARK_EINVAL, "bias_max must be in 0..2^29 - 1 and at most bias_stride");
   DeviceGuard dg(c->device);
   if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
   ConstrainArgs a;
