@@ -583,7 +583,9 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
  *
  * [blog] "形式化定义": the target scores every drafted position in one pass.
  * Row i (0-based) of request b follows the request's history and its first i
- * drafts.  For every vocabulary entry v with logit l, c = the occurrences of v
+ * drafts.  The history is every token before x_1, so it ends with the anchor:
+ * of a step whose cache holds len[b] tokens, hist[b][len[b]] is the anchor and
+ * n_hist[b] = len[b] + 1.  For every vocabulary entry v with logit l, c = the occurrences of v
  * in hist[b][n_prompt[b] .. n_hist[b]) and among tokens[b][0 .. i), seen = v
  * occurs there or in hist[b][0 .. n_prompt[b]):
  *     l1  = seen ? (l > 0 ? l / rep[b] : l * rep[b]) : l

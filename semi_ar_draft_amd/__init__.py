@@ -632,7 +632,9 @@ class Context:
 
         logits (bf16 or float32): [B][>= n_pos][V], or with t_offsets (int32
         [>= B]; [B] where K is None) packed rows [n_rows][V], request b's K[b] + 1 from t_offsets[b]
-        on.  hist int32 [B][hist_max] with n_hist (and n_prompt) int32 [B];
+        on.  hist int32 [B][hist_max] with n_hist (and n_prompt) int32 [B]:
+        every token before the first draft, so the last one is the anchor
+        (n_hist = cached tokens + 1);
         tokens int32 [B][>= n_pos - 1], the drafts; rep, freq, pres float32
         [B]; bias = (ids int32 [B][n], ascending, values float32 [B][n],
         counts int32 [B] or None); mask int32 words of allowed bits, shaped as
