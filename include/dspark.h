@@ -552,10 +552,10 @@ int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int head
  * non-causal query block).  gamma = 0 is one token a request.  The rows' own
  * keys and values are in the cache already (dspark_cache_write).  Masked
  * tokens and the places of a page behind the last token have no effect,
- * whatever their bits are.  Scores and sums are float32; before its product
- * with the values a weight is rounded by 2^-15 of it at most (bf16 cache) or
- * to f16 (e4m3 cache: 2^-11 of it, 2^-32 of the row's largest), and the result
- * to bf16.
+ * whatever their bits are.  Scores (below 1.8e8 in magnitude) and sums are
+ * float32; before its product with the values a weight is rounded by 2^-15 of
+ * it at most (bf16 cache) or to f16 (e4m3 cache: 2^-11 of it, 2^-32 of the row's
+ * largest), and the result to bf16.
  * len, K: int32 [B] (K NULL: gamma for all; -1: no rows; outside -1..gamma:
  * clamped and flagged); t_offsets: int32 [>= B] or NULL for b * (gamma + 1);
  * rows that no request takes are left as they are.  A request whose length

@@ -270,7 +270,8 @@ struct Tile {
   static constexpr int DT = D / 16;                      // 16-wide blocks of a value row
   // m stands this far below the row's maximum (in the exponent) when it is set.  The weights of an e4m3 cache
   // are f16 in the second product: a row's largest lies between 2^7 and 2^15, below 65504, and what f16 cannot
-  // hold of the small ones is 2^-32 of it.
+  // hold of the small ones is 2^-32 of it.  (From maxima of 2^25 on, where a float's step is 4, the largest may lie
+  // as low as 2^-8; from 2^28 on, where it is 32, it may pass 65504.)
   static constexpr float kHead = E4M3 ? 7.0f : 0.0f;
 
   uint4 q[MT][KS];
@@ -350,7 +351,9 @@ struct Tile {
       float x = fmaxf(fmaxf(s[mt][0][0], s[mt][0][1]), fmaxf(s[mt][0][2], s[mt][0][3]));
       x = fmaxf(x, fmaxf(fmaxf(s[mt][1][0], s[mt][1][1]), fmaxf(s[mt][1][2], s[mt][1][3])));
       top[mt] = x + ref[mt];
-      grows |= top[mt] > m[mt] + (8.0f + kHead);
+      // (the difference, not top > m + 15, which rounds past the limit of f16 where m is large; before
+      // the first score it is infinite, or NaN where nothing is seen)
+      grows |= top[mt] - m[mt] > 8.0f + kHead;
     }
     if (__any(grows)) {
 #pragma unroll
