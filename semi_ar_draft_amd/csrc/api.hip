@@ -1946,6 +1946,7 @@ int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   a.K = K;
   a.offs = t_offsets;
   a.scale2 = scale * kLog2e;
+  a.unrest = e4m3 ? 1.0f : 1.0f / kRestFactor;
   a.out = static_cast<uint16_t*>(out);
   a.o_row = o_stride_row;
   a.o_head = o_stride_head;

@@ -376,7 +376,9 @@ struct Tile {
     // The weights of the second product.  bf16 values: a weight is the sum of
     // two bf16 numbers, its leading 8 bits and the rest to nearest, off by
     // 2^-15 of it at most (rounded to one, 2^-8 of it, they cost as much as the
-    // rounding of the result does).  e4m3 values are exact in f16, whose 11
+    // rounding of the result does).  The rest is that of 1 + 2^-16 times the
+    // weight (a.unrest takes the factor out of the result): positive wherever
+    // the weight is, since 0 times an infinite value is NaN.  e4m3 values are exact in f16, whose 11
     // bits leave 2^-11 of a weight, far below the rounding of the values that
     // such a cache holds.
     uint4 p[MT], rest[E4M3 ? 1 : MT];
@@ -396,7 +398,8 @@ struct Tile {
         } else {
           const uint32_t a = __float_as_uint(e[2 * j]), b = __float_as_uint(e[2 * j + 1]);
           w[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-          x[j] = pack_bf16(e[2 * j] - __uint_as_float(a & 0xFFFF0000u), e[2 * j + 1] - __uint_as_float(b & 0xFFFF0000u));
+          x[j] = pack_bf16(__builtin_fmaf(e[2 * j], kRestFactor, -__uint_as_float(a & 0xFFFF0000u)),
+                           __builtin_fmaf(e[2 * j + 1], kRestFactor, -__uint_as_float(b & 0xFFFF0000u)));
         }
       }
       p[mt] = make_uint4(w[0], w[1], w[2], w[3]);
@@ -525,7 +528,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
       const int grow = now.rt * kRows + mt * 16 + (lane & 15);
       if (grow >= a.group * now.r.n) continue;
       const int i = grow / a.group, hh = grow - i * a.group;
-      const float inv = vs / t.l[mt];
+      const float inv = vs * a.unrest / t.l[mt];
       uint16_t* op = a.out + (int64_t)(now.r.row0 + i) * a.o_row + (int64_t)(now.h * a.group + hh) * a.o_head +
                      4 * DT * (lane >> 4);
 #pragma unroll
@@ -777,7 +780,7 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_impl(const AttendA
   }
   if (row >= d.rows) return;
   const int grow = d.rt * rows + row, q = grow / a.group, hh = grow - q * a.group;
-  const float inv = (a.v_scale ? a.v_scale[d.h] : 1.0f) / L;
+  const float inv = (a.v_scale ? a.v_scale[d.h] : 1.0f) * a.unrest / L;
   uint16_t* op = a.out + (int64_t)(d.row0 + q) * a.o_row + (int64_t)(d.h * a.group + hh) * a.o_head +
                  4 * DT * (lane >> 4) + dt0;
 #pragma unroll

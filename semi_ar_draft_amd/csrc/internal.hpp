@@ -300,6 +300,7 @@ struct AttendArgs {
   const int32_t* K;              // nullable: gamma
   const int32_t* offs;           // nullable: b * (gamma + 1)
   float scale2;                  // scale * log2(e)
+  float unrest;                  // 1 / kRestFactor for a bf16 cache, else 1
   uint16_t* out;                 // bf16
   int64_t o_row, o_head;
   float* lse;                    // [n_rows][Hq], nullable
@@ -308,6 +309,7 @@ struct AttendArgs {
   int32_t* err;
 };
 constexpr int kAttendThreads = 256;
+constexpr float kRestFactor = 1.0f + 0x1p-16f;   // of a weight's rest beside its leading bits
 constexpr int kAttendMaxGrid = 512;    // workgroups: one per CU
 constexpr size_t kAttendJoinBytes = kAttendMaxGrid * sizeof(AttendJoin);
 constexpr size_t kAttendPartBytes = kAttendMaxGrid * 2 * 8320 * sizeof(float);   // 16 mt (d + 2) <= 64 * 130
