@@ -531,7 +531,8 @@ int dspark_pages_commit(dspark_ctx* ctx, hipStream_t stream, int B, int page_siz
  * k / k_scale[head] (ties to even, magnitudes above 448 become 448; NaN
  * stays), a single rounding of the exact quotient; k_scale, v_scale float
  * [heads], positive and normal, or NULL for 1; they must be NULL for BF16.
- * One launch (timing class DSPARK_K_CACHE).  Errors: DSPARK_EINVAL. */
+ * k and v may not overlap the caches.  One launch (timing class
+ * DSPARK_K_CACHE).  Errors: DSPARK_EINVAL. */
 int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
                        const void* k, int64_t k_stride_row, int64_t k_stride_head,
                        const void* v, int64_t v_stride_row, int64_t v_stride_head,

@@ -11,7 +11,7 @@
 //
 // Work: a tile is the rows of one request that share a cache head (rows times
 // heads per group, 16 MT of them at a time, so that a key is read once for
-// all of them) over the request's tokens in steps of 32.  All tiles of the
+// all of a tile) over the request's tokens in steps of 32.  All tiles of the
 // batch stand in one line, request by request, each as long as its steps and
 // what it costs besides them, and every wave takes an equal stretch of the
 // line, so that ragged lengths load the chip evenly without the host knowing
@@ -37,12 +37,13 @@
 // key, value or score passes through LDS.
 //
 // Measured: 128 requests of 64 to 8192 tokens, up to 8 rows, 32 query and 8
-// cache heads of 128, 106 us and 6 for the second launch (537 MB, each key and
-// value read once; 6.1 TB/s on 64 requests of 8192), bound by memory; 6
-// requests of 60000 to 131000 tokens in e4m3, 64 rows a tile, 99 and 11 us,
-// bound by the issue of vector instructions (255 and 64 matrix ones a step);
-// 48 draft blocks of 7 positions, heads of 64, 19 and 4 us, bound by the
-// latency of finding a stretch and its first keys.
+// cache heads of 128, 107 us and 6 for the second launch (537 MB, each key and
+// value read once; 6.1 TB/s on 64 requests of 8192), bound by memory, with heads
+// of 256 both launches 214 (5.0 TB/s), in e4m3 138 (4.0); 6 requests of 60000 to
+// 131000 tokens in e4m3, 64 rows a tile, 105 and 11 us, bound by the issue of
+// vector instructions (about 255, and 64 matrix ones, a step); 48 draft blocks
+// of 7 positions, heads of 64, 19.5 and 4 us, bound by the latency of finding a
+// stretch and its first keys.
 #include "common.hpp"
 #include "internal.hpp"
 
@@ -378,9 +379,9 @@ struct Tile {
     // 2^-15 of it at most (rounded to one, 2^-8 of it, they cost as much as the
     // rounding of the result does).  The rest is that of 1 + 2^-16 times the
     // weight (a.unrest takes the factor out of the result): positive wherever
-    // the weight is, since 0 times an infinite value is NaN.  e4m3 values are exact in f16, whose 11
-    // bits leave 2^-11 of a weight, far below the rounding of the values that
-    // such a cache holds.
+    // the weight is, since 0 times an infinite value is NaN.  e4m3 values are
+    // exact in f16, whose 11 bits leave 2^-11 of a weight, far below the
+    // rounding of the values that such a cache holds.
     uint4 p[MT], rest[E4M3 ? 1 : MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {

@@ -5,8 +5,8 @@
 // rows by the launch).  A thread owns 16 bytes of the key cache and of the
 // value cache, so both tensors' loads are in flight together, and consecutive
 // threads write consecutive bytes of a token's head.  Measured: 16381 rows of 8
-// heads of 128 into e4m3, 101 MB, 24.1 us (4.2 TB/s, a copy reaches 4.8); a
-// step's rows of 128 requests 2.9 us.
+// heads of 128 into e4m3, 101 MB, 24.4 us (4.1 TB/s, a copy reaches 4.8); a
+// step's rows of 128 requests 3.3 us.
 #include "common.hpp"
 #include "internal.hpp"
 

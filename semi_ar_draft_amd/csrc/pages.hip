@@ -9,8 +9,8 @@
 // waits for another and a row costs one search in LDS and one load behind it.
 // Arrays that may be updated in place (held, n_free, len) are written by the
 // last workgroup to finish, after every other has read them.  Measured, of
-// which a launch of nothing takes 2 to 3: reserve 3.2 us for one request, 5.8
-// for 512 requests and 3300 rows; commit 2.8 for 9 requests, 5.6 for 512.
+// which a launch of nothing takes 2 to 3: reserve 3.3 us for one request, 5.9
+// for 512 requests and 3300 rows; commit 3.0 for 9 requests, 5.7 for 512.
 #include "common.hpp"
 #include "internal.hpp"
 
