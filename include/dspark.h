@@ -73,9 +73,11 @@ enum {
 };
 
 /* Element types: of the Markov head's weights (F32, BF16), of logits to
- * constrain (F32, BF16) and of a key-value cache (BF16, or E4M3: 8 bits, 4 of
- * exponent and 3 of mantissa, largest value 448, no infinities). */
-typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_E4M3 = 2 } dspark_dtype;
+ * constrain (F32, BF16) and of a key-value cache (BF16; E4M3: 8 bits, 4 of
+ * exponent and 3 of mantissa, largest value 448, no infinities; or MXFP4, the
+ * Open Compute Project's microscaling format: 4 bits a value, e2m1, 0, 0.5,
+ * 1, 1.5, 2, 3, 4 or 6 and a sign, and a power of two for 32 values). */
+typedef enum { DSPARK_F32 = 0, DSPARK_BF16 = 1, DSPARK_E4M3 = 2, DSPARK_MXFP4 = 3 } dspark_dtype;
 
 /* Library ABI version (major * 100 + minor). */
 int dspark_version(void);
@@ -100,7 +102,7 @@ const char* dspark_last_error(const dspark_ctx* ctx);
 /* Synchronise `stream`, read and clear the device error flag.  Returns
  * DSPARK_EDEVICE if any kernel since the last check met an out-of-range
  * token id, verify length or accepted length, a bad candidate temperature
- * (dspark_sts_fit), a page, length, slot or row outside its array (the
+ * (dspark_sts_fit), a page, length, slot, position or row outside its array (the
  * calls over a paged cache), or a grid barrier of the whole-draft kernel
  * gave up waiting (see dspark_draft_markov; the message names which),
  * DSPARK_EHIP on a HIP error, else DSPARK_OK. */
@@ -139,10 +141,11 @@ enum {
   DSPARK_K_VERIFY_CHAIN = 13,  /* verify chain: every needed target row in one launch */
   DSPARK_K_CONF_MERGE = 14,    /* draft merge + confidences (dspark_draft_markov_conf) */
   DSPARK_K_PAGES = 15,         /* page bookkeeping (reserve, commit) */
-  DSPARK_K_CACHE = 16,         /* keys and values into the cache */
+  DSPARK_K_CACHE = 16,         /* keys and values into the cache, rows of it back */
   DSPARK_K_ATTEND = 17,        /* attention over the paged cache */
   DSPARK_K_CONSTRAIN = 18,     /* penalties, biases and masks on logit rows */
-  DSPARK_K_COUNT = 19
+  DSPARK_K_ROPE = 19,          /* rotary positions, into rows or into the cache */
+  DSPARK_K_COUNT = 20
 };
 int dspark_timing_enable(dspark_ctx* ctx, int enable);
 int dspark_timing_read(dspark_ctx* ctx, double* ms, int* launches);
@@ -459,7 +462,8 @@ int dspark_verify_packed(dspark_ctx* ctx, hipStream_t stream,
  * and attend:
  *     dspark_schedule -> K
  *     dspark_pages_reserve -> t_offsets, row positions and cache slots
- *     (per layer) dspark_cache_write, dspark_attend
+ *     (per layer) dspark_rope_write (or dspark_rope, dspark_cache_write),
+ *         dspark_attend
  *     dspark_constrain -> the float32 rows that verification reads
  *     dspark_verify_packed (t_offsets, K) -> accept_len
  *     dspark_pages_commit -> new lengths, surplus pages back in the pool
@@ -540,6 +544,98 @@ int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int head
                        int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
                        dspark_dtype kv_dtype, const float* k_scale, const float* v_scale);
 
+/* The same into a cache of 4 bits (MXFP4).  kcache, vcache: bytes
+ * [n_pages][page_size][heads][d / 2], two values each, the first in the low
+ * half, through page, token and head strides in bytes (multiples of 16, d / 2
+ * contiguous, either order as above).  k_power, v_power: bytes [n_pages]
+ * [heads][page_size][d / 32], contiguous whatever the order of the caches, 16-
+ * byte aligned: value i of a head is its code times 2^(power[i / 32] - 127),
+ * NaN where that byte is 255 (bytes of 253 and 254 are not written; what rows
+ * that see such a block get is not defined).
+ * With A the largest magnitude of 32 values, their power is the least 2^e with
+ * A <= 7 * 2^e, e kept within -120 .. 125, and each becomes the value nearest
+ * it (ties to the even code; larger ones, infinities too, become 6 * 2^e), so
+ * that every value of magnitude up to 7 * 2^125 is off by at most half the
+ * distance of its two neighbours.  A block with a NaN has byte 255 and codes
+ * 0.  The rows of a slot given twice may mix, a block's codes and its power
+ * too. */
+int dspark_cache_write_mxfp4(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads, int d, int page_size,
+                             int n_pages, const void* k, int64_t k_stride_row, int64_t k_stride_head,
+                             const void* v, int64_t v_stride_row, int64_t v_stride_head,
+                             const int32_t* row_slot, void* kcache, void* vcache,
+                             int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                             uint8_t* k_power, uint8_t* v_power);
+
+/* Rows of the paged cache back as bf16: k[row], v[row] take what slot
+ * row_slot[row] holds (a prefix for a prompt's next piece, tokens that move to
+ * another cache).  Rows with slot -1 are left as they are, slots outside [-1,
+ * n_pages * page_size) are flagged and their rows left; a slot may be given
+ * any number of times.  Caches, scales (E4M3) and powers (MXFP4) as the writes
+ * have them, those of other types NULL.  k, v: bf16 [n_rows][heads][d] through
+ * row and head strides (multiples of 8, 16-byte aligned).  bf16 and MXFP4
+ * values come back exactly (MXFP4: from 2^-126 on), E4M3 ones times their scale rounded
+ * to float32 and then to bf16.  k and v may not overlap each other or the
+ * caches.  One launch (timing class DSPARK_K_CACHE).  Errors: DSPARK_EINVAL. */
+int dspark_cache_read(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
+                      const int32_t* row_slot, const void* kcache, const void* vcache,
+                      int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                      dspark_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                      const uint8_t* k_power, const uint8_t* v_power,
+                      void* k, int64_t k_stride_row, int64_t k_stride_head,
+                      void* v, int64_t v_stride_row, int64_t v_stride_head);
+
+/* Rotary positions of packed rows.
+ *
+ * Row i stands at position t = row_pos[i] of its sequence (dspark_pages_reserve
+ * gives them).  Of every head's d values the first rot are turned in pairs by
+ * the angles a = t * freq[j], j < rot / 2:
+ *     x0' = factor * (x0 cos a - x1 sin a),  x1' = factor * (x1 cos a + x0 sin a)
+ * with (x0, x1) values j and j + rot / 2 of the head (interleaved = 0) or 2 j
+ * and 2 j + 1 (interleaved != 0); the others stay as they are.  freq: double
+ * [rot / 2] on the device, radians a position: theta^(-2 j / rot) for a base
+ * theta, stretched as a long context asks (linear: over the stretch s; a base
+ * of theta s^(rot / (rot - 2)); or a mixture of freq and freq / s by how often
+ * a pair turns within the trained length, with factor = 0.1 ln s + 1); factor:
+ * finite, 1 where nothing scales the result.  Angles, sines and cosines are
+ * float64, the products float32, the results bf16.
+ * q, k: bf16 [n_rows][heads_q], [n_rows][heads] rows of d values through row
+ * and head strides (multiples of 8, 16-byte aligned); q_out, k_out likewise,
+ * each either the input itself with equal strides, or apart from every input.
+ * heads_q or heads may be 0 (no queries, no keys: NULL).  Rows of position -1
+ * are left as they are; positions below are flagged and their rows left.
+ * d: a multiple of 8 in 16..1024; rot: a multiple of 16 in 16..d; heads_q +
+ * heads <= 8192.  One launch (timing class DSPARK_K_ROPE), no workspace.
+ * Errors: DSPARK_EINVAL. */
+int dspark_rope(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads_q, int heads, int d, int rot,
+                int interleaved, const int32_t* row_pos, const double* freq, float factor,
+                const void* q, int64_t q_stride_row, int64_t q_stride_head,
+                const void* k, int64_t k_stride_row, int64_t k_stride_head,
+                void* q_out, int64_t qo_stride_row, int64_t qo_stride_head,
+                void* k_out, int64_t ko_stride_row, int64_t ko_stride_head);
+
+/* The same with keys and values going into the paged cache: q_out = q turned
+ * (heads_q may be 0), and for every row with position >= 0 and slot >= 0 the
+ * cache takes k[row] turned and v[row] as it is, in one launch.  A bf16 cache
+ * holds what dspark_rope and dspark_cache_write leave there, bit for bit; for
+ * an E4M3 or MXFP4 cache keys are turned in float64 and rounded once (rounded
+ * to bf16 in between, a key may go to its second nearest value).  Slots,
+ * caches, scales and powers as the writes have them (scales: E4M3, powers:
+ * MXFP4, else NULL); a row with slot -1 has its query turned all the same; d =
+ * 64, 128 or 256.  q_out may be q with equal strides; k and v may not overlap
+ * it or the caches.  One launch (timing class DSPARK_K_ROPE), no workspace.
+ * Errors: DSPARK_EINVAL. */
+int dspark_rope_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads_q, int heads, int d, int rot,
+                      int interleaved, int page_size, int n_pages,
+                      const int32_t* row_pos, const int32_t* row_slot, const double* freq, float factor,
+                      const void* q, int64_t q_stride_row, int64_t q_stride_head,
+                      void* q_out, int64_t qo_stride_row, int64_t qo_stride_head,
+                      const void* k, int64_t k_stride_row, int64_t k_stride_head,
+                      const void* v, int64_t v_stride_row, int64_t v_stride_head,
+                      void* kcache, void* vcache,
+                      int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                      dspark_dtype kv_dtype, const float* k_scale, const float* v_scale,
+                      uint8_t* k_power, uint8_t* v_power);
+
 /* Attention of packed rows over the paged cache.
  *
  * Row i (0 .. K[b]) of request b stands at t_offsets[b] + i of q and out.  For
@@ -579,6 +675,19 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
                   int page_size, int n_pages, const int32_t* table, int64_t table_stride, int max_pages,
                   const int32_t* len, const int32_t* K, const int32_t* t_offsets, int causal, float scale,
                   void* out, int64_t o_stride_row, int64_t o_stride_head, float* lse);
+
+/* The same over a cache of 4 bits (MXFP4, placed as dspark_cache_write_mxfp4
+ * has it).  Keys and values are taken exactly as bf16; weights are rounded by
+ * 2^-15 of them at most, as over a bf16 cache.  A value block with byte 255 is
+ * NaN to the rows that see its token, a key block makes their results NaN. */
+int dspark_attend_mxfp4(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads,
+                        int d, const void* q, int64_t q_stride_row, int64_t q_stride_head,
+                        const void* kcache, const void* vcache,
+                        int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                        const uint8_t* k_power, const uint8_t* v_power,
+                        int page_size, int n_pages, const int32_t* table, int64_t table_stride, int max_pages,
+                        const int32_t* len, const int32_t* K, const int32_t* t_offsets, int causal, float scale,
+                        void* out, int64_t o_stride_row, int64_t o_stride_head, float* lse);
 
 /* Penalties, biases and grammar masks on logit rows.
  *

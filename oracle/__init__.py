@@ -35,6 +35,7 @@ from .schedule import schedule, schedule_async, ScheduleResult
 from .verify import verify, VerifyResult, target_logprobs, accept_ratio, residual_weights, accept_prob
 from .step import run_step, step_lengths, StepResult
 from .paged import pages_reserve, pages_commit, e4m3_levels, to_e4m3, attend
+from .rope import rope, mxfp4_power, to_mxfp4, from_mxfp4, E2M1
 from .constrain import constrain, MASKED
 from .sts_fit import ece, labels, candidate_scores, sts_fit, StsFit
 
@@ -45,4 +46,5 @@ __all__ = [
     "VerifyResult", "target_logprobs", "accept_ratio", "residual_weights", "accept_prob", "run_step", "step_lengths",
     "StepResult", "ece", "labels", "candidate_scores", "sts_fit", "StsFit",
     "pages_reserve", "pages_commit", "e4m3_levels", "to_e4m3", "attend", "constrain", "MASKED",
+    "rope", "mxfp4_power", "to_mxfp4", "from_mxfp4", "E2M1",
 ]

@@ -11,6 +11,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import importlib
+import math
 import os
 from typing import Optional
 
@@ -20,7 +21,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libdspark.so")
 
 DSPARK_OK, DSPARK_EINVAL, DSPARK_EHIP, DSPARK_ENOMEM, DSPARK_EDEVICE = 0, 1, 2, 3, 4
-DSPARK_F32, DSPARK_BF16, DSPARK_E4M3 = 0, 1, 2
+DSPARK_F32, DSPARK_BF16, DSPARK_E4M3, DSPARK_MXFP4 = 0, 1, 2, 3
 MASKED = ctypes.c_float(-1.0e30).value  # what constrain writes where nothing is allowed
 
 EXPORTS = (
@@ -29,12 +30,13 @@ EXPORTS = (
     "dspark_confidence", "dspark_schedule", "dspark_schedule_async", "dspark_verify",
     "dspark_verify_packed", "dspark_accept_prob", "dspark_sts_fit", "dspark_stream_read",
     "dspark_pages_reserve", "dspark_pages_commit", "dspark_cache_write", "dspark_attend", "dspark_constrain",
+    "dspark_cache_write_mxfp4", "dspark_cache_read", "dspark_rope", "dspark_rope_write", "dspark_attend_mxfp4",
     "dspark_timing_enable", "dspark_timing_read", "dspark_timing_read_classes",
 )
 KERNEL_CLASSES = ("draft_sweep", "draft_combine", "confidence", "survival", "schedule",
                   "verify_rows", "verify_decide", "resid_sweep", "resid_combine", "gru", "diag", "sts_fit",
                   "draft_chain", "verify_chain", "conf_merge", "pages", "cache", "attend",
-                  "constrain")
+                  "constrain", "rope")
 
 _lib = None
 _native_module = None
@@ -126,6 +128,24 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
     lib.dspark_attend.argtypes = [
         _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _i64, _i64, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp,
         _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _f32, _vp, _i64, _i64, _vp]
+    rows = [_vp, _i64, _i64]
+    lib.dspark_cache_write_mxfp4.restype = _i32
+    lib.dspark_cache_write_mxfp4.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, *rows, *rows, _vp, _vp, _vp, _i64, _i64, _i64, _vp, _vp]
+    lib.dspark_cache_read.restype = _i32
+    lib.dspark_cache_read.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, *rows, *rows]
+    lib.dspark_rope.restype = _i32
+    lib.dspark_rope.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _f32, *rows, *rows, *rows, *rows]
+    lib.dspark_rope_write.restype = _i32
+    lib.dspark_rope_write.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _f32, *rows, *rows, *rows, *rows,
+        _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]
+    lib.dspark_attend_mxfp4.restype = _i32
+    lib.dspark_attend_mxfp4.argtypes = [
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, *rows, _vp, _vp, _i64, _i64, _i64, _vp, _vp,
+        _i32, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i32, _f32, *rows, _vp]
     lib.dspark_constrain.restype = _i32
     lib.dspark_constrain.argtypes = [
         _vp, _vp, _i32, _i32, _i32, _vp, _i32, _i64, _i64, _vp, _vp, _i32, _vp, _i64, _i32, _vp, _vp, _vp, _i64,
@@ -195,6 +215,61 @@ def _compiled():
             raise RuntimeError("the binding's compiled part is not built; run `python -m semi_ar_draft_amd.build`") from e
         _native_module = module
     return _native_module
+
+
+_FOUR_BITS = (torch.uint8, torch.float4_e2m1fn_x2)
+
+
+def rope_frequencies(rot: int, theta: float = 10000.0, scaling: Optional[str] = None, stretch: float = 1.0,
+                     trained: Optional[int] = None, slow: float = 1.0, fast: Optional[float] = None, device=None):
+    """Frequencies of rotary positions and their factor, for ``rope`` and
+    ``rope_write``: (float64 [rot / 2] radians a position, factor).
+
+    theta^(-2 j / rot) for pair j, and for a context ``stretch`` times as long
+    as the one a model was trained with:
+      "linear"  every frequency over stretch
+      "ntk"     a base of theta * stretch^(rot / (rot - 2)): the fastest pair
+                stays, the slowest is stretched
+      "parts"   pairs that turn at least ``fast`` (4) times within ``trained``
+                positions stay, those that turn at most ``slow`` (1) times are
+                stretched, those between mixed linearly in their turns
+      "yarn"    the same mixed linearly in j, between the pairs (rounded
+                outwards) that turn ``fast`` (32) and ``slow`` (1) times, and
+                a factor of 0.1 ln stretch + 1
+    """
+    if rot < 2 or rot % 2:
+        raise ValueError(f"rot must be even and positive, got {rot}")
+    if not (theta > 1.0 and math.isfinite(theta)) or not (stretch >= 1.0 and math.isfinite(stretch)):
+        raise ValueError("theta must be above 1, stretch at least 1, both finite")
+    if scaling not in (None, "linear", "ntk", "parts", "yarn"):
+        raise ValueError(f"scaling must be None, 'linear', 'ntk', 'parts' or 'yarn', got {scaling!r}")
+    if scaling is None and stretch != 1.0:
+        raise ValueError("a stretch needs a scaling")
+    j = torch.arange(rot // 2, dtype=torch.float64)
+    base, factor = theta, 1.0
+    if scaling == "ntk":
+        if rot < 4:
+            raise ValueError("'ntk' needs at least two pairs")
+        base = theta * stretch ** (rot / (rot - 2))
+    freq = torch.exp(j * (-2.0 * math.log(base) / rot))
+    if scaling == "linear":
+        freq = freq / stretch
+    elif scaling in ("parts", "yarn"):
+        if trained is None or trained < 1:
+            raise ValueError(f"'{scaling}' needs the trained length")
+        fast = (4.0 if scaling == "parts" else 32.0) if fast is None else fast
+        if not 0.0 < slow < fast:
+            raise ValueError("slow and fast must be positive, slow below fast")
+        if scaling == "parts":
+            keep = ((trained * freq / (2 * math.pi) - slow) / (fast - slow)).clamp(0, 1)
+        else:
+            def pair_of(turns):
+                return rot * math.log(trained / (turns * 2 * math.pi)) / (2 * math.log(theta))
+            lo, hi = max(0, math.floor(pair_of(fast))), min(rot - 1, math.ceil(pair_of(slow)))
+            keep = 1 - ((j - lo) / max(hi - lo, 1e-3)).clamp(0, 1)
+            factor = 0.1 * math.log(stretch) + 1.0
+        freq = freq * keep + freq / stretch * (1 - keep)
+    return freq.to(device), factor
 
 
 class Context:
@@ -603,15 +678,71 @@ class Context:
         """Rows k, v (bf16 [n_rows][heads][d]) into their slots of the caches
         ([n_pages][page_size][heads][d], bf16 or float8_e4m3fn with a scale per
         head; any order of pages, tokens and heads in memory that the strides
-        describe)."""
+        describe).  A 4-bit cache (MXFP4) is uint8 (or float4_e2m1fn_x2)
+        [n_pages][page_size][heads][d / 2], two values a byte, with the powers
+        of two of its blocks of 32 in k_scale and v_scale: uint8 (or
+        float8_e8m0fnu) [n_pages][heads][page_size][d / 32], contiguous, which
+        are written too."""
         self._rc(self._native.cache_write(self._h.value, self.device.index, _stream(self.device, stream), kcache, vcache,
                                           k_scale, v_scale, k, v, row_slot))
+
+    # -- dspark_cache_read ------------------------------------------------------------
+    def cache_read(self, kcache, vcache, row_slot, k_scale=None, v_scale=None, out=None, stream=None):
+        """What the caches (bf16, float8_e4m3fn or mxfp4, with their scales as
+        cache_write has them) hold in the slots row_slot (int32 [n_rows], -1: none), as bf16
+        [n_rows][heads][d].  Returns (k, v), or ``out``; rows of slot -1 are
+        left as they are (new ones hold zeros there)."""
+        dev = self.device
+        if out is None:
+            d = kcache.shape[-1] * (2 if kcache.dtype in _FOUR_BITS else 1)
+            with _on(stream):
+                out = tuple(torch.zeros((row_slot.shape[0], kcache.shape[2], d), dtype=torch.bfloat16, device=dev)
+                            for _ in range(2))
+        k, v = out
+        self._rc(self._native.cache_read(self._h.value, dev.index, _stream(dev, stream), kcache, vcache, k_scale, v_scale,
+                                         row_slot, k, v))
+        return k, v
+
+    # -- dspark_rope ------------------------------------------------------------------
+    def rope(self, q, k, row_pos, freq, interleaved: bool = False, factor: float = 1.0, q_out=None, k_out=None,
+             stream=None):
+        """Rows q and k (bf16 [n_rows][heads_q or heads][d]; either may be None)
+        turned by their positions row_pos (int32 [n_rows], -1: none): the first
+        2 len(freq) values of every head, in pairs (j, j + len(freq)) or
+        (2 j, 2 j + 1), by row_pos * freq[j] radians (freq float64, see
+        rope_frequencies), times factor.  q_out and k_out may be q and k
+        themselves.  Returns (q_out, k_out); rows of position -1 are left as
+        they are (new ones hold zeros there)."""
+        dev = self.device
+        with _on(stream):
+            if q is not None and q_out is None:
+                q_out = torch.zeros(q.shape, dtype=torch.bfloat16, device=dev)
+            if k is not None and k_out is None:
+                k_out = torch.zeros(k.shape, dtype=torch.bfloat16, device=dev)
+        self._rc(self._native.rope(self._h.value, dev.index, _stream(dev, stream), freq, interleaved, factor, row_pos,
+                                   k, k_out, q, q_out))
+        return q_out, k_out
+
+    # -- dspark_rope_write ------------------------------------------------------------
+    def rope_write(self, q, k, v, row_pos, row_slot, freq, kcache, vcache, k_scale=None, v_scale=None,
+                   interleaved: bool = False, factor: float = 1.0, q_out=None, stream=None):
+        """rope with the turned keys, and the values v, going into their slots of
+        the caches (as cache_write has them) in the same launch; q may be None.
+        Returns q_out."""
+        dev = self.device
+        if q is not None and q_out is None:
+            with _on(stream):
+                q_out = torch.zeros(q.shape, dtype=torch.bfloat16, device=dev)
+        self._rc(self._native.rope_write(self._h.value, dev.index, _stream(dev, stream), kcache, vcache, k_scale, v_scale,
+                                         freq, interleaved, factor, row_pos, row_slot, k, v, q, q_out))
+        return q_out
 
     # -- dspark_attend ----------------------------------------------------------------
     def attend(self, q, kcache, vcache, table, length, gamma: int, K=None, t_offsets=None, causal: bool = True,
                scale: Optional[float] = None, k_scale=None, v_scale=None, out=None, lse=None, stream=None):
         """Attention of the packed rows q (bf16 [n_rows][heads_q][d]) over the
-        paged cache ([n_pages][page_size][heads][d]).  Request b has K[b] + 1
+        paged cache ([n_pages][page_size][heads][d], bf16, float8_e4m3fn or
+        mxfp4 as cache_write has them).  Request b has K[b] + 1
         rows (gamma + 1 where K is None) from t_offsets[b] on (b * (gamma + 1)
         where None).  scale defaults to d ** -0.5.  Returns out (bf16, q's
         shape; rows of no request are left as they are); ``lse``: a float32
@@ -697,4 +828,4 @@ class Context:
 
 __all__ = ["Context", "DSparkError", "load_library", "LIB_PATH", "EXPORTS", "KERNEL_CLASSES",
            "DSPARK_OK", "DSPARK_EINVAL", "DSPARK_EHIP", "DSPARK_ENOMEM", "DSPARK_EDEVICE",
-           "DSPARK_F32", "DSPARK_BF16", "DSPARK_E4M3", "MASKED"]
+           "DSPARK_F32", "DSPARK_BF16", "DSPARK_E4M3", "DSPARK_MXFP4", "MASKED", "rope_frequencies"]

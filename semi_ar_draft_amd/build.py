@@ -20,7 +20,7 @@ BUILD_DIR = os.path.join(ROOT, "_build")
 LIB_PATH = os.path.join(HERE, "libdspark.so")
 NATIVE_PATH = os.path.join(HERE, "_native.so")
 SOURCES = ["api.hip", "sweep.hip", "verify.hip", "confidence.hip", "schedule.hip", "gru.hip", "sts.hip",
-           "stream.hip", "pages.hip", "cache.hip", "attend.hip", "constrain.hip"]
+           "stream.hip", "pages.hip", "cache.hip", "rope.hip", "attend.hip", "constrain.hip"]
 ARCH = os.environ.get("DSPARK_OFFLOAD_ARCH", "gfx950")
 
 COMMON_FLAGS = [

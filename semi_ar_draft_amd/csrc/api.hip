@@ -1187,10 +1187,11 @@ int check_cache(dspark_ctx* c, int heads, int d, int page_size, const void* kc, 
                 int64_t c_tok, int64_t c_head, int kv_dtype) {
   if (heads < 1 || heads > 1024) return fail(c, DSPARK_EINVAL, "cache heads must be in 1..1024 (got %d)", heads);
   if (d != 64 && d != 128 && d != 256) return fail(c, DSPARK_EINVAL, "head size must be 64, 128 or 256 (got %d)", d);
-  if (kv_dtype != DSPARK_BF16 && kv_dtype != DSPARK_E4M3)
-    return fail(c, DSPARK_EINVAL, "the cache must be bf16 or e4m3");
+  if (kv_dtype != DSPARK_BF16 && kv_dtype != DSPARK_E4M3 && kv_dtype != DSPARK_MXFP4)
+    return fail(c, DSPARK_EINVAL, "the cache must be bf16, e4m3 or mxfp4");
   if (!kc || !vc) return fail(c, DSPARK_EINVAL, "null pointer argument");
-  const int64_t step = kv_dtype == DSPARK_E4M3 ? 16 : 8;
+  const int64_t step = kv_dtype == DSPARK_BF16 ? 8 : 16;
+  if (kv_dtype == DSPARK_MXFP4) d /= 2;                  // strides count bytes of two values
   if (!aligned16(kc) || !aligned16(vc) || c_page % step || c_tok % step || c_head % step)
     return fail(c, DSPARK_EINVAL, "the caches must be 16-byte aligned, their strides multiples of 16 bytes");
   if (c_tok > INT32_MAX / 32 || c_head > INT64_MAX >> 16 || c_page > INT64_MAX >> 16)
@@ -1199,6 +1200,248 @@ int check_cache(dspark_ctx* c, int heads, int d, int page_size, const void* kc, 
   const bool head_major = c_tok >= d && c_head >= page_size * c_tok && c_page >= heads * c_head;
   if (!tok_major && !head_major) return fail(c, DSPARK_EINVAL, "cache strides overlap");
   return DSPARK_OK;
+}
+
+// A cache's element type, and its scales or powers as the type needs them.
+int cache_type(int kv_dtype) {
+  return kv_dtype == DSPARK_MXFP4 ? kCacheMxfp4 : kv_dtype == DSPARK_E4M3 ? kCacheE4m3 : kCacheBf16;
+}
+
+int check_scales(dspark_ctx* c, int kv_dtype, const float* k_scale, const float* v_scale, const uint8_t* k_power,
+                 const uint8_t* v_power) {
+  if (kv_dtype != DSPARK_E4M3 && (k_scale || v_scale)) return fail(c, DSPARK_EINVAL, "scales belong to an e4m3 cache");
+  if (kv_dtype != DSPARK_MXFP4) {
+    if (k_power || v_power) return fail(c, DSPARK_EINVAL, "powers belong to an mxfp4 cache");
+    return DSPARK_OK;
+  }
+  if (!k_power || !v_power) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  if (!aligned16(k_power) || !aligned16(v_power) || k_power == v_power)
+    return fail(c, DSPARK_EINVAL, "the powers must be two 16-byte aligned arrays");
+  return DSPARK_OK;
+}
+
+// bf16 rows [n_rows][heads][d] through a row and a head stride.
+int check_rows(dspark_ctx* c, const char* name, const void* p, int64_t s_row, int64_t s_head) {
+  if (!p) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  if (!aligned16(p) || (s_row & 7) || (s_head & 7) || s_row < 0 || s_head < 0)
+    return fail(c, DSPARK_EINVAL, "%s must be 16-byte aligned, its strides multiples of 8", name);
+  return DSPARK_OK;
+}
+
+// Rows that are written: those and their heads that are there more than once must not overlap.
+int check_out_rows(dspark_ctx* c, const char* name, const void* p, int n_rows, int heads, int d, int64_t s_row,
+                   int64_t s_head) {
+  if (int rc = check_rows(c, name, p, s_row, s_head)) return rc;
+  const bool row_major = (heads == 1 || s_head >= d) && (n_rows == 1 || s_row >= (heads == 1 ? d : heads * s_head));
+  const bool head_major = (n_rows == 1 || s_row >= d) && (heads == 1 || s_head >= (n_rows == 1 ? d : n_rows * s_row));
+  if (!row_major && !head_major) return fail(c, DSPARK_EINVAL, "%s strides overlap", name);
+  return DSPARK_OK;
+}
+
+int check_slots(dspark_ctx* c, int page_size, int n_pages) {
+  const int sh = page_shift(page_size);
+  if (sh < 0) return fail(c, DSPARK_EINVAL, "page_size must be a power of two in 8..1024 (got %d)", page_size);
+  if (n_pages < 1 || n_pages > (INT32_MAX >> sh))
+    return fail(c, DSPARK_EINVAL, "n_pages must be >= 1 and n_pages * page_size < 2^31");
+  return DSPARK_OK;
+}
+
+// 2^32 / d rounded up, as the kernels divide by it.
+unsigned inverse(unsigned d) { return d <= 1 ? 0u : (unsigned)(((1ull << 32) + d - 1) / d); }
+
+// What the calls with rotary positions share: their checks and arguments.
+int rope_args(dspark_ctx* c, RopeArgs& a, int n_rows, int heads_q, int heads, int d, int rot, const int32_t* row_pos,
+              const double* freq, float factor, const void* q, int64_t q_row, int64_t q_head, void* q_out, int64_t qo_row,
+              int64_t qo_head) {
+  if (n_rows < 0) return fail(c, DSPARK_EINVAL, "n_rows must be >= 0");
+  if (heads_q < 0 || heads < 0 || heads_q + (int64_t)heads > 8192)
+    return fail(c, DSPARK_EINVAL, "heads_q and heads must be >= 0, together <= 8192");
+  if (rot < 16 || rot % 16 || rot > d) return fail(c, DSPARK_EINVAL, "rot must be a multiple of 16 in 16..d (got %d)", rot);
+  if (!std::isfinite(factor)) return fail(c, DSPARK_EINVAL, "factor must be finite");
+  if (n_rows == 0) return DSPARK_OK;
+  if (!row_pos || !freq) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  if (heads_q > 0) {
+    int rc = check_rows(c, "q", q, q_row, q_head);
+    if (!rc) rc = check_out_rows(c, "q_out", q_out, n_rows, heads_q, d, qo_row, qo_head);
+    if (rc) return rc;
+    if (q == q_out && ((n_rows > 1 && q_row != qo_row) || (heads_q > 1 && q_head != qo_head)))
+      return fail(c, DSPARK_EINVAL, "q_out may be q with equal strides only");
+  }
+  memset(&a, 0, sizeof(a));
+  a.n_rows = n_rows;
+  a.heads_q = heads_q;
+  a.d = d;
+  a.rot = rot;
+  a.pairs_inv = inverse(rot / 2);
+  a.pos = row_pos;
+  a.freq = freq;
+  a.factor = factor;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_row = q_row;
+  a.q_head = q_head;
+  a.qo = static_cast<uint16_t*>(q_out);
+  a.qo_row = qo_row;
+  a.qo_head = qo_head;
+  // rows of a workgroup: as many as share its sines while every CU has four workgroups
+  a.rows = std::max(1, std::min({4, n_rows / (4 * c->cu_count), kRopeTable / (rot / 2)}));
+  a.err = c->dev_err;
+  return DSPARK_OK;
+}
+
+int cache_write_common(dspark_ctx* c, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
+                       const void* k, int64_t k_stride_row, int64_t k_stride_head, const void* v,
+                       int64_t v_stride_row, int64_t v_stride_head, const int32_t* row_slot, void* kcache,
+                       void* vcache, int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                       int kv_dtype, const float* k_scale, const float* v_scale, uint8_t* k_power, uint8_t* v_power) {
+  if (int rc = check_slots(c, page_size, n_pages)) return rc;
+  const int sh = page_shift(page_size);
+  int rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype);
+  if (rc) return rc;
+  const bool e4m3 = kv_dtype == DSPARK_E4M3;
+  if ((rc = check_scales(c, kv_dtype, k_scale, v_scale, k_power, v_power))) return rc;
+  if (n_rows < 0) return fail(c, DSPARK_EINVAL, "n_rows must be >= 0");
+  if (n_rows == 0) return DSPARK_OK;
+  if (!k || !v || !row_slot) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  if (!aligned16(k) || !aligned16(v) || (k_stride_row & 7) || (k_stride_head & 7) || (v_stride_row & 7) ||
+      (v_stride_head & 7) || k_stride_row < 0 || k_stride_head < 0 || v_stride_row < 0 || v_stride_head < 0)
+    return fail(c, DSPARK_EINVAL, "k and v must be 16-byte aligned, their strides multiples of 8");
+  const int per_head = e4m3 ? d / 16 : d / 8;
+  if ((int64_t)n_rows * heads * per_head > INT32_MAX - kCacheThreads)
+    return fail(c, DSPARK_EINVAL, "too many rows (%d)", n_rows);
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
+  const int64_t size = kv_dtype == DSPARK_BF16 ? 2 : 1;
+  CacheWriteArgs a;
+  memset(&a, 0, sizeof(a));
+  a.n_slots = (int64_t)n_pages << sh;
+  a.n_rows = n_rows;
+  a.heads = heads;
+  a.chunks = heads * per_head;
+  a.chunk_shift = __builtin_ctz(per_head);
+  a.page_shift = sh;
+  a.k = static_cast<const uint16_t*>(k);
+  a.k_row = k_stride_row;
+  a.k_head = k_stride_head;
+  a.v = static_cast<const uint16_t*>(v);
+  a.v_row = v_stride_row;
+  a.v_head = v_stride_head;
+  a.slot = row_slot;
+  a.kc = static_cast<unsigned char*>(kcache);
+  a.vc = static_cast<unsigned char*>(vcache);
+  a.c_page = c_stride_page * size;
+  a.c_tok = c_stride_tok * size;
+  a.c_head = c_stride_head * size;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.k_power = k_power;
+  a.v_power = v_power;
+  a.blocks = d / 32;
+  a.s_head = (int64_t)page_size * a.blocks;
+  a.s_page = heads * a.s_head;
+  a.err = c->dev_err;
+  const int grid = (n_rows * a.chunks + kCacheThreads - 1) / kCacheThreads;
+  return klaunch(c, DSPARK_K_CACHE, cache_write_kernel(cache_type(kv_dtype)), dim3(grid), dim3(kCacheThreads), &a, stream);
+}
+
+int attend_common(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads, int d,
+                  const void* q, int64_t q_stride_row, int64_t q_stride_head, const void* kcache, const void* vcache,
+                  int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head, int kv_dtype,
+                  const float* k_scale, const float* v_scale, const uint8_t* k_power, const uint8_t* v_power, int page_size, int n_pages, const int32_t* table,
+                  int64_t table_stride, int max_pages, const int32_t* len, const int32_t* K,
+                  const int32_t* t_offsets, int causal, float scale, void* out, int64_t o_stride_row,
+                  int64_t o_stride_head, float* lse) {
+  int rc = check_pages(c, B, page_size, n_pages, max_pages, table_stride, table);
+  if (rc) return rc;
+  if ((rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype)))
+    return rc;
+  const int sh = page_shift(page_size);
+  const bool e4m3 = kv_dtype == DSPARK_E4M3;
+  if ((rc = check_scales(c, kv_dtype, k_scale, v_scale, k_power, v_power))) return rc;
+  if (gamma < 0 || gamma > kMaxGamma) return fail(c, DSPARK_EINVAL, "gamma must be in 0..%d", kMaxGamma);
+  if (n_rows < 0 || (!t_offsets && (int64_t)B * (gamma + 1) > n_rows))
+    return fail(c, DSPARK_EINVAL, "n_rows must hold B * (gamma + 1) rows where t_offsets is NULL");
+  if (n_rows == 0) return DSPARK_OK;
+  if (heads_q < 1 || heads_q % heads || heads_q / heads > 64)
+    return fail(c, DSPARK_EINVAL, "heads_q must be 1 to 64 times heads (got %d, %d)", heads_q, heads);
+  if (!q || !out || !len) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  if (!aligned16(q) || !aligned16(out) || (q_stride_row & 7) || (q_stride_head & 7) || (o_stride_row & 7) ||
+      (o_stride_head & 7) || q_stride_row < 0 || q_stride_head < 0 || o_stride_row < 0 || o_stride_head < 0)
+    return fail(c, DSPARK_EINVAL, "q and out must be 16-byte aligned, their strides multiples of 8");
+  // rows and heads of the result that are there more than once must not overlap
+  const bool row_major = (heads_q == 1 || o_stride_head >= d) &&
+                         (n_rows == 1 || o_stride_row >= (heads_q == 1 ? d : heads_q * o_stride_head));
+  const bool head_major = (n_rows == 1 || o_stride_row >= d) &&
+                          (heads_q == 1 || o_stride_head >= (n_rows == 1 ? d : n_rows * o_stride_row));
+  if (!row_major && !head_major) return fail(c, DSPARK_EINVAL, "out strides overlap");
+  // (several workgroups may read a row of q while one of them writes its result)
+  if (out == q) return fail(c, DSPARK_EINVAL, "out may not be q");
+  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(c, DSPARK_EINVAL, "scale must be positive and finite");
+  // the fewest 16-row blocks that hold a request's rows of one cache head, up
+  // to 64 rows (d = 256: 32, its sums fill the registers): a tile reads its keys
+  // once for all of them, and unused blocks cost products and registers (blocks
+  // of 1 / the rule / 4: 181 / 117 / 126 us for 32 rows a cache head, 349 / 141 /
+  // 140 for 64, 23.6 / 23.6 / 29 for 7)
+  const int group = heads_q / heads, most = group * (gamma + 1);
+  const int mt = most <= 16 ? 1 : most <= 32 || d == 256 ? 2 : 4;
+  const int64_t tiles = (most + 16 * mt - 1) / (16 * mt);
+  const int64_t tokens = (int64_t)max_pages << sh;
+  if (tokens > INT32_MAX - 4096 || heads * tiles * (tokens / 32 + 64) > INT32_MAX)
+    return fail(c, DSPARK_EINVAL, "max_pages * page_size is too large");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
+  if (!c->attend_buf) {
+    if (hipMalloc(&c->attend_buf, kAttendJoinBytes + kAttendPartBytes) != hipSuccess) {
+      (void)hipGetLastError();
+      c->attend_buf = nullptr;
+      return fail(c, DSPARK_ENOMEM, "allocation of %zu bytes failed", kAttendJoinBytes + kAttendPartBytes);
+    }
+  }
+  const void* fn = attend_kernel(d, mt, cache_type(kv_dtype));
+  const int grid = std::min(kAttendMaxGrid, c->cu_count);
+  AttendArgs a;
+  memset(&a, 0, sizeof(a));
+  const int64_t size = kv_dtype == DSPARK_BF16 ? 2 : 1;
+  a.B = B;
+  a.n_rows = n_rows;
+  a.gamma = gamma;
+  a.Hq = heads_q;
+  a.Hkv = heads;
+  a.group = group;
+  a.page_shift = sh;
+  a.n_pages = n_pages;
+  a.cols = max_pages;
+  a.causal = causal != 0;
+  a.rows = 16 * mt;
+  a.q = static_cast<const uint16_t*>(q);
+  a.q_row = q_stride_row;
+  a.q_head = q_stride_head;
+  a.kc = static_cast<const unsigned char*>(kcache);
+  a.vc = static_cast<const unsigned char*>(vcache);
+  a.c_page = c_stride_page * size;
+  a.c_tok = c_stride_tok * size;
+  a.c_head = c_stride_head * size;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.k_power = k_power;
+  a.v_power = v_power;
+  a.s_head = (int64_t)page_size * (d / 32);
+  a.s_page = heads * a.s_head;
+  a.table = table;
+  a.tstride = table_stride;
+  a.len = len;
+  a.K = K;
+  a.offs = t_offsets;
+  a.scale2 = scale * kLog2e;
+  a.unrest = e4m3 ? 1.0f : 1.0f / kRestFactor;
+  a.out = static_cast<uint16_t*>(out);
+  a.o_row = o_stride_row;
+  a.o_head = o_stride_head;
+  a.lse = lse;
+  a.joins = reinterpret_cast<AttendJoin*>(c->attend_buf);
+  a.part = reinterpret_cast<float*>(c->attend_buf + kAttendJoinBytes);
+  a.err = c->dev_err;
+  if ((rc = klaunch(c, DSPARK_K_ATTEND, fn, dim3(grid), dim3(kAttendThreads), &a, stream))) return rc;
+  return klaunch(c, DSPARK_K_ATTEND, attend_join_kernel(d), dim3(grid, mt), dim3(kAttendThreads), &a, stream);
 }
 
 }  // namespace
@@ -1394,7 +1637,7 @@ int dspark_check(dspark_ctx* c, hipStream_t stream) {
   DSPARK_HIP(c, hipMemcpy(&flag, c->dev_err, sizeof(flag), hipMemcpyDeviceToHost));
   if (flag) {
     DSPARK_HIP(c, hipMemset(c->dev_err, 0, sizeof(int32_t)));
-    return fail(c, DSPARK_EDEVICE, "device error flag 0x%x:%s%s%s%s%s%s%s%s%s%s%s%s%s", flag,
+    return fail(c, DSPARK_EDEVICE, "device error flag 0x%x:%s%s%s%s%s%s%s%s%s%s%s%s%s%s", flag,
                 (flag & kErrToken) ? " token id out of range" : "",
                 (flag & kErrK) ? " verify length out of range" : "",
                 (flag & kErrRow) ? " packed target row out of range" : "",
@@ -1406,7 +1649,8 @@ int dspark_check(dspark_ctx* c, hipStream_t stream) {
                 (flag & kErrSlot) ? " cache slot out of range" : "",
                 (flag & kErrHist) ? " history or bias length out of range" : "",
                 (flag & kErrBias) ? " bias ids not ascending" : "",
-                (flag & kErrPenalty) ? " repetition penalty not positive, normal and finite" : "");
+                (flag & kErrPenalty) ? " repetition penalty not positive, normal and finite" : "",
+                (flag & kErrPos) ? " row position out of range" : "");
   }
   c->err.clear();
   return DSPARK_OK;
@@ -1812,34 +2056,154 @@ int dspark_cache_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads,
                        dspark_dtype kv_dtype, const float* k_scale, const float* v_scale) {
   TraceRange trace_range("dspark_cache_write");
   if (!c) return DSPARK_EINVAL;
-  const int sh = page_shift(page_size);
-  if (sh < 0) return fail(c, DSPARK_EINVAL, "page_size must be a power of two in 8..1024 (got %d)", page_size);
-  if (n_pages < 1 || n_pages > (INT32_MAX >> sh))
-    return fail(c, DSPARK_EINVAL, "n_pages must be >= 1 and n_pages * page_size < 2^31");
-  int rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype);
+  if (kv_dtype == DSPARK_MXFP4) return fail(c, DSPARK_EINVAL, "an mxfp4 cache is written by dspark_cache_write_mxfp4");
+  return cache_write_common(c, stream, n_rows, heads, d, page_size, n_pages, k, k_stride_row, k_stride_head, v,
+                            v_stride_row, v_stride_head, row_slot, kcache, vcache, c_stride_page, c_stride_tok,
+                            c_stride_head, kv_dtype, k_scale, v_scale, nullptr, nullptr);
+}
+
+int dspark_cache_write_mxfp4(dspark_ctx* c, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
+                             const void* k, int64_t k_stride_row, int64_t k_stride_head, const void* v,
+                             int64_t v_stride_row, int64_t v_stride_head, const int32_t* row_slot, void* kcache,
+                             void* vcache, int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                             uint8_t* k_power, uint8_t* v_power) {
+  TraceRange trace_range("dspark_cache_write_mxfp4");
+  if (!c) return DSPARK_EINVAL;
+  return cache_write_common(c, stream, n_rows, heads, d, page_size, n_pages, k, k_stride_row, k_stride_head, v,
+                            v_stride_row, v_stride_head, row_slot, kcache, vcache, c_stride_page, c_stride_tok,
+                            c_stride_head, DSPARK_MXFP4, nullptr, nullptr, k_power, v_power);
+}
+
+int dspark_cache_read(dspark_ctx* c, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
+                      const int32_t* row_slot, const void* kcache, const void* vcache, int64_t c_stride_page,
+                      int64_t c_stride_tok, int64_t c_stride_head, dspark_dtype kv_dtype, const float* k_scale,
+                      const float* v_scale, const uint8_t* k_power, const uint8_t* v_power, void* k,
+                      int64_t k_stride_row, int64_t k_stride_head, void* v, int64_t v_stride_row,
+                      int64_t v_stride_head) {
+  TraceRange trace_range("dspark_cache_read");
+  if (!c) return DSPARK_EINVAL;
+  int rc = check_slots(c, page_size, n_pages);
   if (rc) return rc;
-  const bool e4m3 = kv_dtype == DSPARK_E4M3;
-  if (!e4m3 && (k_scale || v_scale)) return fail(c, DSPARK_EINVAL, "scales belong to an e4m3 cache");
+  if ((rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype)))
+    return rc;
+  if ((rc = check_scales(c, kv_dtype, k_scale, v_scale, k_power, v_power))) return rc;
   if (n_rows < 0) return fail(c, DSPARK_EINVAL, "n_rows must be >= 0");
   if (n_rows == 0) return DSPARK_OK;
-  if (!k || !v || !row_slot) return fail(c, DSPARK_EINVAL, "null pointer argument");
-  if (!aligned16(k) || !aligned16(v) || (k_stride_row & 7) || (k_stride_head & 7) || (v_stride_row & 7) ||
-      (v_stride_head & 7) || k_stride_row < 0 || k_stride_head < 0 || v_stride_row < 0 || v_stride_head < 0)
-    return fail(c, DSPARK_EINVAL, "k and v must be 16-byte aligned, their strides multiples of 8");
-  const int per_head = e4m3 ? d / 16 : d / 8;
-  if ((int64_t)n_rows * heads * per_head > INT32_MAX - kCacheThreads)
+  if (!row_slot) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  if ((rc = check_out_rows(c, "k", k, n_rows, heads, d, k_stride_row, k_stride_head))) return rc;
+  if ((rc = check_out_rows(c, "v", v, n_rows, heads, d, v_stride_row, v_stride_head))) return rc;
+  if (k == v || k == kcache || k == vcache || v == kcache || v == vcache)
+    return fail(c, DSPARK_EINVAL, "k, v and the caches must be different arrays");
+  if ((int64_t)n_rows * heads * (d / 8) > INT32_MAX - kCacheThreads)
     return fail(c, DSPARK_EINVAL, "too many rows (%d)", n_rows);
   DeviceGuard dg(c->device);
   if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
-  const int64_t size = e4m3 ? 1 : 2;
-  CacheWriteArgs a;
+  const int sh = page_shift(page_size);
+  const int64_t size = kv_dtype == DSPARK_BF16 ? 2 : 1;
+  CacheReadArgs a;
   memset(&a, 0, sizeof(a));
   a.n_slots = (int64_t)n_pages << sh;
   a.n_rows = n_rows;
-  a.heads = heads;
-  a.chunks = heads * per_head;
-  a.chunk_shift = __builtin_ctz(per_head);
+  a.chunks = heads * (d / 8);
+  a.chunk_shift = __builtin_ctz(d / 8);
   a.page_shift = sh;
+  a.slot = row_slot;
+  a.kc = static_cast<const unsigned char*>(kcache);
+  a.vc = static_cast<const unsigned char*>(vcache);
+  a.c_page = c_stride_page * size;
+  a.c_tok = c_stride_tok * size;
+  a.c_head = c_stride_head * size;
+  a.k_scale = k_scale;
+  a.v_scale = v_scale;
+  a.k_power = k_power;
+  a.v_power = v_power;
+  a.blocks = d / 32;
+  a.s_head = (int64_t)page_size * a.blocks;
+  a.s_page = heads * a.s_head;
+  a.k = static_cast<uint16_t*>(k);
+  a.k_row = k_stride_row;
+  a.k_head = k_stride_head;
+  a.v = static_cast<uint16_t*>(v);
+  a.v_row = v_stride_row;
+  a.v_head = v_stride_head;
+  a.err = c->dev_err;
+  const int grid = (n_rows * a.chunks + kCacheThreads - 1) / kCacheThreads;
+  return klaunch(c, DSPARK_K_CACHE, cache_read_kernel(cache_type(kv_dtype)), dim3(grid), dim3(kCacheThreads), &a, stream);
+}
+
+int dspark_rope(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q, int heads, int d, int rot, int interleaved,
+                const int32_t* row_pos, const double* freq, float factor, const void* q, int64_t q_stride_row,
+                int64_t q_stride_head, const void* k, int64_t k_stride_row, int64_t k_stride_head, void* q_out,
+                int64_t qo_stride_row, int64_t qo_stride_head, void* k_out, int64_t ko_stride_row,
+                int64_t ko_stride_head) {
+  TraceRange trace_range("dspark_rope");
+  if (!c) return DSPARK_EINVAL;
+  if (d < 16 || d > kRopeMaxD || d % 8)
+    return fail(c, DSPARK_EINVAL, "head size must be a multiple of 8 in 16..%d (got %d)", kRopeMaxD, d);
+  RopeArgs a;
+  int rc = rope_args(c, a, n_rows, heads_q, heads, d, rot, row_pos, freq, factor, q, q_stride_row, q_stride_head, q_out,
+                     qo_stride_row, qo_stride_head);
+  if (rc) return rc;
+  if (n_rows == 0 || heads_q + heads == 0) return DSPARK_OK;
+  if (heads > 0) {
+    if ((rc = check_rows(c, "k", k, k_stride_row, k_stride_head))) return rc;
+    if ((rc = check_out_rows(c, "k_out", k_out, n_rows, heads, d, ko_stride_row, ko_stride_head))) return rc;
+    if (k == k_out && ((n_rows > 1 && k_stride_row != ko_stride_row) || (heads > 1 && k_stride_head != ko_stride_head)))
+      return fail(c, DSPARK_EINVAL, "k_out may be k with equal strides only");
+    if (heads_q > 0 && (q_out == k || q_out == k_out || k_out == q))
+      return fail(c, DSPARK_EINVAL, "q_out and k_out must be different arrays, and not the other's input");
+  }
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
+  a.heads_k = heads;
+  a.heads_inv = inverse(heads_q + heads);
+  a.k = static_cast<const uint16_t*>(k);
+  a.k_row = k_stride_row;
+  a.k_head = k_stride_head;
+  a.ko = static_cast<uint16_t*>(k_out);
+  a.ko_row = ko_stride_row;
+  a.ko_head = ko_stride_head;
+  // what is not turned has to be copied unless it is there already
+  const bool in_place = (heads_q == 0 || q == q_out) && (heads == 0 || k == k_out);
+  a.units = rot / 16 + (in_place ? 0 : (d - rot) / 8);
+  a.units_inv = inverse(a.units);
+  const int grid = (n_rows + a.rows - 1) / a.rows;
+  return klaunch(c, DSPARK_K_ROPE, rope_kernel(interleaved != 0), dim3(grid), dim3(kRopeThreads), &a, stream);
+}
+
+int dspark_rope_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q, int heads, int d, int rot,
+                      int interleaved, int page_size, int n_pages, const int32_t* row_pos, const int32_t* row_slot,
+                      const double* freq, float factor, const void* q, int64_t q_stride_row, int64_t q_stride_head,
+                      void* q_out, int64_t qo_stride_row, int64_t qo_stride_head, const void* k, int64_t k_stride_row,
+                      int64_t k_stride_head, const void* v, int64_t v_stride_row, int64_t v_stride_head, void* kcache,
+                      void* vcache, int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                      dspark_dtype kv_dtype, const float* k_scale, const float* v_scale, uint8_t* k_power,
+                      uint8_t* v_power) {
+  TraceRange trace_range("dspark_rope_write");
+  if (!c) return DSPARK_EINVAL;
+  int rc = check_slots(c, page_size, n_pages);
+  if (rc) return rc;
+  if ((rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype)))
+    return rc;
+  if ((rc = check_scales(c, kv_dtype, k_scale, v_scale, k_power, v_power))) return rc;
+  RopeArgs a;
+  rc = rope_args(c, a, n_rows, heads_q, heads, d, rot, row_pos, freq, factor, q, q_stride_row, q_stride_head, q_out,
+                 qo_stride_row, qo_stride_head);
+  if (rc) return rc;
+  if (n_rows == 0) return DSPARK_OK;
+  if (!row_slot) return fail(c, DSPARK_EINVAL, "null pointer argument");
+  if ((rc = check_rows(c, "k", k, k_stride_row, k_stride_head))) return rc;
+  if ((rc = check_rows(c, "v", v, v_stride_row, v_stride_head))) return rc;
+  if (heads_q > 0 && (q_out == k || q_out == v))
+    return fail(c, DSPARK_EINVAL, "q_out must be another array than k and v");
+  DeviceGuard dg(c->device);
+  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
+  const int64_t size = kv_dtype == DSPARK_BF16 ? 2 : 1;
+  a.heads_inv = inverse(heads_q);
+  a.heads_kv = heads;
+  a.heads_kv_inv = inverse(heads);
+  a.units = rot / 16 + (q == q_out ? 0 : (d - rot) / 8);
+  a.units_inv = inverse(a.units);
   a.k = static_cast<const uint16_t*>(k);
   a.k_row = k_stride_row;
   a.k_head = k_stride_head;
@@ -1847,6 +2211,8 @@ int dspark_cache_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads,
   a.v_row = v_stride_row;
   a.v_head = v_stride_head;
   a.slot = row_slot;
+  a.page_shift = page_shift(page_size);
+  a.n_slots = (int64_t)n_pages << a.page_shift;
   a.kc = static_cast<unsigned char*>(kcache);
   a.vc = static_cast<unsigned char*>(vcache);
   a.c_page = c_stride_page * size;
@@ -1854,9 +2220,13 @@ int dspark_cache_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads,
   a.c_head = c_stride_head * size;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.err = c->dev_err;
-  const int grid = (n_rows * a.chunks + kCacheThreads - 1) / kCacheThreads;
-  return klaunch(c, DSPARK_K_CACHE, cache_write_kernel(e4m3), dim3(grid), dim3(kCacheThreads), &a, stream);
+  a.k_power = k_power;
+  a.v_power = v_power;
+  a.s_head = (int64_t)page_size * (d / 32);
+  a.s_page = heads * a.s_head;
+  const int grid = (n_rows + a.rows - 1) / a.rows;
+  return klaunch(c, DSPARK_K_ROPE, rope_write_kernel(interleaved != 0, cache_type(kv_dtype)), dim3(grid),
+                 dim3(kRopeThreads), &a, stream);
 }
 
 int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads, int d,
@@ -1868,94 +2238,26 @@ int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
                   int64_t o_stride_head, float* lse) {
   TraceRange trace_range("dspark_attend");
   if (!c) return DSPARK_EINVAL;
-  int rc = check_pages(c, B, page_size, n_pages, max_pages, table_stride, table);
-  if (rc) return rc;
-  if ((rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype)))
-    return rc;
-  const int sh = page_shift(page_size);
-  const bool e4m3 = kv_dtype == DSPARK_E4M3;
-  if (!e4m3 && (k_scale || v_scale)) return fail(c, DSPARK_EINVAL, "scales belong to an e4m3 cache");
-  if (gamma < 0 || gamma > kMaxGamma) return fail(c, DSPARK_EINVAL, "gamma must be in 0..%d", kMaxGamma);
-  if (n_rows < 0 || (!t_offsets && (int64_t)B * (gamma + 1) > n_rows))
-    return fail(c, DSPARK_EINVAL, "n_rows must hold B * (gamma + 1) rows where t_offsets is NULL");
-  if (n_rows == 0) return DSPARK_OK;
-  if (heads_q < 1 || heads_q % heads || heads_q / heads > 64)
-    return fail(c, DSPARK_EINVAL, "heads_q must be 1 to 64 times heads (got %d, %d)", heads_q, heads);
-  if (!q || !out || !len) return fail(c, DSPARK_EINVAL, "null pointer argument");
-  if (!aligned16(q) || !aligned16(out) || (q_stride_row & 7) || (q_stride_head & 7) || (o_stride_row & 7) ||
-      (o_stride_head & 7) || q_stride_row < 0 || q_stride_head < 0 || o_stride_row < 0 || o_stride_head < 0)
-    return fail(c, DSPARK_EINVAL, "q and out must be 16-byte aligned, their strides multiples of 8");
-  // rows and heads of the result that are there more than once must not overlap
-  const bool row_major = (heads_q == 1 || o_stride_head >= d) &&
-                         (n_rows == 1 || o_stride_row >= (heads_q == 1 ? d : heads_q * o_stride_head));
-  const bool head_major = (n_rows == 1 || o_stride_row >= d) &&
-                          (heads_q == 1 || o_stride_head >= (n_rows == 1 ? d : n_rows * o_stride_row));
-  if (!row_major && !head_major) return fail(c, DSPARK_EINVAL, "out strides overlap");
-  // (several workgroups may read a row of q while one of them writes its result)
-  if (out == q) return fail(c, DSPARK_EINVAL, "out may not be q");
-  if (!(scale > 0.0f) || !std::isfinite(scale)) return fail(c, DSPARK_EINVAL, "scale must be positive and finite");
-  // the fewest 16-row blocks that hold a request's rows of one cache head, up
-  // to 64 rows (d = 256: 32, its sums fill the registers): a tile reads its keys
-  // once for all of them, and unused blocks cost products and registers (blocks
-  // of 1 / the rule / 4: 181 / 117 / 126 us for 32 rows a cache head, 349 / 141 /
-  // 140 for 64, 23.6 / 23.6 / 29 for 7)
-  const int group = heads_q / heads, most = group * (gamma + 1);
-  const int mt = most <= 16 ? 1 : most <= 32 || d == 256 ? 2 : 4;
-  const int64_t tiles = (most + 16 * mt - 1) / (16 * mt);
-  const int64_t tokens = (int64_t)max_pages << sh;
-  if (tokens > INT32_MAX - 4096 || heads * tiles * (tokens / 32 + 64) > INT32_MAX)
-    return fail(c, DSPARK_EINVAL, "max_pages * page_size is too large");
-  DeviceGuard dg(c->device);
-  if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
-  if (!c->attend_buf) {
-    if (hipMalloc(&c->attend_buf, kAttendJoinBytes + kAttendPartBytes) != hipSuccess) {
-      (void)hipGetLastError();
-      c->attend_buf = nullptr;
-      return fail(c, DSPARK_ENOMEM, "allocation of %zu bytes failed", kAttendJoinBytes + kAttendPartBytes);
-    }
-  }
-  const void* fn = attend_kernel(d, mt, e4m3);
-  const int grid = std::min(kAttendMaxGrid, c->cu_count);
-  AttendArgs a;
-  memset(&a, 0, sizeof(a));
-  const int64_t size = e4m3 ? 1 : 2;
-  a.B = B;
-  a.n_rows = n_rows;
-  a.gamma = gamma;
-  a.Hq = heads_q;
-  a.Hkv = heads;
-  a.group = group;
-  a.page_shift = sh;
-  a.n_pages = n_pages;
-  a.cols = max_pages;
-  a.causal = causal != 0;
-  a.rows = 16 * mt;
-  a.q = static_cast<const uint16_t*>(q);
-  a.q_row = q_stride_row;
-  a.q_head = q_stride_head;
-  a.kc = static_cast<const unsigned char*>(kcache);
-  a.vc = static_cast<const unsigned char*>(vcache);
-  a.c_page = c_stride_page * size;
-  a.c_tok = c_stride_tok * size;
-  a.c_head = c_stride_head * size;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.table = table;
-  a.tstride = table_stride;
-  a.len = len;
-  a.K = K;
-  a.offs = t_offsets;
-  a.scale2 = scale * kLog2e;
-  a.unrest = e4m3 ? 1.0f : 1.0f / kRestFactor;
-  a.out = static_cast<uint16_t*>(out);
-  a.o_row = o_stride_row;
-  a.o_head = o_stride_head;
-  a.lse = lse;
-  a.joins = reinterpret_cast<AttendJoin*>(c->attend_buf);
-  a.part = reinterpret_cast<float*>(c->attend_buf + kAttendJoinBytes);
-  a.err = c->dev_err;
-  if ((rc = klaunch(c, DSPARK_K_ATTEND, fn, dim3(grid), dim3(kAttendThreads), &a, stream))) return rc;
-  return klaunch(c, DSPARK_K_ATTEND, attend_join_kernel(d), dim3(grid, mt), dim3(kAttendThreads), &a, stream);
+  if (kv_dtype == DSPARK_MXFP4) return fail(c, DSPARK_EINVAL, "an mxfp4 cache is read by dspark_attend_mxfp4");
+  return attend_common(c, stream, B, n_rows, gamma, heads_q, heads, d, q, q_stride_row, q_stride_head, kcache, vcache,
+                       c_stride_page, c_stride_tok, c_stride_head, kv_dtype, k_scale, v_scale, nullptr, nullptr,
+                       page_size, n_pages, table, table_stride, max_pages, len, K, t_offsets, causal, scale, out,
+                       o_stride_row, o_stride_head, lse);
+}
+
+int dspark_attend_mxfp4(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads, int d,
+                        const void* q, int64_t q_stride_row, int64_t q_stride_head, const void* kcache,
+                        const void* vcache, int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
+                        const uint8_t* k_power, const uint8_t* v_power, int page_size, int n_pages,
+                        const int32_t* table, int64_t table_stride, int max_pages, const int32_t* len,
+                        const int32_t* K, const int32_t* t_offsets, int causal, float scale, void* out,
+                        int64_t o_stride_row, int64_t o_stride_head, float* lse) {
+  TraceRange trace_range("dspark_attend_mxfp4");
+  if (!c) return DSPARK_EINVAL;
+  return attend_common(c, stream, B, n_rows, gamma, heads_q, heads, d, q, q_stride_row, q_stride_head, kcache, vcache,
+                       c_stride_page, c_stride_tok, c_stride_head, DSPARK_MXFP4, nullptr, nullptr, k_power, v_power,
+                       page_size, n_pages, table, table_stride, max_pages, len, K, t_offsets, causal, scale, out,
+                       o_stride_row, o_stride_head, lse);
 }
 
 int dspark_constrain(dspark_ctx* c, hipStream_t stream, int B, int n_pos, int V, const void* logits,

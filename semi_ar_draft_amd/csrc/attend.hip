@@ -86,6 +86,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
+__device__ __forceinline__ uint2 load8(const unsigned char* p) {
+  typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
+  const u32x2_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
+  return make_uint2(v[0], v[1]);
+}
+
 __device__ __forceinline__ uint4 load16(const unsigned char* p) {
   typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
   const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
@@ -99,6 +105,23 @@ __device__ __forceinline__ uint32_t odd_bf16(uint32_t x) {
 }
 __device__ __forceinline__ uint32_t odd_e4m3(uint32_t x) {
   return ((((x & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xFFu;
+}
+
+// The bit pattern of 2^(b - 127) as the conversions below read it (the exponent's eight bits alone), b the byte of x that
+// a rotation by `turn` = (8 place + 9) % 32 bits brings there.
+__device__ __forceinline__ float power_at(uint32_t x, unsigned turn) {
+  return __uint_as_float(__builtin_amdgcn_alignbit(x, x, turn));
+}
+__device__ __forceinline__ bool odd_power(float s) { return (__float_as_uint(s) & 0x7F800000u) >= 0x7E800000u; }
+
+// Two e2m1 values (byte c of w) times a power of two as bf16: exact from 2^-126 on, NaN for a byte of 255.
+__device__ __forceinline__ uint32_t widen4(uint32_t w, float s, int c) {
+  switch (c) {                                           // (the place is an immediate)
+    case 0: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 0));
+    case 1: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 1));
+    case 2: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 2));
+    default: return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(w, s, 3));
+  }
 }
 
 // Two e4m3 values (the low or high half of w) as bf16 or f16: exact.
@@ -141,43 +164,75 @@ __device__ __forceinline__ Rows request_rows(const AttendArgs& a, P K, P len, P 
   return r;
 }
 
+// Places of the four groups of eight tokens of a step: bytes from the beginning of a cache, and (MXFP4) of its scales.
+template <int F>
+struct At {
+  int64_t v[4];
+};
+template <>
+struct At<kCacheMxfp4> {
+  int64_t v[4], s[4];
+};
+
 // Keys and values of a step as a lane has them loaded.
-template <int D, int E4M3>
+template <int D, int F>
 struct Loaded {
-  static constexpr int KW = E4M3 ? D / 64 : D / 32;      // 16-byte loads of a key per lane
-  static constexpr int VW = D / 16 * (E4M3 ? 1 : 2) / 4; // words of a value per lane
+  static constexpr bool kBf16 = F == kCacheBf16, kFp4 = F == kCacheMxfp4;
+  static constexpr int kBits = kBf16 ? 16 : kFp4 ? 4 : 8;
+  static constexpr int KB = D * kBits / 32 < 16 ? D * kBits / 32 : 16;   // bytes of a lane's load of a key
+  static constexpr int KW = D * kBits / 32 / KB;         // such loads of a key per lane
+  static constexpr int VB = D * kBits / 128;             // bytes of a value per lane
+  static constexpr int VW = VB < 4 ? 1 : VB / 4;
+  static constexpr int NB = D / 32;                      // blocks that share a power of two (MXFP4)
   uint4 k[2][KW];
   uint32_t v[8][VW];
+  uint32_t ks[kFp4 ? 2 : 1][KW];                         // MXFP4: powers of the keys' blocks,
+  uint32_t vs[kFp4 ? 8 : 1];                             // of the values' (words; from take_v on those of the lane's tokens)
 
   // A lane's keys: token lane % 16 of either half, `kl` its place in a group.
-  __device__ __forceinline__ void load_k(const unsigned char* kc, const int64_t (&at)[4], unsigned kl, int lane) {
+  __device__ __forceinline__ void load_k(const unsigned char* kc, const unsigned char* sc, const At<F>& at, unsigned kl,
+                                         int lane) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int64_t lo = at[2 * s], hi = at[2 * s + 1];
+      const int64_t lo = at.v[2 * s], hi = at.v[2 * s + 1];
       const unsigned char* p = kc + (lane & 8 ? hi : lo) + kl;
 #pragma unroll
-      for (int w = 0; w < KW; ++w) k[s][w] = load16(p + 64 * w);
+      for (int w = 0; w < KW; ++w) {
+        if constexpr (KB == 8) {
+          const uint2 x = load8(p);
+          k[s][w] = make_uint4(x.x, x.y, 0, 0);
+        } else {
+          k[s][w] = load16(p + 64 * w);
+        }
+      }
+      if constexpr (kFp4) {
+        const int64_t slo = at.s[2 * s], shi = at.s[2 * s + 1];
+        const unsigned char* ps = sc + (lane & 8 ? shi : slo) + (lane & 7) * NB + (D == 64 ? lane >> 5 : lane >> 4);
+#pragma unroll
+        for (int w = 0; w < KW; ++w) ks[s][w] = ps[4 * w];
+      }
     }
   }
 
   // A lane's values: tokens 4 g + i of either half, `vl` the first one's place in its group.
-  __device__ __forceinline__ void load_v(const unsigned char* vc, const int64_t (&at)[4], unsigned vl, int64_t c_tok,
-                                         int lane) {
+  __device__ __forceinline__ void load_v(const unsigned char* vc, const unsigned char* sc, const At<F>& at, unsigned vl,
+                                         int64_t c_tok, int lane) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int64_t lo = at[2 * s], hi = at[2 * s + 1];
+      const int64_t lo = at.v[2 * s], hi = at.v[2 * s + 1];
       const unsigned char* p = vc + (lane & 32 ? hi : lo) + vl;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const unsigned char* pt = p + i * c_tok;
         uint32_t(&w)[VW] = v[4 * s + i];
-        if constexpr (VW == 1) {
+        if constexpr (VB == 2) {
+          w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(pt));
+        } else if constexpr (VW == 1) {
           w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(pt));
         } else if constexpr (VW == 2) {
-          typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
-          const u32x2_t x = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(pt));
-          w[0] = x[0];
-          w[1] = x[1];
+          const uint2 x = load8(pt);
+          w[0] = x.x;
+          w[1] = x.y;
         } else {
 #pragma unroll
           for (int c = 0; c < VW / 4; ++c) {
@@ -189,13 +244,64 @@ struct Loaded {
           }
         }
       }
+      if constexpr (kFp4) {
+        // the powers of the lane's four tokens: 2, 4 or 8 bytes each, one after the other
+        const int64_t slo = at.s[2 * s], shi = at.s[2 * s + 1];
+        const unsigned char* ps = sc + (lane & 32 ? shi : slo) + 4 * (lane >> 4 & 1) * NB;
+        if constexpr (D == 64) {
+          const uint2 x = *reinterpret_cast<const uint2*>(ps);
+          vs[4 * s] = x.x;
+          vs[4 * s + 1] = x.y;
+        } else if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(ps);
+          vs[4 * s] = x.x;
+          vs[4 * s + 1] = x.y;
+          vs[4 * s + 2] = x.z;
+          vs[4 * s + 3] = x.w;
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) vs[4 * s + i] = *reinterpret_cast<const uint32_t*>(ps + NB * i + (lane & 8 ? 4 : 0));
+        }
+      }
     }
   }
 
-  // The key operand of product ks: 16 tokens (a lane: its token's values 32 ks
-  // + 8 g ..; e4m3: 64 (ks / 2) + 16 g + 8 (ks % 2) .., the order of the queries too).
+  // MXFP4: from the words of powers to those of the lane's tokens.
+  __device__ __forceinline__ void take_v(int lane) {
+    if constexpr (!kFp4) return;
+    const unsigned b = D == 64 ? lane >> 3 & 1 : D == 128 ? lane >> 2 & 3 : lane >> 1 & 3;
+    const unsigned turn = 8 * b + 9;
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+      if constexpr (D == 64) {
+        const uint32_t x = vs[4 * s], y = vs[4 * s + 1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          vs[4 * s + i] = __float_as_uint(power_at(i < 2 ? x : y, i & 1 ? (turn + 16) & 31 : turn));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) vs[4 * s + i] = __float_as_uint(power_at(vs[4 * s + i], turn & 31));
+      }
+    }
+  }
+
+  // Where product ks's values of lane's group begin in a key and a query.
+  __device__ __forceinline__ static int first(int ks, int lane) {
+    const int g = lane >> 4;
+    if constexpr (kBf16) return 32 * ks + 8 * g;
+    if constexpr (kFp4) return D == 64 ? 16 * g + 8 * ks : 128 * (ks >> 2) + 32 * g + 8 * (ks & 3);
+    return 64 * (ks >> 1) + 16 * g + 8 * (ks & 1);
+  }
+
+  // The key operand of product ks: 16 tokens (a lane: its token's values from first(ks) on).
   __device__ __forceinline__ uint4 key(int s, int ks) const {
-    if constexpr (!E4M3) return k[s][ks];
+    if constexpr (kBf16) return k[s][ks];
+    if constexpr (kFp4) {
+      const uint4 w = k[s][ks >> 2];
+      const uint32_t x = (ks & 3) == 0 ? w.x : (ks & 3) == 1 ? w.y : (ks & 3) == 2 ? w.z : w.w;
+      const float p = __uint_as_float(this->ks[s][ks >> 2] << 23);
+      return make_uint4(widen4(x, p, 0), widen4(x, p, 1), widen4(x, p, 2), widen4(x, p, 3));
+    }
     const uint4 w = k[s][ks >> 1];
     const uint32_t lo = ks & 1 ? w.z : w.x, hi = ks & 1 ? w.w : w.y;
     return make_uint4(widen<false>(lo), widen<true>(lo), widen<false>(hi), widen<true>(hi));
@@ -207,15 +313,22 @@ struct Loaded {
     uint32_t x[2][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      if constexpr (!E4M3) {
-        const uint32_t e = v[2 * j][dt / 2], o = v[2 * j + 1][dt / 2];
-        x[0][j] = __builtin_amdgcn_perm(o, e, 0x05040100u);
-        x[1][j] = __builtin_amdgcn_perm(o, e, 0x07060302u);
-      } else {
+      if constexpr (F == kCacheE4m3) {
         const uint32_t e = v[2 * j][dt / 4], o = v[2 * j + 1][dt / 4];
         const uint32_t w = __builtin_amdgcn_perm(o, e, dt & 2 ? 0x07030602u : 0x05010400u);
         x[0][j] = widen_f16<false>(w);
         x[1][j] = widen_f16<true>(w);
+      } else {
+        uint32_t e, o;
+        if constexpr (kFp4) {
+          e = widen4(v[2 * j][dt / 8], __uint_as_float(vs[2 * j]), dt / 2 & 3);
+          o = widen4(v[2 * j + 1][dt / 8], __uint_as_float(vs[2 * j + 1]), dt / 2 & 3);
+        } else {
+          e = v[2 * j][dt / 2];
+          o = v[2 * j + 1][dt / 2];
+        }
+        x[0][j] = __builtin_amdgcn_perm(o, e, 0x05040100u);
+        x[1][j] = __builtin_amdgcn_perm(o, e, 0x07060302u);
       }
     }
     f[0] = make_uint4(x[0][0], x[0][1], x[0][2], x[0][3]);
@@ -226,13 +339,24 @@ struct Loaded {
   __device__ __forceinline__ uint32_t take_odd() {
     uint32_t odd = 0;
 #pragma unroll
-    for (int t = 0; t < 8; ++t)
+    for (int t = 0; t < 8; ++t) {
+      if constexpr (kFp4) {
+        // whole blocks: those whose power says so
+        if (odd_power(__uint_as_float(vs[t]))) {
+          odd = 1;
+          vs[t] = 0x3F800000u;
 #pragma unroll
-      for (int w = 0; w < VW; ++w) {
-        const uint32_t x = E4M3 ? odd_e4m3(v[t][w]) : odd_bf16(v[t][w]);
-        odd |= x;
-        v[t][w] &= ~x;
+          for (int w = 0; w < VW; ++w) v[t][w] = 0;
+        }
+      } else {
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t x = kBf16 ? odd_bf16(v[t][w]) : odd_e4m3(v[t][w]);
+          odd |= x;
+          v[t][w] &= ~x;
+        }
       }
+    }
     return odd;
   }
 };
@@ -249,8 +373,9 @@ struct Groups {
 #pragma unroll
     for (int j = 0; j < 4; ++j) id[j] = t[first(base, j, last) >> a.page_shift];
   }
-  // Bytes from the cache's beginning, for the step at `base` whose ids are loaded.
-  __device__ __forceinline__ void place(const AttendArgs& a, int base, int last, int64_t (&at)[4]) const {
+  // The places of the step at `base` whose ids are loaded.
+  template <int D, int F>
+  __device__ __forceinline__ void place(const AttendArgs& a, int base, int last, At<F>& at) const {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       int p = id[j];
@@ -258,14 +383,17 @@ struct Groups {
         atomicOr(a.err, kErrPage);
         p = 0;
       }
-      at[j] = (int64_t)p * a.c_page + (int64_t)(first(base, j, last) & ((1 << a.page_shift) - 1)) * a.c_tok;
+      const int place = first(base, j, last) & ((1 << a.page_shift) - 1);
+      at.v[j] = (int64_t)p * a.c_page + (int64_t)place * a.c_tok;
+      if constexpr (F == kCacheMxfp4) at.s[j] = (int64_t)p * a.s_page + place * (D / 32);
     }
   }
 };
 
-template <int D, int MT, int E4M3>
+template <int D, int MT, int F>
 struct Tile {
-  using In = Loaded<D, E4M3>;
+  using In = Loaded<D, F>;
+  static constexpr bool E4M3 = F == kCacheE4m3;
   static constexpr int kRows = 16 * MT;
   static constexpr int KS = D / 32;                      // products of 32 values per score
   static constexpr int DT = D / 16;                      // 16-wide blocks of a value row
@@ -290,8 +418,7 @@ struct Tile {
       const uint16_t* p = a.q + (int64_t)(r.row0 + i) * a.q_row + (int64_t)(h * a.group + hh) * a.q_head;
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) {
-        const int d = E4M3 ? 64 * (ks >> 1) + 16 * (lane >> 4) + 8 * (ks & 1) : 32 * ks + 8 * (lane >> 4);
-        q[mt][ks] = ok ? *reinterpret_cast<const uint4*>(p + d) : make_uint4(0, 0, 0, 0);
+        q[mt][ks] = ok ? *reinterpret_cast<const uint4*>(p + In::first(ks, lane)) : make_uint4(0, 0, 0, 0);
       }
       lim[mt] = a.causal ? r.len + i : r.len + r.n - 1;
     }
@@ -409,6 +536,7 @@ struct Tile {
     // a token that a query does not see must not reach it, but 0 times
     // infinity or NaN is NaN: such values are left out here and added to the
     // results that see them at the end
+    in.take_v(lane);
     if (tail) odd |= in.take_odd();
 #pragma unroll
     for (int dt = 0; dt < DT; dt += 2) {
@@ -433,8 +561,8 @@ struct Tile {
 // Steps loaded ahead: two, or one where two and the sums pass the registers.
 // (More of the small steps cost more at a piece's beginning than they hide: three
 // 24.0, four 26.5 us against 23.4 on 48 draft blocks with heads of 64.)
-template <int D, int MT, int E4M3>
-constexpr int kAhead = D * MT >= 512 && !E4M3 ? 1 : 2;
+template <int D, int MT, int F>
+constexpr int kAhead = D * MT >= 512 && F == kCacheBf16 ? 1 : 2;
 
 // A wave's steps s0 .. s1 - 1 of a tile: the rows of request r at cache head h, row tile rt.
 struct Piece {
@@ -445,10 +573,11 @@ struct Piece {
   __device__ __forceinline__ int last() const { return min(s1 * kStep, r.len + r.n) - 1; }
 };
 
-template <int D, int MT, int E4M3>
+template <int D, int MT, int F>
 __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArgs a) {
-  using T = Tile<D, MT, E4M3>;
-  using In = Loaded<D, E4M3>;
+  using T = Tile<D, MT, F>;
+  using In = Loaded<D, F>;
+  constexpr bool E4M3 = F == kCacheE4m3, kFp4 = F == kCacheMxfp4;
   constexpr int kRows = T::kRows, DT = T::DT;
   __shared__ int64_t sums[kWaves];
   __shared__ Rows start_rows[kWaves];
@@ -457,8 +586,8 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
   __shared__ float2 share_ml[kWaves - 1][kRows];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // a lane's place in a group of eight tokens: its key's and its first value's
-  const unsigned kl = (unsigned)(lane & 7) * (unsigned)a.c_tok + 16 * (lane >> 4);
-  const unsigned vl = 4 * (lane >> 4 & 1) * (unsigned)a.c_tok + 4 * In::VW * (lane & 15);
+  const unsigned kl = (unsigned)(lane & 7) * (unsigned)a.c_tok + In::KB * (lane >> 4);
+  const unsigned vl = 4 * (lane >> 4 & 1) * (unsigned)a.c_tok + In::VB * (lane & 15);
 
   // the line: what every request adds to it, and where the four stretches of
   // this workgroup's waves begin
@@ -607,10 +736,10 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
       }
       return false;
     };
-    constexpr int N = kAhead<D, MT, E4M3>;
+    constexpr int N = kAhead<D, MT, F>;
     In in[N];
     Groups ids[N + 1];
-    int64_t at[4];
+    At<F> at;
     // a piece's first steps: page ids, then queries, keys and values
     auto ask = [&](const Piece& p) {
 #pragma unroll
@@ -618,12 +747,13 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
     };
     auto begin = [&](const Piece& p) {
       const unsigned char *kc = a.kc + (int64_t)p.h * a.c_head, *vc = a.vc + (int64_t)p.h * a.c_head;
+      const unsigned char *ksc = a.k_power + (int64_t)p.h * a.s_head, *vsc = a.v_power + (int64_t)p.h * a.s_head;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
-        ids[i].place(a, (p.s0 + i) * kStep, p.last(), at);
-        in[i].load_k(kc, at, kl, lane);
+        ids[i].template place<D>(a, (p.s0 + i) * kStep, p.last(), at);
+        in[i].load_k(kc, ksc, at, kl, lane);
         if (i == 0) t.load_q(a, p.r, p.h, p.rt, lane);
-        in[i].load_v(vc, at, vl, a.c_tok, lane);
+        in[i].load_v(vc, vsc, at, vl, a.c_tok, lane);
       }
     };
     bool have = take(now);
@@ -638,6 +768,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
       const int L = now.r.len + now.r.n, h = now.h;
       const float sc = a.scale2 * (E4M3 && a.k_scale ? a.k_scale[h] : 1.0f);
       const unsigned char *kc = a.kc + (int64_t)h * a.c_head, *vc = a.vc + (int64_t)h * a.c_head;
+      const unsigned char *ksc = a.k_power + (int64_t)h * a.s_head, *vsc = a.v_power + (int64_t)h * a.s_head;
       const int full = a.causal ? now.r.len : L - 1;     // tokens up to `full` are seen by every row
       const int last = now.last();
       Groups id = ids[N];
@@ -652,12 +783,12 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
                 // (with 64 rows the branch costs more register copies than the loads: those are
                 // the last tokens once more)
                 if (MT < 4 && base + N * kStep > last) return;
-                id.place(a, base + N * kStep, last, at);
+                id.template place<D>(a, base + N * kStep, last, at);
                 id.load(a, now.table, base + (N + 1) * kStep, last);
-                in[i].load_k(kc, at, kl, lane);
+                in[i].load_k(kc, ksc, at, kl, lane);
               },
               [&]() {
-                if (MT == 4 || base + N * kStep <= last) in[i].load_v(vc, at, vl, a.c_tok, lane);
+                if (MT == 4 || base + N * kStep <= last) in[i].load_v(vc, vsc, at, vl, a.c_tok, lane);
               });
           base += kStep;
           if (base > last) goto done;
@@ -676,8 +807,14 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
 #pragma unroll
             for (int dt = 0; dt < DT; ++dt) {
               const int d = DT * (4 * (lane >> 4) + i) + dt;
-              const uint32_t x = E4M3 ? widen<false>(p[d]) & 0xFFFFu : reinterpret_cast<const uint16_t*>(p)[d];
-              const float y = (x & 0x7F80u) == 0x7F80u ? __uint_as_float(x << 16) : 0.0f;
+              float y;
+              if constexpr (kFp4) {
+                const int64_t page0 = (int64_t)((unsigned)page < (unsigned)a.n_pages ? page : 0) * a.s_page;
+                y = vsc[page0 + (tk & ((1 << a.page_shift) - 1)) * (D / 32) + d / 32] >= 253 ? NAN : 0.0f;
+              } else {
+                const uint32_t x = E4M3 ? widen<false>(p[d]) & 0xFFFFu : reinterpret_cast<const uint16_t*>(p)[d];
+                y = (x & 0x7F80u) == 0x7F80u ? __uint_as_float(x << 16) : 0.0f;
+              }
 #pragma unroll
               for (int mt = 0; mt < MT; ++mt)
                 if (tk <= t.lim[mt]) t.o[mt][dt][i] += y;
@@ -799,16 +936,18 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_impl(const AttendA
 }
 
 template <int D, int MT>
-const void* attend_fn(int e4m3) {
-  return e4m3 ? (const void*)&attend_impl<D, MT, 1> : (const void*)&attend_impl<D, MT, 0>;
+const void* attend_fn(int type) {
+  return type == kCacheMxfp4  ? (const void*)&attend_impl<D, MT, kCacheMxfp4>
+         : type == kCacheE4m3 ? (const void*)&attend_impl<D, MT, kCacheE4m3>
+                              : (const void*)&attend_impl<D, MT, kCacheBf16>;
 }
 
 }  // namespace
 
-const void* attend_kernel(int d, int mt, int e4m3) {
-  if (d == 64) return mt == 1 ? attend_fn<64, 1>(e4m3) : mt == 2 ? attend_fn<64, 2>(e4m3) : attend_fn<64, 4>(e4m3);
-  if (d == 128) return mt == 1 ? attend_fn<128, 1>(e4m3) : mt == 2 ? attend_fn<128, 2>(e4m3) : attend_fn<128, 4>(e4m3);
-  return mt == 1 ? attend_fn<256, 1>(e4m3) : attend_fn<256, 2>(e4m3);
+const void* attend_kernel(int d, int mt, int type) {
+  if (d == 64) return mt == 1 ? attend_fn<64, 1>(type) : mt == 2 ? attend_fn<64, 2>(type) : attend_fn<64, 4>(type);
+  if (d == 128) return mt == 1 ? attend_fn<128, 1>(type) : mt == 2 ? attend_fn<128, 2>(type) : attend_fn<128, 4>(type);
+  return mt == 1 ? attend_fn<256, 1>(type) : attend_fn<256, 2>(type);
 }
 
 const void* attend_join_kernel(int d) {

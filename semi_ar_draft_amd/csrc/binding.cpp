@@ -139,7 +139,8 @@ struct Table {
 
 struct Cache {
   void *k, *v;
-  const float *k_scale, *v_scale;
+  float *k_scale = nullptr, *v_scale = nullptr;          // e4m3: a scale a head
+  uint8_t *k_power = nullptr, *v_power = nullptr;        // mxfp4: powers of two, a byte a block
   int n_pages, page, heads, d;
   int64_t s_page, s_tok, s_head;
   dspark_dtype type;
@@ -148,7 +149,8 @@ struct Cache {
     const at::ScalarType st = kc->scalar_type();
     if (st == at::kBFloat16) type = DSPARK_BF16;
     else if (st == at::kFloat8_e4m3fn) type = DSPARK_E4M3;
-    else raise(PyExc_TypeError, "the cache must be bf16 or float8_e4m3fn, got %s", c10::toString(st));
+    else if (st == at::kByte || st == at::kFloat4_e2m1fn_x2) type = DSPARK_MXFP4;
+    else raise(PyExc_TypeError, "the cache must be bf16, float8_e4m3fn or uint8 (mxfp4), got %s", c10::toString(st));
     const T* vc = a.rows("vcache", st, 4);
     if (kc->dim() != 4) raise(PyExc_ValueError, "kcache must have 4 dims, got %lld", (long long)kc->dim());
     bool alike = kc->sizes() == vc->sizes();
@@ -164,8 +166,39 @@ struct Cache {
     s_page = step(*kc, 0, std::max<int64_t>(page * s_tok, heads * s_head));
     k = kc->data_ptr();
     v = vc->data_ptr();
-    k_scale = a.floats("k_scale", heads, true);
-    v_scale = a.floats("v_scale", heads, true);
+    if (type == DSPARK_MXFP4) {
+      d = to_int("d", 2 * kc->size(3));                  // two values a byte
+      k_power = power(a, "k_scale");
+      v_power = power(a, "v_scale");
+    } else {
+      k_scale = a.floats("k_scale", heads, true);
+      v_scale = a.floats("v_scale", heads, true);
+    }
+  }
+
+ private:
+  uint8_t* power(Args& a, const char* name) {
+    const T* t = a.tensor(name);
+    if (t->scalar_type() != at::kByte && t->scalar_type() != at::kFloat8_e8m0fnu)
+      raise(PyExc_TypeError, "%s must be uint8 or float8_e8m0fnu for an mxfp4 cache, got %s", name,
+            c10::toString(t->scalar_type()));
+    if (t->dim() != 4 || t->size(0) != n_pages || t->size(1) != heads || t->size(2) != page || t->size(3) != d / 32 ||
+        !t->is_contiguous())
+      raise(PyExc_ValueError, "%s must be [n_pages][heads][page_size][d / 32] of an mxfp4 cache, contiguous", name);
+    return Args::data<uint8_t>(t);
+  }
+};
+
+// bf16 rows [n_rows][heads][d].
+struct Rows {
+  void* p = nullptr;
+  int64_t row = 0, head = 0;
+  explicit Rows(const T* t) {
+    if (!t) return;
+    p = t->data_ptr();
+    // (a row or head that is the only one: as if the others lay behind it)
+    head = step(*t, 1, t->size(2));
+    row = step(*t, 0, t->size(1) * head);
   }
 };
 
@@ -223,9 +256,89 @@ int cache_write(Args& a) {
   if (k->size(1) != c.heads || k->size(2) != c.d || v->sizes() != k->sizes())
     raise(PyExc_ValueError, "k and v must be [n_rows][heads][d] of the cache");
   const int32_t* slot = a.ints("row_slot", k->size(0));
+  if (c.type == DSPARK_MXFP4)
+    return dspark_cache_write_mxfp4(a.handle, a.stream, to_int("n_rows", k->size(0)), c.heads, c.d, c.page, c.n_pages,
+                                    k->data_ptr(), step(*k, 0), step(*k, 1), v->data_ptr(), step(*v, 0), step(*v, 1),
+                                    slot, c.k, c.v, c.s_page, c.s_tok, c.s_head, c.k_power, c.v_power);
   return dspark_cache_write(a.handle, a.stream, to_int("n_rows", k->size(0)), c.heads, c.d, c.page, c.n_pages,
                             k->data_ptr(), step(*k, 0), step(*k, 1), v->data_ptr(), step(*v, 0), step(*v, 1), slot,
                             c.k, c.v, c.s_page, c.s_tok, c.s_head, c.type, c.k_scale, c.v_scale);
+}
+
+// kcache, vcache, k_scale, v_scale, row_slot, k, v
+int cache_read(Args& a) {
+  const Cache c(a);
+  const T* slot = a.rows("row_slot", at::kInt, 1);
+  const int64_t n = slot->size(0);
+  const T* out[2];
+  for (int i = 0; i < 2; ++i) {
+    out[i] = a.rows(i ? "v" : "k", at::kBFloat16, 3);
+    if (out[i]->size(0) != n || out[i]->size(1) != c.heads || out[i]->size(2) != c.d)
+      raise(PyExc_ValueError, "k and v must be [n_rows][heads][d] of the cache");
+  }
+  const Rows k(out[0]), v(out[1]);
+  return dspark_cache_read(a.handle, a.stream, to_int("n_rows", n), c.heads, c.d, c.page, c.n_pages,
+                           Args::data<int32_t>(slot), c.k, c.v, c.s_page, c.s_tok, c.s_head, c.type, c.k_scale,
+                           c.v_scale, c.k_power, c.v_power, k.p, k.row, k.head, v.p, v.row, v.head);
+}
+
+// freq, factor: the turned values of a head, its pairs' frequencies and the factor.
+struct Turn {
+  const double* freq;
+  int rot;
+  float factor;
+  bool interleaved;
+  explicit Turn(Args& a) {
+    const T* f = a.vector("freq", at::kDouble, -1);
+    rot = to_int("freq", 2 * f->size(0));
+    freq = Args::data<double>(f);
+    interleaved = a.truth();
+    factor = a.real("factor");
+  }
+};
+
+// freq, interleaved, factor, row_pos, k, k_out, q, q_out
+int rope(Args& a) {
+  const Turn turn(a);
+  const T* pos = a.rows("row_pos", at::kInt, 1);
+  const int64_t n = pos->size(0);
+  const T* k = a.rows("k", at::kBFloat16, 3, true);
+  const T* ko = a.rows("k_out", at::kBFloat16, 3, !k);
+  if (k && (k->size(0) != n || ko->sizes() != k->sizes()))
+    raise(PyExc_ValueError, "k and k_out must be [n_rows][heads][d]");
+  const T* q = a.rows("q", at::kBFloat16, 3, k != nullptr);
+  const T* qo = a.rows("q_out", at::kBFloat16, 3, !q);
+  if (q && (q->size(0) != n || (k && q->size(2) != k->size(2)) || qo->sizes() != q->sizes()))
+    raise(PyExc_ValueError, "q and q_out must be [n_rows][heads_q][d]");
+  const Rows rq(q), rk(k), rqo(qo), rko(ko);
+  return dspark_rope(a.handle, a.stream, to_int("n_rows", n), q ? to_int("heads_q", q->size(1)) : 0,
+                     k ? to_int("heads", k->size(1)) : 0, to_int("d", (k ? k : q)->size(2)), turn.rot, turn.interleaved,
+                     Args::data<int32_t>(pos), turn.freq, turn.factor, rq.p, rq.row, rq.head, rk.p, rk.row, rk.head,
+                     rqo.p, rqo.row, rqo.head, rko.p, rko.row, rko.head);
+}
+
+// kcache, vcache, k_scale, v_scale, freq, interleaved, factor, row_pos,
+// row_slot, k, v, q, q_out
+int rope_write(Args& a) {
+  const Cache c(a);
+  const Turn turn(a);
+  const T* pos = a.rows("row_pos", at::kInt, 1);
+  const int64_t n = pos->size(0);
+  const int32_t* slot = a.ints("row_slot", n);
+  const T* k = a.rows("k", at::kBFloat16, 3);
+  const T* v = a.rows("v", at::kBFloat16, 3);
+  if (k->size(0) != n || k->size(1) != c.heads || k->size(2) != c.d || v->sizes() != k->sizes())
+    raise(PyExc_ValueError, "k and v must be [n_rows][heads][d] of the cache");
+  const T* q = a.rows("q", at::kBFloat16, 3, true);
+  const T* qo = a.rows("q_out", at::kBFloat16, 3, !q);
+  if (q && (q->size(0) != n || q->size(2) != c.d || qo->sizes() != q->sizes()))
+    raise(PyExc_ValueError, "q and q_out must be [n_rows][heads_q][d]");
+  const Rows rq(q), rqo(qo), rk(k), rv(v);
+  return dspark_rope_write(a.handle, a.stream, to_int("n_rows", n), q ? to_int("heads_q", q->size(1)) : 0, c.heads, c.d,
+                           turn.rot, turn.interleaved, c.page, c.n_pages, Args::data<int32_t>(pos), slot, turn.freq,
+                           turn.factor, rq.p, rq.row, rq.head, rqo.p, rqo.row, rqo.head, rk.p, rk.row, rk.head, rv.p,
+                           rv.row, rv.head, c.k, c.v, c.s_page, c.s_tok, c.s_head, c.type, c.k_scale, c.v_scale,
+                           c.k_power, c.v_power);
 }
 
 // kcache, vcache, k_scale, v_scale, q, length, table, gamma, K, t_offsets,
@@ -248,6 +361,12 @@ int attend(Args& a) {
   const T* lse = a.rows("lse", at::kFloat, 2, true);
   if (lse && (!lse->is_contiguous() || lse->size(0) != q->size(0) || lse->size(1) != q->size(1)))
     raise(PyExc_ValueError, "lse must be [n_rows][heads_q], contiguous");
+  if (c.type == DSPARK_MXFP4)
+    return dspark_attend_mxfp4(a.handle, a.stream, to_int("B", B), to_int("n_rows", q->size(0)), gamma,
+                               to_int("heads_q", q->size(1)), c.heads, c.d, q->data_ptr(), step(*q, 0), step(*q, 1),
+                               c.k, c.v, c.s_page, c.s_tok, c.s_head, c.k_power, c.v_power, c.page, c.n_pages, table.p,
+                               table.stride, table.cols, Args::data<int32_t>(length), K, offs, causal ? 1 : 0, scale,
+                               out->data_ptr(), step(*out, 0), step(*out, 1), Args::data<float>(lse));
   return dspark_attend(a.handle, a.stream, to_int("B", B), to_int("n_rows", q->size(0)), gamma,
                        to_int("heads_q", q->size(1)), c.heads, c.d, q->data_ptr(), step(*q, 0), step(*q, 1), c.k, c.v,
                        c.s_page, c.s_tok, c.s_head, c.type, c.k_scale, c.v_scale, c.page, c.n_pages, table.p,
@@ -349,7 +468,9 @@ PyMethodDef method(const char* name) {
 PyMethodDef methods[] = {
     method<pages_reserve, 15>("pages_reserve"), method<pages_commit, 12>("pages_commit"),
     method<cache_write, 7>("cache_write"),      method<attend, 14>("attend"),
-    method<constrain, 16>("constrain"),         {nullptr, nullptr, 0, nullptr},
+    method<constrain, 16>("constrain"),         method<cache_read, 7>("cache_read"),
+    method<rope, 8>("rope"),                    method<rope_write, 13>("rope_write"),
+    {nullptr, nullptr, 0, nullptr},
 };
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -1,64 +1,33 @@
 // Keys and values of a step's packed rows into their slots of the paged
-// cache, as bf16 or rounded to e4m3 with a scale per head.
+// cache, as bf16, rounded to e4m3 with a scale per head, or to e2m1 with a
+// power of two for each 32 of them (MXFP4); and rows of a cache back as bf16.
 //
-// A copy with a scattered destination: bound by memory (at a step's few
+// Copies with a scattered side: bound by memory (at a step's few
 // rows by the launch).  A thread owns 16 bytes of the key cache and of the
-// value cache, so both tensors' loads are in flight together, and consecutive
-// threads write consecutive bytes of a token's head.  Measured: 16381 rows of 8
-// heads of 128 into e4m3, 101 MB, 24.4 us (4.1 TB/s, a copy reaches 4.8); a
-// step's rows of 128 requests 3.3 us.
-#include "common.hpp"
-#include "internal.hpp"
+// value cache (MXFP4: 4, of eight values, whose block's largest the lanes of
+// a quad find together), so both tensors' loads are in flight together, and
+// consecutive threads write consecutive bytes of a token's head.  Measured:
+// 16381 rows of 8 heads of 128 into e4m3, 101 MB, 24.4 us (4.1 TB/s, a copy
+// reaches 4.8); a step's rows of 128 requests 3.3 us.
+#include "cache_values.hpp"
 
 namespace dspark {
 namespace {
 
-// x / s as the e4m3 value nearest the exact quotient (ties to even, larger
-// magnitudes kept at 448, NaN as NaN).  A float quotient q may have been
-// rounded onto a border between two e4m3 values that the exact quotient
-// misses, so its last bit is made sticky: with r = x - q s (its sign is
-// exact) nonzero, an even q moves one step towards the exact quotient; an
-// odd q lies on no border (those end in zeros).
-__device__ __forceinline__ float quotient_sticky(float x, float s, float rs) {
-  const float q0 = x * rs;
-  // infinities, and what stays beyond 448 whatever the last bits are
-  if (!(__builtin_fabsf(q0) < 512.0f)) return q0 != q0 ? q0 : __builtin_copysignf(448.0f, q0);
-  const float q = __builtin_fmaf(__builtin_fmaf(-q0, s, x), rs, q0);
-  const float r = __builtin_fmaf(-q, s, x);
-  const uint32_t u = __float_as_uint(q);
-  // r with the sign of x: |q| falls short of |x / s|
-  const bool up = (__float_as_uint(r) ^ __float_as_uint(x)) >> 31 == 0;
-  const bool move = r != 0.0f && (u & 1u) == 0 && (u << 1) != 0;
-  const float t = __uint_as_float(move ? (up ? u + 1 : u - 1) : u);
-  return __builtin_fminf(__builtin_fmaxf(t, -448.0f), 448.0f);
-}
-
-__device__ __forceinline__ uint32_t pack4(const float (&q)[4]) {
-  int w = 0;
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(q[0], q[1], w, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(q[2], q[3], w, true);
-  return (uint32_t)w;
-}
-
-template <int E4M3>
+// 16 bytes of a bf16 or e4m3 cache.
+template <int F>
 __device__ __forceinline__ uint4 to_cache(const uint16_t* p, float s, float rs) {
-  if constexpr (!E4M3) return *reinterpret_cast<const uint4*>(p);
-  const uint4 x[2] = {reinterpret_cast<const uint4*>(p)[0], reinterpret_cast<const uint4*>(p)[1]};
-  uint32_t out[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const uint32_t w0 = j & 1 ? x[j >> 1].z : x[j >> 1].x, w1 = j & 1 ? x[j >> 1].w : x[j >> 1].y;
-    const float v[4] = {__uint_as_float(w0 << 16), __uint_as_float(w0 & 0xFFFF0000u), __uint_as_float(w1 << 16),
-                        __uint_as_float(w1 & 0xFFFF0000u)};
-    float q[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) q[i] = quotient_sticky(v[i], s, rs);
-    out[j] = pack4(q);
-  }
-  return make_uint4(out[0], out[1], out[2], out[3]);
+  const uint4 x = *reinterpret_cast<const uint4*>(p);
+  if constexpr (F == kCacheBf16) return x;
+  const uint4 y = reinterpret_cast<const uint4*>(p)[1];
+  float f[2][8];
+  unpack8(x, f[0]);
+  unpack8(y, f[1]);
+  const uint2 lo = to_e4m3(f[0], s, rs), hi = to_e4m3(f[1], s, rs);
+  return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
-template <int E4M3>
+template <int F>
 __global__ __launch_bounds__(kCacheThreads) void cache_write_impl(const CacheWriteArgs a) {
   const unsigned i = blockIdx.x * kCacheThreads + threadIdx.x;
   const unsigned row = i / (unsigned)a.chunks;
@@ -69,26 +38,102 @@ __global__ __launch_bounds__(kCacheThreads) void cache_write_impl(const CacheWri
     if (slot != -1 && c == 0) atomicOr(a.err, kErrSlot);
     return;
   }
-  constexpr int kElems = E4M3 ? 16 : 8;
+  constexpr int kElems = F == kCacheE4m3 ? 16 : 8;
   const int h = c >> a.chunk_shift;
   const int d0 = (c & ((1 << a.chunk_shift) - 1)) * kElems;
-  const int64_t to = (int64_t)(slot >> a.page_shift) * a.c_page + (int64_t)(slot & ((1 << a.page_shift) - 1)) * a.c_tok +
-                     (int64_t)h * a.c_head + (E4M3 ? d0 : 2 * d0);
+  const int page = slot >> a.page_shift, place = slot & ((1 << a.page_shift) - 1);
+  const int64_t to = (int64_t)page * a.c_page + (int64_t)place * a.c_tok + (int64_t)h * a.c_head;
+  const uint16_t *kp = a.k + row * a.k_row + h * a.k_head + d0, *vp = a.v + row * a.v_row + h * a.v_head + d0;
+  if constexpr (F == kCacheMxfp4) {
+    const uint4 xk = *reinterpret_cast<const uint4*>(kp), xv = *reinterpret_cast<const uint4*>(vp);
+    float k[8], v[8];
+    unpack8(xk, k);
+    unpack8(xv, v);
+    unsigned char pk, pv;
+    const uint32_t wk = to_mxfp4(k, pk), wv = to_mxfp4(v, pv);
+    *reinterpret_cast<uint32_t*>(a.kc + to + d0 / 2) = wk;
+    *reinterpret_cast<uint32_t*>(a.vc + to + d0 / 2) = wv;
+    if ((threadIdx.x & 3) == 0) {
+      const int64_t at = page * a.s_page + h * a.s_head + (int64_t)place * a.blocks + d0 / 32;
+      a.k_power[at] = pk;
+      a.v_power[at] = pv;
+    }
+  } else {
+    float ks = 1.0f, vs = 1.0f;
+    if constexpr (F == kCacheE4m3) {
+      if (a.k_scale) ks = a.k_scale[h];
+      if (a.v_scale) vs = a.v_scale[h];
+    }
+    const uint4 k = to_cache<F>(kp, ks, 1.0f / ks);
+    const uint4 v = to_cache<F>(vp, vs, 1.0f / vs);
+    const int64_t at = to + (F == kCacheE4m3 ? d0 : 2 * d0);
+    *reinterpret_cast<uint4*>(a.kc + at) = k;
+    *reinterpret_cast<uint4*>(a.vc + at) = v;
+  }
+}
+
+// Eight values of a cache as bf16: the product with an e4m3 cache's scale is
+// rounded to float32 and that to bf16, MXFP4 values are exact.
+template <int F>
+__device__ __forceinline__ uint4 from_cache(const unsigned char* p, float s, unsigned char power) {
+  if constexpr (F == kCacheBf16) {
+    return *reinterpret_cast<const uint4*>(p);
+  } else if constexpr (F == kCacheMxfp4) {
+    return from_mxfp4(*reinterpret_cast<const uint32_t*>(p), power);
+  } else {
+    typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+    const uint2 x = *reinterpret_cast<const uint2*>(p);
+    const f32x2_t f[4] = {__builtin_amdgcn_cvt_pk_f32_fp8(x.x, false), __builtin_amdgcn_cvt_pk_f32_fp8(x.x, true),
+                          __builtin_amdgcn_cvt_pk_f32_fp8(x.y, false), __builtin_amdgcn_cvt_pk_f32_fp8(x.y, true)};
+    return make_uint4(pack2_bf16(f[0][0] * s, f[0][1] * s), pack2_bf16(f[1][0] * s, f[1][1] * s),
+                      pack2_bf16(f[2][0] * s, f[2][1] * s), pack2_bf16(f[3][0] * s, f[3][1] * s));
+  }
+}
+
+template <int F>
+__global__ __launch_bounds__(kCacheThreads) void cache_read_impl(const CacheReadArgs a) {
+  const unsigned i = blockIdx.x * kCacheThreads + threadIdx.x;
+  const unsigned row = i / (unsigned)a.chunks;
+  if (row >= (unsigned)a.n_rows) return;
+  const unsigned c = i - row * (unsigned)a.chunks;
+  const int slot = a.slot[row];
+  if (slot < 0 || slot >= a.n_slots) {
+    if (slot != -1 && c == 0) atomicOr(a.err, kErrSlot);
+    return;
+  }
+  const int h = c >> a.chunk_shift;
+  const int d0 = (c & ((1 << a.chunk_shift) - 1)) * 8;
+  const int page = slot >> a.page_shift, place = slot & ((1 << a.page_shift) - 1);
+  const int64_t from = (int64_t)page * a.c_page + (int64_t)place * a.c_tok + (int64_t)h * a.c_head +
+                       (F == kCacheBf16 ? 2 * d0 : F == kCacheE4m3 ? d0 : d0 / 2);
   float ks = 1.0f, vs = 1.0f;
-  if constexpr (E4M3) {
+  unsigned char kp = 0, vp = 0;
+  if constexpr (F == kCacheE4m3) {
     if (a.k_scale) ks = a.k_scale[h];
     if (a.v_scale) vs = a.v_scale[h];
   }
-  const uint4 k = to_cache<E4M3>(a.k + row * a.k_row + h * a.k_head + d0, ks, 1.0f / ks);
-  const uint4 v = to_cache<E4M3>(a.v + row * a.v_row + h * a.v_head + d0, vs, 1.0f / vs);
-  *reinterpret_cast<uint4*>(a.kc + to) = k;
-  *reinterpret_cast<uint4*>(a.vc + to) = v;
+  if constexpr (F == kCacheMxfp4) {
+    const int64_t at = page * a.s_page + h * a.s_head + (int64_t)place * a.blocks + d0 / 32;
+    kp = a.k_power[at];
+    vp = a.v_power[at];
+  }
+  const uint4 k = from_cache<F>(a.kc + from, ks, kp), v = from_cache<F>(a.vc + from, vs, vp);
+  *reinterpret_cast<uint4*>(a.k + row * a.k_row + h * a.k_head + d0) = k;
+  *reinterpret_cast<uint4*>(a.v + row * a.v_row + h * a.v_head + d0) = v;
 }
 
 }  // namespace
 
-const void* cache_write_kernel(int e4m3) {
-  return e4m3 ? (const void*)&cache_write_impl<1> : (const void*)&cache_write_impl<0>;
+const void* cache_write_kernel(int type) {
+  return type == kCacheMxfp4  ? (const void*)&cache_write_impl<kCacheMxfp4>
+         : type == kCacheE4m3 ? (const void*)&cache_write_impl<kCacheE4m3>
+                              : (const void*)&cache_write_impl<kCacheBf16>;
+}
+
+const void* cache_read_kernel(int type) {
+  return type == kCacheMxfp4  ? (const void*)&cache_read_impl<kCacheMxfp4>
+         : type == kCacheE4m3 ? (const void*)&cache_read_impl<kCacheE4m3>
+                              : (const void*)&cache_read_impl<kCacheBf16>;
 }
 
 }  // namespace dspark

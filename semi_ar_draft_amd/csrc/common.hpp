@@ -30,6 +30,7 @@ constexpr int kErrSlot = 512;   // a cache slot outside [-1, n_pages * page_size
 constexpr int kErrHist = 1024;  // a history or bias length outside its array
 constexpr int kErrBias = 2048;  // bias ids that do not ascend
 constexpr int kErrPenalty = 4096;   // a repetition penalty that is not positive and finite
+constexpr int kErrPos = 8192;   // a row position below -1
 
 // What dspark_constrain writes where nothing is allowed: low enough for a
 // weight of zero at any temperature, high enough that scaling and sums of

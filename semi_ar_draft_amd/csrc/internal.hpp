@@ -255,6 +255,12 @@ struct PagesArgs {
 const void* pages_reserve_kernel();
 const void* pages_commit_kernel();
 
+// What a key-value cache holds: bf16, e4m3 with a scale per head, or MXFP4 (e2m1
+// values two a byte, the first in the low half, and a byte b for each 32 of a
+// head's values, their power 2^(b - 127), or 255: a NaN among them; the bytes
+// lie [n_pages][heads][page][d / 32]).
+enum CacheType : int { kCacheBf16 = 0, kCacheE4m3 = 1, kCacheMxfp4 = 2 };
+
 // Cache write (cache.hip): strides in elements.
 struct CacheWriteArgs {
   int64_t n_slots;               // n_pages * page_size
@@ -271,10 +277,76 @@ struct CacheWriteArgs {
   int64_t c_page, c_tok, c_head;
   const float* k_scale;          // [heads], 8-bit cache (nullable: 1)
   const float* v_scale;
+  unsigned char* k_power;        // MXFP4 cache: powers of its blocks, steps of a page and a head in bytes
+  unsigned char* v_power;
+  int64_t s_page, s_head;
+  int blocks;                    // d / 32
   int32_t* err;
 };
 constexpr int kCacheThreads = 256;
-const void* cache_write_kernel(int e4m3);
+const void* cache_write_kernel(int type);
+
+// Rows of a cache back as bf16 (cache.hip): chunks of eight values.
+struct CacheReadArgs {
+  int64_t n_slots;
+  int n_rows, chunks, chunk_shift, page_shift;
+  const int32_t* slot;           // [n_rows], -1 = skip
+  const unsigned char* kc;       // strides in bytes
+  const unsigned char* vc;
+  int64_t c_page, c_tok, c_head;
+  const float* k_scale;
+  const float* v_scale;
+  const unsigned char* k_power;
+  const unsigned char* v_power;
+  int64_t s_page, s_head;
+  int blocks;
+  uint16_t* k;                   // bf16 rows
+  int64_t k_row, k_head;
+  uint16_t* v;
+  int64_t v_row, v_head;
+  int32_t* err;
+};
+const void* cache_read_kernel(int type);
+
+// Rotary positions (rope.hip): strides in elements, a cache's in bytes.
+struct RopeArgs {
+  int n_rows, rows;              // rows of a workgroup: rows * rot / 2 <= kRopeTable
+  int heads_q, heads_k;          // heads turned into rows: of the queries, of the keys (rope alone)
+  int heads_kv;                  // heads that go into a cache
+  int d, rot;
+  unsigned units;                // of a head turned into rows: rot / 16, and (d - rot) / 8 where those are copied
+  unsigned units_inv, heads_inv, heads_kv_inv, pairs_inv;   // 2^32 / units, heads_q + heads_k, heads_kv, rot / 2, rounded up (0 for 1)
+  const int32_t* pos;            // [n_rows], -1 = skip
+  const double* freq;            // [rot / 2] radians a position
+  float factor;
+  const uint16_t* q;
+  int64_t q_row, q_head;
+  uint16_t* qo;
+  int64_t qo_row, qo_head;
+  const uint16_t* k;
+  int64_t k_row, k_head;
+  uint16_t* ko;
+  int64_t ko_row, ko_head;
+  const uint16_t* v;
+  int64_t v_row, v_head;
+  const int32_t* slot;           // [n_rows], -1 = skip
+  int64_t n_slots;
+  int page_shift;
+  unsigned char* kc;
+  unsigned char* vc;
+  int64_t c_page, c_tok, c_head;
+  const float* k_scale;
+  const float* v_scale;
+  unsigned char* k_power;
+  unsigned char* v_power;
+  int64_t s_page, s_head;
+  int32_t* err;
+};
+constexpr int kRopeThreads = 256;
+constexpr int kRopeTable = 512;  // pairs of a workgroup's rows
+constexpr int kRopeMaxD = 1024;
+const void* rope_kernel(int paired);
+const void* rope_write_kernel(int paired, int type);
 
 // Attention of packed rows over the paged cache (attend.hip).
 // A tile to be joined: its request's first row, the rows from its first one
@@ -294,13 +366,16 @@ struct AttendArgs {
   int64_t c_page, c_tok, c_head;
   const float* k_scale;          // [Hkv], e4m3 cache (nullable: 1)
   const float* v_scale;
+  const unsigned char* k_power;  // MXFP4 cache: powers of its blocks, steps of a page and a head in bytes
+  const unsigned char* v_power;
+  int64_t s_page, s_head;
   const int32_t* table;
   int64_t tstride;
   const int32_t* len;
   const int32_t* K;              // nullable: gamma
   const int32_t* offs;           // nullable: b * (gamma + 1)
   float scale2;                  // scale * log2(e)
-  float unrest;                  // 1 / kRestFactor for a bf16 cache, else 1
+  float unrest;                  // 1 / kRestFactor where weights are split in two, else 1
   uint16_t* out;                 // bf16
   int64_t o_row, o_head;
   float* lse;                    // [n_rows][Hq], nullable
@@ -314,7 +389,7 @@ constexpr int kAttendMaxGrid = 512;    // workgroups: one per CU
 constexpr size_t kAttendJoinBytes = kAttendMaxGrid * sizeof(AttendJoin);
 constexpr size_t kAttendPartBytes = kAttendMaxGrid * 2 * 8320 * sizeof(float);   // 16 mt (d + 2) <= 64 * 130
 // mt: 16-row blocks of a tile (1, 2; 4 where d < 256)
-const void* attend_kernel(int d, int mt, int e4m3);
+const void* attend_kernel(int d, int mt, int type);
 const void* attend_join_kernel(int d);
 
 // Logit constraints (constrain.hip): rows (b, i) at b * stride_b + i *
