@@ -553,7 +553,7 @@ int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int head
  * NaN where that byte is 255 (bytes of 253 and 254 are not written; what rows
  * that see such a block get is not defined).
  * With A the largest magnitude of 32 values, their power is the least 2^e with
- * A <= 7 * 2^e, e kept within -120 .. 125, and each becomes the value nearest
+ * A <= 7 * 2^e, e kept within -120 .. 125 (0 where A is 0), and each becomes the value nearest
  * it (ties to the even code; larger ones, infinities too, become 6 * 2^e), so
  * that every value of magnitude up to 7 * 2^125 is off by at most half the
  * distance of its two neighbours.  A block with a NaN has byte 255 and codes
@@ -677,9 +677,10 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
                   void* out, int64_t o_stride_row, int64_t o_stride_head, float* lse);
 
 /* The same over a cache of 4 bits (MXFP4, placed as dspark_cache_write_mxfp4
- * has it).  Keys and values are taken exactly as bf16; weights are rounded by
- * 2^-15 of them at most, as over a bf16 cache.  A value block with byte 255 is
- * NaN to the rows that see its token, a key block makes their results NaN. */
+ * has it).  Keys and values are taken exactly (below 2^-126 as bf16 has them);
+ * weights are rounded as over a bf16 cache, and results are finite for values
+ * up to 2^100.  A value block with byte 255 is NaN to the rows that see its
+ * token, a key block makes their results NaN. */
 int dspark_attend_mxfp4(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads,
                         int d, const void* q, int64_t q_stride_row, int64_t q_stride_head,
                         const void* kcache, const void* vcache,

@@ -39,6 +39,8 @@ def rope(x, pos, freq, interleaved=False, factor=1.0):
 def mxfp4_power(block):
     """Exponent e of a block's power of two (its byte is e + 127)."""
     top = max(abs(float(v)) for v in block)
+    if top == 0:
+        return 0
     if math.isinf(top):
         return 125
     e = -120

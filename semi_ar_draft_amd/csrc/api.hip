@@ -1396,8 +1396,8 @@ int attend_common(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
       return fail(c, DSPARK_ENOMEM, "allocation of %zu bytes failed", kAttendJoinBytes + kAttendPartBytes);
     }
   }
-  const void* fn = attend_kernel(d, mt, cache_type(kv_dtype));
-  const int grid = std::min(kAttendMaxGrid, c->cu_count);
+  const void* fn = attend_kernel(d, mt, cache_type(kv_dtype), page_size);
+  const int grid = std::min(kAttendMaxGrid, c->cu_count * attend_waves(d, mt, cache_type(kv_dtype)));
   AttendArgs a;
   memset(&a, 0, sizeof(a));
   const int64_t size = kv_dtype == DSPARK_BF16 ? 2 : 1;
@@ -1432,7 +1432,7 @@ int attend_common(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   a.K = K;
   a.offs = t_offsets;
   a.scale2 = scale * kLog2e;
-  a.unrest = e4m3 ? 1.0f : 1.0f / kRestFactor;
+  a.unrest = kv_dtype == DSPARK_BF16 ? 1.0f / kRestFactor : 1.0f;
   a.out = static_cast<uint16_t*>(out);
   a.o_row = o_stride_row;
   a.o_head = o_stride_head;

@@ -20,7 +20,7 @@
 // with its neighbours it leaves in memory, and a second launch adds the pieces
 // up in the order of their tokens.
 //
-// One workgroup a CU, one wave a SIMD: its registers hold the next two steps'
+// One workgroup a CU, one wave a SIMD (MXFP4: two, where the registers hold them): its registers hold the next two steps'
 // keys and values in flight (64 to 128 KB a CU), which is what the memory's
 // latency asks for; with more waves the older ones of a SIMD are served first
 // and the younger ones finish alone (measured: two workgroups a CU 139 us
@@ -57,7 +57,11 @@ constexpr int kWaves = kAttendThreads / 64;
 // 1, 119 with 2, 123 with 4; one row of one request of up to 1200 tokens: 14.2 us
 // with at least 1 step, 16.1 with 2 (a wave's first step waits for its loads,
 // the second is nearly free, but so is the wave that would take it).
-constexpr int kTileCost = 1, kMinSteps = 1;
+// Over MXFP4, whose steps are shorter beside it, with the heads' tokens together 58.5 us with a cost of 1, 55.7 with 2,
+// 56.8 with 3.
+template <int F>
+constexpr int kCost = F == kCacheMxfp4 ? 2 : 1;
+constexpr int kMinSteps = 1;
 
 __device__ __forceinline__ f32x4_t mfma(const uint4 a, const uint4 b, const f32x4_t c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b), c, 0,
@@ -86,15 +90,24 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, r);
 }
 
+// A load past the caches, or (KEEP) into them.
+template <bool KEEP, typename T>
+__device__ __forceinline__ T load_as(const unsigned char* p) {
+  if constexpr (KEEP) return *reinterpret_cast<const T*>(p);
+  return __builtin_nontemporal_load(reinterpret_cast<const T*>(p));
+}
+
+template <bool KEEP>
 __device__ __forceinline__ uint2 load8(const unsigned char* p) {
   typedef __attribute__((ext_vector_type(2))) uint32_t u32x2_t;
-  const u32x2_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x2_t*>(p));
+  const u32x2_t v = load_as<KEEP, u32x2_t>(p);
   return make_uint2(v[0], v[1]);
 }
 
+template <bool KEEP>
 __device__ __forceinline__ uint4 load16(const unsigned char* p) {
   typedef __attribute__((ext_vector_type(4))) uint32_t u32x4_t;
-  const u32x4_t v = __builtin_nontemporal_load(reinterpret_cast<const u32x4_t*>(p));
+  const u32x4_t v = load_as<KEEP, u32x4_t>(p);
   return make_uint4(v[0], v[1], v[2], v[3]);
 }
 
@@ -164,18 +177,27 @@ __device__ __forceinline__ Rows request_rows(const AttendArgs& a, P K, P len, P 
   return r;
 }
 
-// Places of the four groups of eight tokens of a step: bytes from the beginning of a cache, and (MXFP4) of its scales.
-template <int F>
+// The places of a step: where its groups of G tokens that a page holds whole (8,
+// or 16 where the pages have them) begin, in bytes from the beginning of a
+// cache and (MXFP4) of its powers.
+template <int F, int G>
 struct At {
-  int64_t v[4];
+  int64_t v[32 / G];
 };
-template <>
-struct At<kCacheMxfp4> {
-  int64_t v[4], s[4];
+template <int G>
+struct At<kCacheMxfp4, G> {
+  int64_t v[32 / G], s[32 / G];
 };
+// The lane's group of half s: uniform where a half is one group, else by `second`.
+template <int G>
+__device__ __forceinline__ int64_t in_half(const int64_t (&at)[32 / G], int s, bool second) {
+  if constexpr (G == 16) return at[s];
+  const int64_t lo = at[2 * s], hi = at[2 * s + 1];
+  return second ? hi : lo;
+}
 
 // Keys and values of a step as a lane has them loaded.
-template <int D, int F>
+template <int D, int F, int G>
 struct Loaded {
   static constexpr bool kBf16 = F == kCacheBf16, kFp4 = F == kCacheMxfp4;
   static constexpr int kBits = kBf16 ? 16 : kFp4 ? 4 : 8;
@@ -184,59 +206,62 @@ struct Loaded {
   static constexpr int VB = D * kBits / 128;             // bytes of a value per lane
   static constexpr int VW = VB < 4 ? 1 : VB / 4;
   static constexpr int NB = D / 32;                      // blocks that share a power of two (MXFP4)
+  // A head of a token that is less than a line of the caches: with tokens
+  // before heads another wave has the line's rest (128 requests of 64 to
+  // 8192 tokens 66.6 us against 69.6, 48 draft blocks with heads of 64 18.9 against 21.1;
+  // of 128 bytes 78.7 against 76.9).
+  static constexpr bool kKeep = D * kBits / 8 < 128;
   uint4 k[2][KW];
   uint32_t v[8][VW];
   uint32_t ks[kFp4 ? 2 : 1][KW];                         // MXFP4: powers of the keys' blocks,
-  uint32_t vs[kFp4 ? 8 : 1];                             // of the values' (words; from take_v on those of the lane's tokens)
+  uint32_t vs[kFp4 ? 8 : 1];                             // of the values' (see take_v)
 
   // A lane's keys: token lane % 16 of either half, `kl` its place in a group.
-  __device__ __forceinline__ void load_k(const unsigned char* kc, const unsigned char* sc, const At<F>& at, unsigned kl,
+  __device__ __forceinline__ void load_k(const unsigned char* kc, const unsigned char* sc, const At<F, G>& at, unsigned kl,
                                          int lane) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int64_t lo = at.v[2 * s], hi = at.v[2 * s + 1];
-      const unsigned char* p = kc + (lane & 8 ? hi : lo) + kl;
+      const unsigned char* p = kc + in_half<G>(at.v, s, lane & 8) + kl;
 #pragma unroll
       for (int w = 0; w < KW; ++w) {
         if constexpr (KB == 8) {
-          const uint2 x = load8(p);
+          const uint2 x = load8<kKeep>(p);
           k[s][w] = make_uint4(x.x, x.y, 0, 0);
         } else {
-          k[s][w] = load16(p + 64 * w);
+          k[s][w] = load16<kKeep>(p + 64 * w);
         }
       }
       if constexpr (kFp4) {
-        const int64_t slo = at.s[2 * s], shi = at.s[2 * s + 1];
-        const unsigned char* ps = sc + (lane & 8 ? shi : slo) + (lane & 7) * NB + (D == 64 ? lane >> 5 : lane >> 4);
+        const unsigned at_s = (unsigned)(lane & (G - 1)) * NB + (D == 64 ? lane >> 5 : lane >> 4);
+        const unsigned char* ps = sc + in_half<G>(at.s, s, lane & 8) + at_s;
 #pragma unroll
         for (int w = 0; w < KW; ++w) ks[s][w] = ps[4 * w];
       }
     }
   }
 
-  // A lane's values: tokens 4 g + i of either half, `vl` the first one's place in its group.
-  __device__ __forceinline__ void load_v(const unsigned char* vc, const unsigned char* sc, const At<F>& at, unsigned vl,
-                                         int64_t c_tok, int lane) {
+  // A lane's values: tokens 4 g + i of either half, `vl` the places of the four in their group.
+  __device__ __forceinline__ void load_v(const unsigned char* vc, const unsigned char* sc, const At<F, G>& at,
+                                         const unsigned (&vl)[4], int lane) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      const int64_t lo = at.v[2 * s], hi = at.v[2 * s + 1];
-      const unsigned char* p = vc + (lane & 32 ? hi : lo) + vl;
+      const unsigned char* p = vc + in_half<G>(at.v, s, lane & 32);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const unsigned char* pt = p + i * c_tok;
+        const unsigned char* pt = p + vl[i];
         uint32_t(&w)[VW] = v[4 * s + i];
         if constexpr (VB == 2) {
-          w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint16_t*>(pt));
+          w[0] = load_as<kKeep, uint16_t>(pt);
         } else if constexpr (VW == 1) {
-          w[0] = __builtin_nontemporal_load(reinterpret_cast<const uint32_t*>(pt));
+          w[0] = load_as<kKeep, uint32_t>(pt);
         } else if constexpr (VW == 2) {
-          const uint2 x = load8(pt);
+          const uint2 x = load8<kKeep>(pt);
           w[0] = x.x;
           w[1] = x.y;
         } else {
 #pragma unroll
           for (int c = 0; c < VW / 4; ++c) {
-            const uint4 x = load16(pt + 16 * c);
+            const uint4 x = load16<kKeep>(pt + 16 * c);
             w[4 * c] = x.x;
             w[4 * c + 1] = x.y;
             w[4 * c + 2] = x.z;
@@ -245,44 +270,32 @@ struct Loaded {
         }
       }
       if constexpr (kFp4) {
-        // the powers of the lane's four tokens: 2, 4 or 8 bytes each, one after the other
-        const int64_t slo = at.s[2 * s], shi = at.s[2 * s + 1];
-        const unsigned char* ps = sc + (lane & 32 ? shi : slo) + 4 * (lane >> 4 & 1) * NB;
-        if constexpr (D == 64) {
-          const uint2 x = *reinterpret_cast<const uint2*>(ps);
-          vs[4 * s] = x.x;
-          vs[4 * s + 1] = x.y;
-        } else if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(ps);
-          vs[4 * s] = x.x;
-          vs[4 * s + 1] = x.y;
-          vs[4 * s + 2] = x.z;
-          vs[4 * s + 3] = x.w;
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) vs[4 * s + i] = *reinterpret_cast<const uint32_t*>(ps + NB * i + (lane & 8 ? 4 : 0));
-        }
+        // the powers of one of the four tokens: take_v exchanges them within the quad
+        const unsigned token = 4 * (lane >> 4 & (G / 4 - 1)) + (lane & 3);
+        const unsigned char* ps = sc + in_half<G>(at.s, s, lane & 32) + token * NB;
+        if constexpr (D == 64) vs[4 * s] = *reinterpret_cast<const uint16_t*>(ps);
+        else vs[4 * s] = *reinterpret_cast<const uint32_t*>(ps + (D == 256 ? lane >> 1 & 4 : 0));
       }
     }
   }
 
-  // MXFP4: from the words of powers to those of the lane's tokens.
+  // MXFP4: the bits of the powers of the lane's tokens, out of what its quad has loaded.
   __device__ __forceinline__ void take_v(int lane) {
     if constexpr (!kFp4) return;
-    const unsigned b = D == 64 ? lane >> 3 & 1 : D == 128 ? lane >> 2 & 3 : lane >> 1 & 3;
-    const unsigned turn = 8 * b + 9;
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-      if constexpr (D == 64) {
-        const uint32_t x = vs[4 * s], y = vs[4 * s + 1];
+      // the byte of the lane's block, which is the quad's where a quad has 32 values at most
+      const unsigned turn = (8 * (D == 64 ? lane >> 3 & 1 : D == 128 ? lane >> 2 & 3 : lane >> 1 & 3) + 9) & 31;
+      const uint32_t w = D == 256 ? vs[4 * s] : __float_as_uint(power_at(vs[4 * s], turn));
+      const uint32_t of[4] = {from_quad<0x00>(w), from_quad<0x55>(w), from_quad<0xAA>(w), from_quad<0xFF>(w)};
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          vs[4 * s + i] = __float_as_uint(power_at(i < 2 ? x : y, i & 1 ? (turn + 16) & 31 : turn));
-      } else {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) vs[4 * s + i] = __float_as_uint(power_at(vs[4 * s + i], turn & 31));
-      }
+      for (int i = 0; i < 4; ++i) vs[4 * s + i] = D == 256 ? __float_as_uint(power_at(of[i], turn)) : of[i];
     }
+  }
+  // x of another lane of the quad (a quad_perm pattern).
+  template <int P>
+  __device__ __forceinline__ static uint32_t from_quad(uint32_t x) {
+    return __builtin_amdgcn_update_dpp(x, x, P, 0xF, 0xF, false);
   }
 
   // Where product ks's values of lane's group begin in a key and a query.
@@ -361,23 +374,24 @@ struct Loaded {
   }
 };
 
-// Where the four groups of eight tokens of a step begin in a cache.  A page
-// holds whole groups; one behind the last token is taken as the last group,
+// Where the groups of a step begin in a cache.  A page holds whole groups; one
+// behind the last token is taken as the last group,
 // and places of a group behind the last token are read and masked.  Page ids
 // are uniform: scalar loads, whose wait is none of the key and value loads'.
+template <int G>
 struct Groups {
-  int id[4];
-  __device__ __forceinline__ static int first(int base, int j, int last) { return min(base + 8 * j, last & ~7); }
+  int id[32 / G];
+  __device__ __forceinline__ static int first(int base, int j, int last) { return min(base + G * j, last & ~(G - 1)); }
   __device__ __forceinline__ void load(const AttendArgs& a, const int32_t* table, int base, int last) {
     const uniform_ptr t = (uniform_ptr)(uintptr_t)table;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) id[j] = t[first(base, j, last) >> a.page_shift];
+    for (int j = 0; j < 32 / G; ++j) id[j] = t[first(base, j, last) >> a.page_shift];
   }
   // The places of the step at `base` whose ids are loaded.
   template <int D, int F>
-  __device__ __forceinline__ void place(const AttendArgs& a, int base, int last, At<F>& at) const {
+  __device__ __forceinline__ void place(const AttendArgs& a, int base, int last, At<F, G>& at) const {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
+    for (int j = 0; j < 32 / G; ++j) {
       int p = id[j];
       if ((unsigned)p >= (unsigned)a.n_pages) {
         atomicOr(a.err, kErrPage);
@@ -390,14 +404,14 @@ struct Groups {
   }
 };
 
-template <int D, int MT, int F>
+template <int D, int MT, int F, int G>
 struct Tile {
-  using In = Loaded<D, F>;
+  using In = Loaded<D, F, G>;
   static constexpr bool E4M3 = F == kCacheE4m3;
   static constexpr int kRows = 16 * MT;
   static constexpr int KS = D / 32;                      // products of 32 values per score
   static constexpr int DT = D / 16;                      // 16-wide blocks of a value row
-  // m stands this far below the row's maximum (in the exponent) when it is set.  The weights of an e4m3 cache
+  // m stands this far below the row's maximum (in the exponent) when it is set.  The weights over an e4m3 cache
   // are f16 in the second product: a row's largest lies between 2^7 and 2^15, below 65504, and what f16 cannot
   // hold of the small ones is 2^-32 of it.  (From maxima of 2^25 on, where a float's step is 4, the largest may lie
   // as low as 2^-8; from 2^28 on, where it is 32, it may pass 65504.)
@@ -435,12 +449,13 @@ struct Tile {
     }
   }
 
-  // Scores, p and sums of the 32 tokens at `base`, in `in`; `tail`: some query
-  // may not see some of them.  next_k and next_v load a later step's keys and
+  // Scores, p and sums of the 32 tokens at `base`, in `in`; `full`: the last
+  // one that every row sees.  next_k and next_v load a later step's keys and
   // values into it once these are used.
   template <typename NextK, typename NextV>
-  __device__ __forceinline__ void step(In& in, int base, bool tail, float sc, int lane, NextK next_k, NextV next_v) {
+  __device__ __forceinline__ void step(In& in, int base, int full, float sc, int lane, NextK next_k, NextV next_v) {
     const int g = lane >> 4;
+    const bool tail = base + kStep - 1 > full;           // some query may not see some of the tokens
     f32x4_t s[MT][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -501,43 +516,60 @@ struct Tile {
         for (int dt = 0; dt < DT; ++dt) o[mt][dt] *= f;
       }
     }
-    // The weights of the second product.  bf16 values: a weight is the sum of
-    // two bf16 numbers, its leading 8 bits and the rest to nearest, off by
-    // 2^-15 of it at most (rounded to one, 2^-8 of it, they cost as much as the
-    // rounding of the result does).  The rest is that of 1 + 2^-16 times the
-    // weight (a.unrest takes the factor out of the result): positive wherever
-    // the weight is, since 0 times an infinite value is NaN.  e4m3 values are
-    // exact in f16, whose 11 bits leave 2^-11 of a weight, far below the
-    // rounding of the values that such a cache holds.
-    uint4 p[MT], rest[E4M3 ? 1 : MT];
+    float e[MT][8];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
-      float e[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[4 * h + i] = fast_exp2(s[mt][h][i]);
-      l[mt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
+        for (int i = 0; i < 4; ++i) e[mt][4 * h + i] = fast_exp2(s[mt][h][i]);
+      const float(&x)[8] = e[mt];
+      l[mt] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+    }
+    // a token that a query does not see must not reach it, but 0 times
+    // infinity or NaN is NaN: such values are left out here and added to the
+    // results that see them at the end
+    uint4 p[MT], rest[E4M3 ? 1 : MT];
+    weights(e, p, rest);
+    in.take_v(lane);
+    if (tail) odd |= in.take_odd();
+    product(in, p, rest);
+    next_v();
+  }
+
+  // The weights of the second product.  bf16 and MXFP4 values: a weight is the sum of two bf16
+  // numbers, its leading 8 bits and the rest to nearest, off by 2^-15 of it
+  // at most (rounded to one, 2^-8 of it, they cost as much as the rounding of
+  // the result does).  Over a bf16 cache the rest is that of 1 + 2^-16 times the
+  // weight (a.unrest takes the factor out of the result): positive wherever
+  // the weight is, since 0 times an infinite value is NaN.  e4m3 values are
+  // exact in f16, whose 11 bits leave 2^-11 of a weight, far below the
+  // rounding of the values that such a cache holds.
+  __device__ __forceinline__ static void weights(const float (&e)[MT][8], uint4 (&p)[MT],
+                                                 uint4 (&rest)[E4M3 ? 1 : MT]) {
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
       uint32_t w[4], x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
+        const float e0 = e[mt][2 * j], e1 = e[mt][2 * j + 1];
         if constexpr (E4M3) {
-          w[j] = pack_f16(e[2 * j], e[2 * j + 1]);
+          w[j] = pack_f16(e0, e1);
         } else {
-          const uint32_t a = __float_as_uint(e[2 * j]), b = __float_as_uint(e[2 * j + 1]);
+          constexpr float kFactor = F == kCacheBf16 ? kRestFactor : 1.0f;
+          const uint32_t a = __float_as_uint(e0), b = __float_as_uint(e1);
           w[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-          x[j] = pack_bf16(__builtin_fmaf(e[2 * j], kRestFactor, -__uint_as_float(a & 0xFFFF0000u)),
-                           __builtin_fmaf(e[2 * j + 1], kRestFactor, -__uint_as_float(b & 0xFFFF0000u)));
+          x[j] = pack_bf16(__builtin_fmaf(e0, kFactor, -__uint_as_float(a & 0xFFFF0000u)),
+                           __builtin_fmaf(e1, kFactor, -__uint_as_float(b & 0xFFFF0000u)));
         }
       }
       p[mt] = make_uint4(w[0], w[1], w[2], w[3]);
       if constexpr (!E4M3) rest[mt] = make_uint4(x[0], x[1], x[2], x[3]);
     }
-    // a token that a query does not see must not reach it, but 0 times
-    // infinity or NaN is NaN: such values are left out here and added to the
-    // results that see them at the end
-    in.take_v(lane);
-    if (tail) odd |= in.take_odd();
+  }
+
+  __device__ __forceinline__ void product(const In& in, const uint4 (&p)[MT],
+                                          const uint4 (&rest)[E4M3 ? 1 : MT]) {
 #pragma unroll
     for (int dt = 0; dt < DT; dt += 2) {
       uint4 f[2];
@@ -554,15 +586,16 @@ struct Tile {
           }
         }
     }
-    next_v();
   }
 };
 
 // Steps loaded ahead: two, or one where two and the sums pass the registers.
 // (More of the small steps cost more at a piece's beginning than they hide: three
 // 24.0, four 26.5 us against 23.4 on 48 draft blocks with heads of 64.)
+// Over MXFP4 with two waves a SIMD one: 69.3 us against 69.6 on 128 requests of
+// 64 to 8192 tokens, 71.5 against 77.3 in pages of 8, where two pass the registers.
 template <int D, int MT, int F>
-constexpr int kAhead = D * MT >= 512 && F == kCacheBf16 ? 1 : 2;
+constexpr int kAhead = (D * MT >= 512 && F == kCacheBf16) || F == kCacheMxfp4 ? 1 : 2;
 
 // A wave's steps s0 .. s1 - 1 of a tile: the rows of request r at cache head h, row tile rt.
 struct Piece {
@@ -573,21 +606,30 @@ struct Piece {
   __device__ __forceinline__ int last() const { return min(s1 * kStep, r.len + r.n) - 1; }
 };
 
-template <int D, int MT, int F>
-__global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArgs a) {
-  using T = Tile<D, MT, F>;
-  using In = Loaded<D, F>;
+template <int D, int MT, int F, int G>
+__global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend_impl(const AttendArgs a) {
+  using T = Tile<D, MT, F, G>;
+  using In = Loaded<D, F, G>;
   constexpr bool E4M3 = F == kCacheE4m3, kFp4 = F == kCacheMxfp4;
-  constexpr int kRows = T::kRows, DT = T::DT;
+  constexpr int kRows = T::kRows, DT = T::DT, kTileCost = kCost<F>;
   __shared__ int64_t sums[kWaves];
   __shared__ Rows start_rows[kWaves];
   __shared__ int start_b[kWaves], start_off[kWaves];
   __shared__ f32x4_t share_o[kWaves - 1][MT * DT][64];    // what waves 1 .. 3 begin with of a tile
   __shared__ float2 share_ml[kWaves - 1][kRows];
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  // a lane's place in a group of eight tokens: its key's and its first value's
-  const unsigned kl = (unsigned)(lane & 7) * (unsigned)a.c_tok + In::KB * (lane >> 4);
-  const unsigned vl = 4 * (lane >> 4 & 1) * (unsigned)a.c_tok + In::VB * (lane & 15);
+  // Workgroups of one XCD (every eighth) have neighbouring stretches: a line of the cache that two heads share
+  // is in its L2 when the second asks (128 requests of 64 to 8192 tokens 62.7 us against 66.7).
+  const int block = kFp4 && gridDim.x % 8 == 0 ? (int)(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8)
+                                               : (int)blockIdx.x;
+  // a lane's places in a group: its key's and its values'
+  const unsigned kl = (unsigned)(lane & (G - 1)) * (unsigned)a.c_tok + In::KB * (lane >> 4);
+  unsigned vl[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const unsigned first = 4 * (lane >> 4 & (G / 4 - 1));
+    vl[i] = (first + i) * (unsigned)a.c_tok + In::VB * (lane & 15);
+  }
 
   // the line: what every request adds to it, and where the four stretches of
   // this workgroup's waves begin
@@ -602,7 +644,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
   Rows r{0, 0, 0, 0};
   for (int b = b0; b < b1; ++b) {
     r = request_rows(a, a.K, a.len, a.offs, b);
-    if (r.bad && blockIdx.x == 0) atomicOr(a.err, r.bad);
+    if (r.bad && block == 0) atomicOr(a.err, r.bad);
     mine += length(r);
   }
   int64_t incl = mine;
@@ -621,9 +663,9 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
   }
   const int64_t workers = (int64_t)gridDim.x * kWaves;
   const int64_t chunk = max((int64_t)kTileCost + kMinSteps, (total + workers - 1) / workers);
-  const int64_t group_chunk = kWaves * chunk, group_u0 = blockIdx.x * group_chunk;
+  const int64_t group_chunk = kWaves * chunk, group_u0 = block * group_chunk;
   if (group_u0 >= total) {
-    if (tid == 0) a.joins[blockIdx.x].n = 0;
+    if (tid == 0) a.joins[block].n = 0;
     return;
   }
   for (int w = 0; w < kWaves; ++w) {
@@ -680,7 +722,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
   };
   // A workgroup leaves at most two pieces in memory: what it begins with and what it ends with.
   auto leave = [&]() {
-    float* part = a.part + (int64_t)(2 * blockIdx.x + (group_u0 < now.real0 - kTileCost ? 1 : 0)) * (kRows * (D + 2));
+    float* part = a.part + (int64_t)(2 * block + (group_u0 < now.real0 - kTileCost ? 1 : 0)) * (kRows * (D + 2));
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
       if (lane < 16) *reinterpret_cast<float2*>(part + 2 * (mt * 16 + lane)) = make_float2(t.m[mt], t.l[mt]);
@@ -720,10 +762,10 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
             j.rows = a.group * r.n - p.rt * kRows;
             j.h = p.h;
             j.rt = p.rt;
-            j.n = (int)((p.real0 + p.n_s - 1) / group_chunk) - (int)blockIdx.x + 2;
-            j.slot = 2 * ((int)blockIdx.x - 1) + (group_u0 - group_chunk < p.real0 - kTileCost ? 1 : 0);
+            j.n = (int)((p.real0 + p.n_s - 1) / group_chunk) - (int)block + 2;
+            j.slot = 2 * (block - 1) + (group_u0 - group_chunk < p.real0 - kTileCost ? 1 : 0);
           }
-          a.joins[blockIdx.x] = j;
+          a.joins[block] = j;
         }
         u += x1 - x0;
         off += x1 - x0;
@@ -738,8 +780,8 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
     };
     constexpr int N = kAhead<D, MT, F>;
     In in[N];
-    Groups ids[N + 1];
-    At<F> at;
+    Groups<G> ids[N + 1];
+    At<F, G> at;
     // a piece's first steps: page ids, then queries, keys and values
     auto ask = [&](const Piece& p) {
 #pragma unroll
@@ -753,7 +795,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
         ids[i].template place<D>(a, (p.s0 + i) * kStep, p.last(), at);
         in[i].load_k(kc, ksc, at, kl, lane);
         if (i == 0) t.load_q(a, p.r, p.h, p.rt, lane);
-        in[i].load_v(vc, vsc, at, vl, a.c_tok, lane);
+        in[i].load_v(vc, vsc, at, vl, lane);
       }
     };
     bool have = take(now);
@@ -771,14 +813,14 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
       const unsigned char *ksc = a.k_power + (int64_t)h * a.s_head, *vsc = a.v_power + (int64_t)h * a.s_head;
       const int full = a.causal ? now.r.len : L - 1;     // tokens up to `full` are seen by every row
       const int last = now.last();
-      Groups id = ids[N];
+      Groups<G> id = ids[N];
       if (have) ask(next);
       int base = now.s0 * kStep;
       for (;;) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           t.step(
-              in[i], base, base + kStep - 1 > full, sc, lane,
+              in[i], base, full, sc, lane,
               [&]() {
                 // (with 64 rows the branch costs more register copies than the loads: those are
                 // the last tokens once more)
@@ -788,7 +830,7 @@ __global__ __launch_bounds__(kAttendThreads, 1) void attend_impl(const AttendArg
                 in[i].load_k(kc, ksc, at, kl, lane);
               },
               [&]() {
-                if (MT == 4 || base + N * kStep <= last) in[i].load_v(vc, vsc, at, vl, a.c_tok, lane);
+                if (MT == 4 || base + N * kStep <= last) in[i].load_v(vc, vsc, at, vl, lane);
               });
           base += kStep;
           if (base > last) goto done;
@@ -936,18 +978,20 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_impl(const AttendA
 }
 
 template <int D, int MT>
-const void* attend_fn(int type) {
-  return type == kCacheMxfp4  ? (const void*)&attend_impl<D, MT, kCacheMxfp4>
-         : type == kCacheE4m3 ? (const void*)&attend_impl<D, MT, kCacheE4m3>
-                              : (const void*)&attend_impl<D, MT, kCacheBf16>;
+const void* attend_fn(int type, int g) {
+  return type == kCacheE4m3   ? (const void*)&attend_impl<D, MT, kCacheE4m3, 8>
+         : type == kCacheBf16 ? (const void*)&attend_impl<D, MT, kCacheBf16, 8>
+         : g == 8             ? (const void*)&attend_impl<D, MT, kCacheMxfp4, 8>
+                              : (const void*)&attend_impl<D, MT, kCacheMxfp4, 16>;
 }
 
 }  // namespace
 
-const void* attend_kernel(int d, int mt, int type) {
-  if (d == 64) return mt == 1 ? attend_fn<64, 1>(type) : mt == 2 ? attend_fn<64, 2>(type) : attend_fn<64, 4>(type);
-  if (d == 128) return mt == 1 ? attend_fn<128, 1>(type) : mt == 2 ? attend_fn<128, 2>(type) : attend_fn<128, 4>(type);
-  return mt == 1 ? attend_fn<256, 1>(type) : attend_fn<256, 2>(type);
+const void* attend_kernel(int d, int mt, int type, int page) {
+  const int g = page < 16 ? 8 : 16;
+  if (d == 64) return mt == 1 ? attend_fn<64, 1>(type, g) : mt == 2 ? attend_fn<64, 2>(type, g) : attend_fn<64, 4>(type, g);
+  if (d == 128) return mt == 1 ? attend_fn<128, 1>(type, g) : mt == 2 ? attend_fn<128, 2>(type, g) : attend_fn<128, 4>(type, g);
+  return mt == 1 ? attend_fn<256, 1>(type, g) : attend_fn<256, 2>(type, g);
 }
 
 const void* attend_join_kernel(int d) {

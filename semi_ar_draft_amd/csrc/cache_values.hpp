@@ -99,7 +99,8 @@ __device__ __forceinline__ uint32_t quad_max(uint32_t x) {
 // or x - 1 where m > 1.75, so every value, the largest too, is off by half
 // the distance of its neighbours at most; e stays within -120 .. 125 (results
 // normal floats, 6 2^e finite; what passes 6 2^125, infinities too, becomes
-// that).  A block with a NaN gets the byte 255 and codes 0.
+// that).  A block of zeros has the power 1, one with a NaN the byte 255 and
+// codes 0.
 __device__ __forceinline__ uint32_t to_mxfp4(const float (&x)[8], unsigned char& power) {
   uint32_t top = 0;
 #pragma unroll
@@ -109,7 +110,7 @@ __device__ __forceinline__ uint32_t to_mxfp4(const float (&x)[8], unsigned char&
   }
   top = quad_max(top);
   int b = (int)((top + 0x1FFFFFu) >> 23) - 2;            // a mantissa above 0.75 carries
-  b = b < 7 ? 7 : b > 252 ? 252 : b;
+  b = top == 0 ? 127 : b < 7 ? 7 : b > 252 ? 252 : b;
   const float p = __uint_as_float((uint32_t)b << 23);
   uint32_t w = 0;
   w = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(w, x[0], x[1], p, 0);   // ties to even, magnitudes above 6 kept at 6

@@ -375,7 +375,7 @@ struct AttendArgs {
   const int32_t* K;              // nullable: gamma
   const int32_t* offs;           // nullable: b * (gamma + 1)
   float scale2;                  // scale * log2(e)
-  float unrest;                  // 1 / kRestFactor where weights are split in two, else 1
+  float unrest;                  // 1 / kRestFactor for a bf16 cache, else 1
   uint16_t* out;                 // bf16
   int64_t o_row, o_head;
   float* lse;                    // [n_rows][Hq], nullable
@@ -388,8 +388,12 @@ constexpr float kRestFactor = 1.0f + 0x1p-16f;   // of a weight's rest beside it
 constexpr int kAttendMaxGrid = 512;    // workgroups: one per CU
 constexpr size_t kAttendJoinBytes = kAttendMaxGrid * sizeof(AttendJoin);
 constexpr size_t kAttendPartBytes = kAttendMaxGrid * 2 * 8320 * sizeof(float);   // 16 mt (d + 2) <= 64 * 130
+// Waves of a SIMD, which is workgroups of a CU.  Over MXFP4 a step is bound by the issue of
+// vector instructions, of which one wave reaches two thirds (16 rows a tile, all in the caches: 115 us with
+// one wave, 95 with two, 97 with three; heads of 256 77 with one, 78 with two).
+constexpr int attend_waves(int d, int mt, int type) { return type == kCacheMxfp4 && d <= 128 && mt <= 2 ? 2 : 1; }
 // mt: 16-row blocks of a tile (1, 2; 4 where d < 256)
-const void* attend_kernel(int d, int mt, int type);
+const void* attend_kernel(int d, int mt, int type, int page);
 const void* attend_join_kernel(int d);
 
 // Logit constraints (constrain.hip): rows (b, i) at b * stride_b + i *

@@ -153,6 +153,50 @@ def check_blocks(s, out, lse, d):
         assert worst_error(dict(t, vc=vc), part, lse, True, 2.0 ** -15, 2.0 ** -60) <= 1.0
 
 
+@pytest.mark.parametrize("step", [-3, -1, 1, 3])
+def test_powers_that_rise_and_fall_along_a_request(ctx, step):
+    """From token to token, by 2^100 in all; values stay below 2^100."""
+    for d, page in ((64, 16), (128, 8), (128, 32), (256, 16)):
+        s = make(15, [70, 8, 333], [3, 0, 1], 2, 4, d, page)
+        for b, (n, k) in enumerate(zip(s["length"], s["K"])):
+            for t in range(n + k + 1):
+                s["vp"][s["table"][b][t // page], :, t % page] = int(np.clip(110 + step * (t // 3), 30, 170))
+        s["vp"][:, 1, :, 0] += 40
+        out, lse = call(ctx, s)
+        ctx.check()
+        check_blocks(s, out, lse, d)
+        # a NaN among them reaches who sees it
+        t2 = dict(s, vp=s["vp"].clone())
+        t2["vp"][s["table"][2][4], 1, 2, 1] = 255
+        t2["vp"][s["table"][0][(s["length"][0] + 2) // page], 0, (s["length"][0] + 2) % page, 0] = 255
+        out2, _ = call(ctx, t2)
+        nan = torch.zeros_like(out, dtype=torch.bool)
+        nan[s["offs"][2]:, 4:, 32:64] = True
+        nan[2:4, :4, :32] = True
+        assert torch.isnan(out2[nan]).all() and torch.isfinite(out2[~nan]).all()
+        # (a block that is NaN has no power: sums may be in another order)
+        assert ((out2 - out)[~nan].abs() <= 2.0 ** -7 * out[~nan].abs()).all()
+
+
+def test_loud_drafts_leave_the_rows_before_them_alone(ctx):
+    """Later drafts whose values are 2^60 larger or smaller: rows that do not see them are as they were."""
+    for d, page in ((64, 8), (128, 16), (256, 32)):
+        for up in (60, -60):
+            s = make(16, [40, 0, 31, 700], [7, 5, 3, 6], 2, 3, d, page)
+            out, lse = call(ctx, s)
+            check(s, out, lse)
+            for b in range(4):
+                t = s["length"][b] + 3
+                s["vp"][s["table"][b][t // page], :, t % page] += up % 256
+            out2, lse2 = call(ctx, s)
+            ctx.check()
+            check_blocks(s, out2, lse2, d)
+            for b in range(4):
+                lo = s["offs"][b]
+                assert torch.equal(lse2[lo:lo + 3], lse[lo:lo + 3])
+                assert ((out2 - out)[lo:lo + 3].abs() <= 2.0 ** -7 * out[lo:lo + 3].abs()).all()
+
+
 def test_large_scores(ctx):
     for spread in (30.0, 300.0):
         s = make(6, [200, 900, 31], [2, 0, 4], 2, 3, 128, 16, spread=spread)
