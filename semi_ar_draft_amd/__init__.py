@@ -714,11 +714,12 @@ class Context:
         themselves.  Returns (q_out, k_out); rows of position -1 are left as
         they are (new ones hold zeros there)."""
         dev = self.device
-        with _on(stream):
-            if q is not None and q_out is None:
-                q_out = torch.zeros(q.shape, dtype=torch.bfloat16, device=dev)
-            if k is not None and k_out is None:
-                k_out = torch.zeros(k.shape, dtype=torch.bfloat16, device=dev)
+        if (q is not None and q_out is None) or (k is not None and k_out is None):
+            with _on(stream):
+                if q is not None and q_out is None:
+                    q_out = torch.zeros(q.shape, dtype=torch.bfloat16, device=dev)
+                if k is not None and k_out is None:
+                    k_out = torch.zeros(k.shape, dtype=torch.bfloat16, device=dev)
         self._rc(self._native.rope(self._h.value, dev.index, _stream(dev, stream), freq, interleaved, factor, row_pos,
                                    k, k_out, q, q_out))
         return q_out, k_out

@@ -1282,8 +1282,7 @@ int rope_args(dspark_ctx* c, RopeArgs& a, int n_rows, int heads_q, int heads, in
   a.qo = static_cast<uint16_t*>(q_out);
   a.qo_row = qo_row;
   a.qo_head = qo_head;
-  // rows of a workgroup: as many as share its sines while every CU has four workgroups
-  a.rows = std::max(1, std::min({4, n_rows / (4 * c->cu_count), kRopeTable / (rot / 2)}));
+  a.rows = 1;
   a.err = c->dev_err;
   return DSPARK_OK;
 }
@@ -2224,6 +2223,10 @@ int dspark_rope_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q
   a.v_power = v_power;
   a.s_head = (int64_t)page_size * (d / 32);
   a.s_page = heads * a.s_head;
+  // Rows of a workgroup: one, or where there are many and their keys are turned in float64 two, which
+  // keep its waves busier (8190 rows of 32 and 8 heads of 128 into e4m3 46.6 us with one, 45.2 with two, 48.4 with four;
+  // into bf16 40.3, 42.0, 46.1)
+  if (kv_dtype != DSPARK_BF16 && n_rows >= 8 * c->cu_count) a.rows = 2;
   const int grid = (n_rows + a.rows - 1) / a.rows;
   return klaunch(c, DSPARK_K_ROPE, rope_write_kernel(interleaved != 0, cache_type(kv_dtype)), dim3(grid),
                  dim3(kRopeThreads), &a, stream);

@@ -620,8 +620,7 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Workgroups of one XCD (every eighth) have neighbouring stretches: a line of the cache that two heads share
   // is in its L2 when the second asks (128 requests of 64 to 8192 tokens 62.7 us against 66.7).
-  const int block = kFp4 && gridDim.x % 8 == 0 ? (int)(blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8)
-                                               : (int)blockIdx.x;
+  const int block = kFp4 && gridDim.x % 8 == 0 ? (int)xcd_block() : (int)blockIdx.x;
   // a lane's places in a group: its key's and its values'
   const unsigned kl = (unsigned)(lane & (G - 1)) * (unsigned)a.c_tok + In::KB * (lane >> 4);
   unsigned vl[4];

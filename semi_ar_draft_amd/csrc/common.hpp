@@ -91,6 +91,10 @@ __device__ __forceinline__ float hash_uniform(uint32_t h) {
   return __builtin_fmaf((float)(h >> 9), 0x1.0p-23f, 0x1.0p-24f);
 }
 
+// The workgroup's place in an order in which each XCD (which has every eighth
+// workgroup) has neighbours; the grid is a multiple of 8.
+__device__ __forceinline__ unsigned xcd_block() { return blockIdx.x % 8 * (gridDim.x / 8) + blockIdx.x / 8; }
+
 __device__ __forceinline__ float fast_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float fast_log2(float x) { return __builtin_amdgcn_logf(x); }
 

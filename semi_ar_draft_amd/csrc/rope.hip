@@ -10,7 +10,11 @@
 // cache rounds to 8 or 4 bits in float64, so that a value near a border between
 // two of those goes to the side of the exact one.
 //
-// Bound by memory.
+// Bound by memory: 16381 rows of 40 heads of 128 62.9 us (335 MB, 5.3 TB/s, a
+// copy of 2 GiB reaches 4.9), 8190 of 32 and 8 heads into a bf16 cache 40.4 (5.0), into e4m3
+// 45.5, into MXFP4 44 (of which the float64 part hides least).  A row a workgroup: its sines, a quarter of
+// its threads' work, pass under the loads of its values, and several
+// workgroups of a CU are at different stages (four rows 69.0 us against 62.4).
 #include "cache_values.hpp"
 
 namespace dspark {
@@ -55,49 +59,84 @@ __device__ __forceinline__ void angles(const RopeArgs& a, int row0, Angle32* t32
   }
 }
 
-// Rows of one tensor's heads turned: unit u < rot / 16 of a head is its pairs
-// 8 u .. 8 u + 7, the others are eight values that stay as they are.
+// Heads of this workgroup's rows turned: unit u < rot / 16 of a head is its
+// pairs 8 u .. 8 u + 7, the others are eight values that stay as they are.  A
+// thread has one unit of every `slots`-th head; a head's values are loaded
+// while the one before it is turned, the first one's while the angles are
+// worked out, whatever the row's position is, which only the store waits for.
 template <bool PAIRED>
-__device__ __forceinline__ void turn_heads(const RopeArgs& a, int row0, const Angle32* t32) {
-  const unsigned heads = a.heads_q + a.heads_k;
-  const unsigned slots = kRopeThreads / a.units;
-  const unsigned first = divide(threadIdx.x, a.units_inv), u = threadIdx.x - first * a.units;
-  if (first >= slots) return;
-  const int turned = a.rot / 16;
-  for (unsigned it = first; it < a.rows * heads; it += slots) {
-    const unsigned r = divide(it, a.heads_inv), head = it - r * heads;
-    const int row = row0 + (int)r;
-    if (row >= a.n_rows || a.pos[row] < 0) continue;
+struct Heads {
+  const RopeArgs& a;
+  const Angle32* t32;
+  int row0;
+  unsigned heads, slots, u, it, row_in;
+  bool turned;
+  int at0, at1;
+  uint16_t* out;                 // of the loaded head; null: none
+  uint4 x0, x1;
+
+  __device__ __forceinline__ Heads(const RopeArgs& a_, const Angle32* t, int row0_) : a(a_), t32(t), row0(row0_) {
+    heads = a.heads_q + a.heads_k;
+    slots = kRopeThreads / a.units;
+    it = divide(threadIdx.x, a.units_inv);
+    u = threadIdx.x - it * a.units;
+    if (it >= slots) it = 1u << 16;                      // a thread too many
+    turned = (int)u < a.rot / 16;
+    at0 = !turned ? a.rot + 8 * ((int)u - a.rot / 16) : PAIRED ? 16 * u : 8 * u;
+    at1 = !turned ? at0 : PAIRED ? at0 + 8 : at0 + a.rot / 2;
+    load();
+  }
+
+  __device__ __forceinline__ void load() {
+    out = nullptr;
+    if (it >= a.rows * heads) return;
+    row_in = divide(it, a.heads_inv);
+    const unsigned head = it - row_in * heads;
+    const int row = row0 + (int)row_in;
+    if (row >= a.n_rows) return;
     const bool is_k = head >= (unsigned)a.heads_q;
     const int64_t h = is_k ? head - a.heads_q : head;
     const uint16_t* in = is_k ? a.k + row * a.k_row + h * a.k_head : a.q + row * a.q_row + h * a.q_head;
-    uint16_t* out = is_k ? a.ko + row * a.ko_row + h * a.ko_head : a.qo + row * a.qo_row + h * a.qo_head;
-    if ((int)u >= turned) {
-      const int at = a.rot + 8 * ((int)u - turned);
-      *reinterpret_cast<uint4*>(out + at) = *reinterpret_cast<const uint4*>(in + at);
-      continue;
-    }
-    const int at0 = PAIRED ? 16 * u : 8 * u, at1 = PAIRED ? 16 * u + 8 : 8 * u + a.rot / 2;
-    float x[2][8], y[2][8];
-    unpack8(*reinterpret_cast<const uint4*>(in + at0), x[0]);
-    unpack8(*reinterpret_cast<const uint4*>(in + at1), x[1]);
-    const Angle32* t = t32 + r * (a.rot / 2) + 8 * u;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const Angle32 w = t[i];
-      if constexpr (PAIRED) {
-        const float x0 = x[i >> 2][2 * (i & 3)], x1 = x[i >> 2][2 * (i & 3) + 1];
-        y[i >> 2][2 * (i & 3)] = turned0(x0, x1, w.c, w.s);
-        y[i >> 2][2 * (i & 3) + 1] = turned1(x0, x1, w.c, w.s);
-      } else {
-        y[0][i] = turned0(x[0][i], x[1][i], w.c, w.s);
-        y[1][i] = turned1(x[0][i], x[1][i], w.c, w.s);
-      }
-    }
-    *reinterpret_cast<uint4*>(out + at0) = pack8(y[0]);
-    *reinterpret_cast<uint4*>(out + at1) = pack8(y[1]);
+    out = is_k ? a.ko + row * a.ko_row + h * a.ko_head : a.qo + row * a.qo_row + h * a.qo_head;
+    x0 = *reinterpret_cast<const uint4*>(in + at0);
+    x1 = *reinterpret_cast<const uint4*>(in + at1);
   }
-}
+
+  // (the angles are there)
+  __device__ __forceinline__ void turn() {
+    while (it < a.rows * heads) {
+      const uint4 w0 = x0, w1 = x1;
+      uint16_t* to = out;
+      const unsigned r = row_in;
+      it += slots;
+      load();
+      if (!to) continue;
+      const Angle32* t = t32 + r * (a.rot / 2) + 8 * u;
+      if (a.pos[row0 + (int)r] < 0) continue;
+      if (!turned) {
+        *reinterpret_cast<uint4*>(to + at0) = w0;
+        continue;
+      }
+      float x[2][8], y[2][8];
+      unpack8(w0, x[0]);
+      unpack8(w1, x[1]);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const Angle32 w = t[i];
+        if constexpr (PAIRED) {
+          const float x0 = x[i >> 2][2 * (i & 3)], x1 = x[i >> 2][2 * (i & 3) + 1];
+          y[i >> 2][2 * (i & 3)] = turned0(x0, x1, w.c, w.s);
+          y[i >> 2][2 * (i & 3) + 1] = turned1(x0, x1, w.c, w.s);
+        } else {
+          y[0][i] = turned0(x[0][i], x[1][i], w.c, w.s);
+          y[1][i] = turned1(x[0][i], x[1][i], w.c, w.s);
+        }
+      }
+      *reinterpret_cast<uint4*>(to + at0) = pack8(y[0]);
+      *reinterpret_cast<uint4*>(to + at1) = pack8(y[1]);
+    }
+  }
+};
 
 // Eight turned values of a key, from those eight (x) and (halves) their
 // partners (xp): values 8 c .. of a head.
@@ -145,71 +184,103 @@ __device__ __forceinline__ uint2 to_e4m3_wide(const double (&y)[8], double s) {
   return make_uint2(w[0], w[1]);
 }
 
-// Keys turned and values as they are into the cache, eight of each a thread.
+// Keys turned and values as they are into the cache, eight of each a thread;
+// loaded as the heads above are.
 template <bool PAIRED, int F>
-__device__ __forceinline__ void write_heads(const RopeArgs& a, int row0, const Angle32* t32, const Angle64* t64) {
-  const unsigned chunks = a.d / 8;                       // 8, 16 or 32: a quad's threads have one token and head
-  const unsigned slots = kRopeThreads / chunks;
-  const int c = threadIdx.x & (chunks - 1);
-  for (unsigned it = threadIdx.x / chunks; it < a.rows * (unsigned)a.heads_kv; it += slots) {
-    const unsigned r = divide(it, a.heads_kv_inv), h = it - r * a.heads_kv;
-    const int row = row0 + (int)r;
-    if (row >= a.n_rows || a.pos[row] < 0) continue;
-    const int slot = a.slot[row];
-    if (slot < 0 || slot >= a.n_slots) {
-      if (slot != -1 && c == 0 && h == 0) atomicOr(a.err, kErrSlot);
-      continue;
-    }
-    const int page = slot >> a.page_shift, place = slot & ((1 << a.page_shift) - 1);
-    const int64_t to = (int64_t)page * a.c_page + (int64_t)place * a.c_tok + (int64_t)h * a.c_head;
-    const uint16_t* kp = a.k + row * a.k_row + h * a.k_head;
-    const uint4 xk = *reinterpret_cast<const uint4*>(kp + 8 * c);
-    const uint4 xv = *reinterpret_cast<const uint4*>(a.v + row * a.v_row + h * a.v_head + 8 * c);
+struct CacheHeads {
+  const RopeArgs& a;
+  int row0, c;
+  unsigned slots, it, row_in, h;
+  bool there;
+  uint4 xk, xo, xv;
+
+  __device__ __forceinline__ CacheHeads(const RopeArgs& a_, int row0_) : a(a_), row0(row0_) {
+    const unsigned chunks = a.d / 8;                     // 8, 16 or 32: a quad's threads have one token and head
+    slots = kRopeThreads / chunks;
+    c = threadIdx.x & (chunks - 1);
+    it = threadIdx.x / chunks;
+    load();
+  }
+
+  __device__ __forceinline__ void load() {
+    there = false;
+    if (it >= a.rows * (unsigned)a.heads_kv) return;
+    row_in = divide(it, a.heads_kv_inv);
+    h = it - row_in * a.heads_kv;
+    const int row = row0 + (int)row_in;
+    if (row >= a.n_rows) return;
+    there = true;
     const int half = a.rot / 16;
-    uint4 xo = xk;
-    if (!PAIRED && c < 2 * half) xo = *reinterpret_cast<const uint4*>(kp + 8 * (c < half ? c + half : c - half));
-    float x[8], xp[8], v[8];
-    unpack8(xk, x);
-    unpack8(xo, xp);
-    const unsigned row_t = r * (a.rot / 2);
-    if constexpr (F == kCacheBf16) {
-      float y[8];
-      turn_chunk<PAIRED>(a, c, x, xp, t32 + row_t, y);
-      *reinterpret_cast<uint4*>(a.kc + to + 16 * c) = c < 2 * half ? pack8(y) : xk;
-      *reinterpret_cast<uint4*>(a.vc + to + 16 * c) = xv;
-    } else {
-      double y[8];
-      turn_chunk<PAIRED>(a, c, x, xp, t64 + row_t, y);
-      unpack8(xv, v);
-      if constexpr (F == kCacheE4m3) {
-        const float ks = a.k_scale ? a.k_scale[h] : 1.0f, vs = a.v_scale ? a.v_scale[h] : 1.0f;
-        *reinterpret_cast<uint2*>(a.kc + to + 8 * c) = to_e4m3_wide(y, (double)ks);
-        *reinterpret_cast<uint2*>(a.vc + to + 8 * c) = to_e4m3(v, vs, 1.0f / vs);
+    const uint16_t* kp = a.k + row * a.k_row + h * a.k_head;
+    xk = *reinterpret_cast<const uint4*>(kp + 8 * c);
+    xv = *reinterpret_cast<const uint4*>(a.v + row * a.v_row + h * a.v_head + 8 * c);
+    // (halves: the partners of the pairs)
+    const int co = PAIRED || c >= 2 * half ? c : c < half ? c + half : c - half;
+    xo = *reinterpret_cast<const uint4*>(kp + 8 * co);
+  }
+
+  __device__ __forceinline__ void write(const Angle32* t32, const Angle64* t64) {
+    const int half = a.rot / 16;
+    while (it < a.rows * (unsigned)a.heads_kv) {
+      const uint4 wk = xk, wo = xo, wv = xv;
+      const unsigned r = row_in, head = h;
+      const bool now = there;
+      it += slots;
+      load();
+      if (!now) continue;
+      const int row = row0 + (int)r;
+      const int slot = a.slot[row];
+      if (a.pos[row] < 0) continue;
+      if (slot < 0 || slot >= a.n_slots) {
+        if (slot != -1 && c == 0 && head == 0) atomicOr(a.err, kErrSlot);
+        continue;
+      }
+      const int page = slot >> a.page_shift, place = slot & ((1 << a.page_shift) - 1);
+      const int64_t to = (int64_t)page * a.c_page + (int64_t)place * a.c_tok + (int64_t)head * a.c_head;
+      float x[8], xp[8], v[8];
+      unpack8(wk, x);
+      unpack8(wo, xp);
+      const unsigned row_t = r * (a.rot / 2);
+      if constexpr (F == kCacheBf16) {
+        float y[8];
+        turn_chunk<PAIRED>(a, c, x, xp, t32 + row_t, y);
+        *reinterpret_cast<uint4*>(a.kc + to + 16 * c) = c < 2 * half ? pack8(y) : wk;
+        *reinterpret_cast<uint4*>(a.vc + to + 16 * c) = wv;
       } else {
-        float z[8];
+        double y[8];
+        turn_chunk<PAIRED>(a, c, x, xp, t64 + row_t, y);
+        unpack8(wv, v);
+        if constexpr (F == kCacheE4m3) {
+          const float ks = a.k_scale ? a.k_scale[head] : 1.0f, vs = a.v_scale ? a.v_scale[head] : 1.0f;
+          *reinterpret_cast<uint2*>(a.kc + to + 8 * c) = to_e4m3_wide(y, (double)ks);
+          *reinterpret_cast<uint2*>(a.vc + to + 8 * c) = to_e4m3(v, vs, 1.0f / vs);
+        } else {
+          float z[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] = to_odd(y[i]);
-        unsigned char pk, pv;
-        const uint32_t wk = to_mxfp4(z, pk), wv = to_mxfp4(v, pv);
-        *reinterpret_cast<uint32_t*>(a.kc + to + 4 * c) = wk;
-        *reinterpret_cast<uint32_t*>(a.vc + to + 4 * c) = wv;
-        if ((c & 3) == 0) {
-          const int64_t at = page * a.s_page + h * a.s_head + (int64_t)place * (a.d / 32) + c / 4;
-          a.k_power[at] = pk;
-          a.v_power[at] = pv;
+          for (int i = 0; i < 8; ++i) z[i] = to_odd(y[i]);
+          unsigned char pk, pv;
+          const uint32_t codes_k = to_mxfp4(z, pk), codes_v = to_mxfp4(v, pv);
+          *reinterpret_cast<uint32_t*>(a.kc + to + 4 * c) = codes_k;
+          *reinterpret_cast<uint32_t*>(a.vc + to + 4 * c) = codes_v;
+          if ((c & 3) == 0) {
+            const int64_t at = page * a.s_page + head * a.s_head + (int64_t)place * (a.d / 32) + c / 4;
+            a.k_power[at] = pk;
+            a.v_power[at] = pv;
+          }
         }
       }
     }
   }
-}
+};
 
 template <bool PAIRED>
 __global__ __launch_bounds__(kRopeThreads) void rope_impl(const RopeArgs a) {
   __shared__ Angle32 t32[kRopeTable];
   const int row0 = blockIdx.x * a.rows;
+  Heads<PAIRED> heads(a, t32, row0);
   angles<false>(a, row0, t32, nullptr);
   __syncthreads();
-  turn_heads<PAIRED>(a, row0, t32);
+  heads.turn();
 }
 
 template <bool PAIRED, int F>
@@ -218,10 +289,12 @@ __global__ __launch_bounds__(kRopeThreads) void rope_write_impl(const RopeArgs a
   __shared__ Angle32 t32[kRopeTable];
   __shared__ Angle64 t64[kWide ? kRopeTable : 1];
   const int row0 = blockIdx.x * a.rows;
+  CacheHeads<PAIRED, F> cache(a, row0);
+  Heads<PAIRED> heads(a, t32, row0);
   angles<kWide>(a, row0, t32, t64);
   __syncthreads();
-  if (a.heads_q > 0) turn_heads<PAIRED>(a, row0, t32);
-  write_heads<PAIRED, F>(a, row0, t32, t64);
+  cache.write(t32, t64);
+  heads.turn();
 }
 
 template <bool PAIRED>
