@@ -1282,7 +1282,10 @@ int rope_args(dspark_ctx* c, RopeArgs& a, int n_rows, int heads_q, int heads, in
   a.qo = static_cast<uint16_t*>(q_out);
   a.qo_row = qo_row;
   a.qo_head = qo_head;
-  a.rows = 1;
+  // rows of a workgroup: one, or as many as a grid of at most 2^32 threads needs
+  a.rows = (int)(((int64_t)n_rows + kRopeMaxGrid - 1) / kRopeMaxGrid);
+  if (n_rows > INT32_MAX - kRopeTable || a.rows * (rot / 2) > kRopeTable || a.rows * ((int64_t)heads_q + heads) >= 1 << 16)
+    return fail(c, DSPARK_EINVAL, "too many rows (%d)", n_rows);
   a.err = c->dev_err;
   return DSPARK_OK;
 }
@@ -2226,7 +2229,7 @@ int dspark_rope_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q
   // Rows of a workgroup: one, or where there are many and their keys are turned in float64 two, which
   // keep its waves busier (8190 rows of 32 and 8 heads of 128 into e4m3 46.6 us with one, 45.2 with two, 48.4 with four;
   // into bf16 40.3, 42.0, 46.1)
-  if (kv_dtype != DSPARK_BF16 && n_rows >= 8 * c->cu_count) a.rows = 2;
+  if (kv_dtype != DSPARK_BF16 && n_rows >= 8 * c->cu_count) a.rows = std::max(a.rows, 2);
   const int grid = (n_rows + a.rows - 1) / a.rows;
   return klaunch(c, DSPARK_K_ROPE, rope_write_kernel(interleaved != 0, cache_type(kv_dtype)), dim3(grid),
                  dim3(kRopeThreads), &a, stream);

@@ -344,6 +344,7 @@ struct RopeArgs {
 };
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTable = 512;  // pairs of a workgroup's rows
+constexpr int kRopeMaxGrid = 1 << 23;   // workgroups: fewer than 2^32 threads
 constexpr int kRopeMaxD = 1024;
 const void* rope_kernel(int paired);
 const void* rope_write_kernel(int paired, int type);

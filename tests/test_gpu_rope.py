@@ -339,3 +339,24 @@ def test_another_stream_and_a_captured_graph(ctx):
         torch.cuda.synchronize()
         assert all([torch.equal(a, b) for a, b in zip(eager, (q_out, *back, kc, vc, ks, vs))])
     ctx.check()
+
+
+def test_timing_class_and_many_rows(ctx):
+    """Counted as launches of the rope class; more rows than a workgroup each would have threads for."""
+    n = (1 << 23) + 5
+    q = torch.ones((n, 1, 16), dtype=torch.bfloat16, device="cuda")
+    q[n - 1] = 2
+    pos = torch.zeros(n, dtype=torch.int32, device="cuda")
+    pos[n - 1] = 3
+    freq = torch.full((8,), np.pi / 2, dtype=torch.float64, device="cuda")
+    ctx.timing(True)
+    ctx.read_timing()
+    ctx.rope(q, None, pos, freq, q_out=q)
+    assert ctx.read_timing()["rope"][1] == 1
+    ctx.timing(False)
+    ctx.check()
+    assert (q[:-1] == 1).all()
+    assert torch.equal(q[n - 1, 0], torch.tensor([2.0] * 8 + [-2.0] * 8, dtype=torch.bfloat16, device="cuda"))
+    wide = torch.ones((1, 1, 1024), dtype=torch.bfloat16, device="cuda").expand(n, 1, 1024)
+    refused(lambda: ctx.rope(wide, None, pos, torch.zeros(512, dtype=torch.float64, device="cuda"),
+                             q_out=torch.empty((n, 1, 1024), dtype=torch.bfloat16, device="cuda")), "too many rows")
