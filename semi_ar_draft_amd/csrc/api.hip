@@ -1270,7 +1270,6 @@ int rope_args(dspark_ctx* c, RopeArgs& a, int n_rows, int heads_q, int heads, in
   memset(&a, 0, sizeof(a));
   a.n_rows = n_rows;
   a.heads_q = heads_q;
-  a.d = d;
   a.rot = rot;
   a.pairs_inv = inverse(rot / 2);
   a.pos = row_pos;
@@ -1313,8 +1312,9 @@ int cache_write_common(dspark_ctx* c, hipStream_t stream, int n_rows, int heads,
   DeviceGuard dg(c->device);
   if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
   const int64_t size = kv_dtype == DSPARK_BF16 ? 2 : 1;
-  CacheWriteArgs a;
-  memset(&a, 0, sizeof(a));
+  CacheWritePowers p;
+  memset(&p, 0, sizeof(p));
+  CacheWriteArgs& a = p.w;
   a.n_slots = (int64_t)n_pages << sh;
   a.n_rows = n_rows;
   a.heads = heads;
@@ -1335,14 +1335,14 @@ int cache_write_common(dspark_ctx* c, hipStream_t stream, int n_rows, int heads,
   a.c_head = c_stride_head * size;
   a.k_scale = k_scale;
   a.v_scale = v_scale;
-  a.k_power = k_power;
-  a.v_power = v_power;
-  a.blocks = d / 32;
-  a.s_head = (int64_t)page_size * a.blocks;
-  a.s_page = heads * a.s_head;
+  p.k_power = k_power;
+  p.v_power = v_power;
+  p.blocks = d / 32;
+  p.s_head = (int64_t)page_size * p.blocks;
+  p.s_page = heads * p.s_head;
   a.err = c->dev_err;
   const int grid = (n_rows * a.chunks + kCacheThreads - 1) / kCacheThreads;
-  return klaunch(c, DSPARK_K_CACHE, cache_write_kernel(cache_type(kv_dtype)), dim3(grid), dim3(kCacheThreads), &a, stream);
+  return klaunch(c, DSPARK_K_CACHE, cache_write_kernel(cache_type(kv_dtype)), dim3(grid), dim3(kCacheThreads), &p, stream);
 }
 
 int attend_common(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads, int d,
@@ -1422,12 +1422,8 @@ int attend_common(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   a.c_page = c_stride_page * size;
   a.c_tok = c_stride_tok * size;
   a.c_head = c_stride_head * size;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.k_power = k_power;
-  a.v_power = v_power;
-  a.s_head = (int64_t)page_size * (d / 32);
-  a.s_page = heads * a.s_head;
+  a.k_scale = k_power ? reinterpret_cast<const float*>(k_power) : k_scale;
+  a.v_scale = v_power ? reinterpret_cast<const float*>(v_power) : v_scale;
   a.table = table;
   a.tstride = table_stride;
   a.len = len;
@@ -1443,6 +1439,7 @@ int attend_common(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
   a.part = reinterpret_cast<float*>(c->attend_buf + kAttendJoinBytes);
   a.err = c->dev_err;
   if ((rc = klaunch(c, DSPARK_K_ATTEND, fn, dim3(grid), dim3(kAttendThreads), &a, stream))) return rc;
+  a.v_scale = v_scale;
   return klaunch(c, DSPARK_K_ATTEND, attend_join_kernel(d), dim3(grid, mt), dim3(kAttendThreads), &a, stream);
 }
 
@@ -2188,7 +2185,9 @@ int dspark_rope_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q
   if ((rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype)))
     return rc;
   if ((rc = check_scales(c, kv_dtype, k_scale, v_scale, k_power, v_power))) return rc;
-  RopeArgs a;
+  RopeWriteArgs p;
+  memset(&p, 0, sizeof(p));
+  RopeArgs& a = p.r;
   rc = rope_args(c, a, n_rows, heads_q, heads, d, rot, row_pos, freq, factor, q, q_stride_row, q_stride_head, q_out,
                  qo_stride_row, qo_stride_head);
   if (rc) return rc;
@@ -2202,37 +2201,38 @@ int dspark_rope_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q
   if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
   const int64_t size = kv_dtype == DSPARK_BF16 ? 2 : 1;
   a.heads_inv = inverse(heads_q);
-  a.heads_kv = heads;
-  a.heads_kv_inv = inverse(heads);
+  p.d = d;
+  p.heads_kv = heads;
+  p.heads_kv_inv = inverse(heads);
   a.units = rot / 16 + (q == q_out ? 0 : (d - rot) / 8);
   a.units_inv = inverse(a.units);
   a.k = static_cast<const uint16_t*>(k);
   a.k_row = k_stride_row;
   a.k_head = k_stride_head;
-  a.v = static_cast<const uint16_t*>(v);
-  a.v_row = v_stride_row;
-  a.v_head = v_stride_head;
-  a.slot = row_slot;
-  a.page_shift = page_shift(page_size);
-  a.n_slots = (int64_t)n_pages << a.page_shift;
-  a.kc = static_cast<unsigned char*>(kcache);
-  a.vc = static_cast<unsigned char*>(vcache);
-  a.c_page = c_stride_page * size;
-  a.c_tok = c_stride_tok * size;
-  a.c_head = c_stride_head * size;
-  a.k_scale = k_scale;
-  a.v_scale = v_scale;
-  a.k_power = k_power;
-  a.v_power = v_power;
-  a.s_head = (int64_t)page_size * (d / 32);
-  a.s_page = heads * a.s_head;
+  p.v = static_cast<const uint16_t*>(v);
+  p.v_row = v_stride_row;
+  p.v_head = v_stride_head;
+  p.slot = row_slot;
+  p.page_shift = page_shift(page_size);
+  p.n_slots = (int64_t)n_pages << p.page_shift;
+  p.kc = static_cast<unsigned char*>(kcache);
+  p.vc = static_cast<unsigned char*>(vcache);
+  p.c_page = c_stride_page * size;
+  p.c_tok = c_stride_tok * size;
+  p.c_head = c_stride_head * size;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.k_power = k_power;
+  p.v_power = v_power;
+  p.s_head = (int64_t)page_size * (d / 32);
+  p.s_page = heads * p.s_head;
   // Rows of a workgroup: one, or where there are many and their keys are turned in float64 two, which
   // keep its waves busier (8190 rows of 32 and 8 heads of 128 into e4m3 46.6 us with one, 45.2 with two, 48.4 with four;
   // into bf16 40.3, 42.0, 46.1)
   if (kv_dtype != DSPARK_BF16 && n_rows >= 8 * c->cu_count) a.rows = std::max(a.rows, 2);
   const int grid = (n_rows + a.rows - 1) / a.rows;
   return klaunch(c, DSPARK_K_ROPE, rope_write_kernel(interleaved != 0, cache_type(kv_dtype)), dim3(grid),
-                 dim3(kRopeThreads), &a, stream);
+                 dim3(kRopeThreads), &p, stream);
 }
 
 int dspark_attend(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads, int d,

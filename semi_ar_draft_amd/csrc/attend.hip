@@ -210,7 +210,7 @@ struct Loaded {
   // before heads another wave has the line's rest (128 requests of 64 to
   // 8192 tokens 66.6 us against 69.6, 48 draft blocks with heads of 64 18.9 against 21.1;
   // of 128 bytes 78.7 against 76.9).
-  static constexpr bool kKeep = D * kBits / 8 < 128;
+  static constexpr bool kKeep = kFp4 && D * kBits / 8 < 128;
   uint4 k[2][KW];
   uint32_t v[8][VW];
   uint32_t ks[kFp4 ? 2 : 1][KW];                         // MXFP4: powers of the keys' blocks,
@@ -240,15 +240,16 @@ struct Loaded {
     }
   }
 
-  // A lane's values: tokens 4 g + i of either half, `vl` the places of the four in their group.
+  // A lane's values: tokens 4 g + i of either half, `vl` the first one's place in its group.
   __device__ __forceinline__ void load_v(const unsigned char* vc, const unsigned char* sc, const At<F, G>& at,
-                                         const unsigned (&vl)[4], int lane) {
+                                         unsigned vl, int64_t c_tok, int lane) {
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
       const unsigned char* p = vc + in_half<G>(at.v, s, lane & 32);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const unsigned char* pt = p + vl[i];
+        // (groups of 16: a uniform address and 32 bits of a lane's own)
+        const unsigned char* pt = G == 16 ? p + (vl + i * (unsigned)c_tok) : p + vl + i * c_tok;
         uint32_t(&w)[VW] = v[4 * s + i];
         if constexpr (VB == 2) {
           w[0] = load_as<kKeep, uint16_t>(pt);
@@ -397,9 +398,9 @@ struct Groups {
         atomicOr(a.err, kErrPage);
         p = 0;
       }
-      const int place = first(base, j, last) & ((1 << a.page_shift) - 1);
-      at.v[j] = (int64_t)p * a.c_page + (int64_t)place * a.c_tok;
-      if constexpr (F == kCacheMxfp4) at.s[j] = (int64_t)p * a.s_page + place * (D / 32);
+      at.v[j] = (int64_t)p * a.c_page + (int64_t)(first(base, j, last) & ((1 << a.page_shift) - 1)) * a.c_tok;
+      if constexpr (F == kCacheMxfp4)
+        at.s[j] = (((int64_t)p * a.Hkv << a.page_shift) + (first(base, j, last) & ((1 << a.page_shift) - 1))) * (D / 32);
     }
   }
 };
@@ -449,13 +450,12 @@ struct Tile {
     }
   }
 
-  // Scores, p and sums of the 32 tokens at `base`, in `in`; `full`: the last
-  // one that every row sees.  next_k and next_v load a later step's keys and
+  // Scores, p and sums of the 32 tokens at `base`, in `in`; `tail`: some query
+  // may not see some of them.  next_k and next_v load a later step's keys and
   // values into it once these are used.
   template <typename NextK, typename NextV>
-  __device__ __forceinline__ void step(In& in, int base, int full, float sc, int lane, NextK next_k, NextV next_v) {
+  __device__ __forceinline__ void step(In& in, int base, bool tail, float sc, int lane, NextK next_k, NextV next_v) {
     const int g = lane >> 4;
-    const bool tail = base + kStep - 1 > full;           // some query may not see some of the tokens
     f32x4_t s[MT][2];
 #pragma unroll
     for (int h = 0; h < 2; ++h)
@@ -516,60 +516,47 @@ struct Tile {
         for (int dt = 0; dt < DT; ++dt) o[mt][dt] *= f;
       }
     }
-    float e[MT][8];
+    // The weights of the second product.  bf16 and MXFP4 values: a weight is the sum of
+    // two bf16 numbers, its leading 8 bits and the rest to nearest, off by
+    // 2^-15 of it at most (rounded to one, 2^-8 of it, they cost as much as the
+    // rounding of the result does).  Over a bf16 cache the rest is that of 1 + 2^-16 times the
+    // weight (a.unrest takes the factor out of the result): positive wherever
+    // the weight is, since 0 times an infinite value is NaN.  e4m3 values are
+    // exact in f16, whose 11 bits leave 2^-11 of a weight, far below the
+    // rounding of the values that such a cache holds.  (MXFP4 values are not, for their powers: where those
+    // of a step span no more than f16 does, one product would do, 109 us against 119 on 6 requests of 60000
+    // to 131000 tokens, 69.5 against 69.3 on 128 of 64 to 8192; but a way around for the others costs
+    // the common case more than that.)
+    uint4 p[MT], rest[E4M3 ? 1 : MT];
 #pragma unroll
     for (int mt = 0; mt < MT; ++mt) {
+      float e[8];
 #pragma unroll
       for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) e[mt][4 * h + i] = fast_exp2(s[mt][h][i]);
-      const float(&x)[8] = e[mt];
-      l[mt] += ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-    }
-    // a token that a query does not see must not reach it, but 0 times
-    // infinity or NaN is NaN: such values are left out here and added to the
-    // results that see them at the end
-    uint4 p[MT], rest[E4M3 ? 1 : MT];
-    weights(e, p, rest);
-    in.take_v(lane);
-    if (tail) odd |= in.take_odd();
-    product(in, p, rest);
-    next_v();
-  }
-
-  // The weights of the second product.  bf16 and MXFP4 values: a weight is the sum of two bf16
-  // numbers, its leading 8 bits and the rest to nearest, off by 2^-15 of it
-  // at most (rounded to one, 2^-8 of it, they cost as much as the rounding of
-  // the result does).  Over a bf16 cache the rest is that of 1 + 2^-16 times the
-  // weight (a.unrest takes the factor out of the result): positive wherever
-  // the weight is, since 0 times an infinite value is NaN.  e4m3 values are
-  // exact in f16, whose 11 bits leave 2^-11 of a weight, far below the
-  // rounding of the values that such a cache holds.
-  __device__ __forceinline__ static void weights(const float (&e)[MT][8], uint4 (&p)[MT],
-                                                 uint4 (&rest)[E4M3 ? 1 : MT]) {
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+        for (int i = 0; i < 4; ++i) e[4 * h + i] = fast_exp2(s[mt][h][i]);
+      l[mt] += ((e[0] + e[1]) + (e[2] + e[3])) + ((e[4] + e[5]) + (e[6] + e[7]));
       uint32_t w[4], x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float e0 = e[mt][2 * j], e1 = e[mt][2 * j + 1];
         if constexpr (E4M3) {
-          w[j] = pack_f16(e0, e1);
+          w[j] = pack_f16(e[2 * j], e[2 * j + 1]);
         } else {
           constexpr float kFactor = F == kCacheBf16 ? kRestFactor : 1.0f;
-          const uint32_t a = __float_as_uint(e0), b = __float_as_uint(e1);
+          const uint32_t a = __float_as_uint(e[2 * j]), b = __float_as_uint(e[2 * j + 1]);
           w[j] = __builtin_amdgcn_perm(b, a, 0x07060302u);
-          x[j] = pack_bf16(__builtin_fmaf(e0, kFactor, -__uint_as_float(a & 0xFFFF0000u)),
-                           __builtin_fmaf(e1, kFactor, -__uint_as_float(b & 0xFFFF0000u)));
+          x[j] = pack_bf16(__builtin_fmaf(e[2 * j], kFactor, -__uint_as_float(a & 0xFFFF0000u)),
+                           __builtin_fmaf(e[2 * j + 1], kFactor, -__uint_as_float(b & 0xFFFF0000u)));
         }
       }
       p[mt] = make_uint4(w[0], w[1], w[2], w[3]);
       if constexpr (!E4M3) rest[mt] = make_uint4(x[0], x[1], x[2], x[3]);
     }
-  }
-
-  __device__ __forceinline__ void product(const In& in, const uint4 (&p)[MT],
-                                          const uint4 (&rest)[E4M3 ? 1 : MT]) {
+    // a token that a query does not see must not reach it, but 0 times
+    // infinity or NaN is NaN: such values are left out here and added to the
+    // results that see them at the end
+    in.take_v(lane);
+    if (tail) odd |= in.take_odd();
 #pragma unroll
     for (int dt = 0; dt < DT; dt += 2) {
       uint4 f[2];
@@ -586,6 +573,7 @@ struct Tile {
           }
         }
     }
+    next_v();
   }
 };
 
@@ -620,15 +608,10 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
   const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   // Workgroups of one XCD (every eighth) have neighbouring stretches: a line of the cache that two heads share
   // is in its L2 when the second asks (128 requests of 64 to 8192 tokens 62.7 us against 66.7).
-  const int block = kFp4 && gridDim.x % 8 == 0 ? (int)xcd_block() : (int)blockIdx.x;
-  // a lane's places in a group: its key's and its values'
+  const unsigned block = kFp4 && gridDim.x % 8 == 0 ? xcd_block() : blockIdx.x;
+  // a lane's place in a group: its key's and its first value's
   const unsigned kl = (unsigned)(lane & (G - 1)) * (unsigned)a.c_tok + In::KB * (lane >> 4);
-  unsigned vl[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const unsigned first = 4 * (lane >> 4 & (G / 4 - 1));
-    vl[i] = (first + i) * (unsigned)a.c_tok + In::VB * (lane & 15);
-  }
+  const unsigned vl = 4 * (lane >> 4 & (G / 4 - 1)) * (unsigned)a.c_tok + In::VB * (lane & 15);
 
   // the line: what every request adds to it, and where the four stretches of
   // this workgroup's waves begin
@@ -684,6 +667,10 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
     start_rows[w] = r;
   }
   __syncthreads();
+  // MXFP4: powers, [n_pages][Hkv][page][D / 32]
+  const unsigned char* k_power = reinterpret_cast<const unsigned char*>(a.k_scale);
+  const unsigned char* v_power = reinterpret_cast<const unsigned char*>(a.v_scale);
+  const int64_t power_head = (int64_t)(D / 32) << a.page_shift;
   auto uniform = [](int x) { return __builtin_amdgcn_readfirstlane(x); };
   const int64_t u0 = group_u0 + wave * chunk, u1 = min(total, u0 + chunk);
   const uniform_ptr uK = (uniform_ptr)(uintptr_t)a.K, ulen = (uniform_ptr)(uintptr_t)a.len,
@@ -762,7 +749,7 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
             j.h = p.h;
             j.rt = p.rt;
             j.n = (int)((p.real0 + p.n_s - 1) / group_chunk) - (int)block + 2;
-            j.slot = 2 * (block - 1) + (group_u0 - group_chunk < p.real0 - kTileCost ? 1 : 0);
+            j.slot = 2 * ((int)block - 1) + (group_u0 - group_chunk < p.real0 - kTileCost ? 1 : 0);
           }
           a.joins[block] = j;
         }
@@ -788,13 +775,13 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
     };
     auto begin = [&](const Piece& p) {
       const unsigned char *kc = a.kc + (int64_t)p.h * a.c_head, *vc = a.vc + (int64_t)p.h * a.c_head;
-      const unsigned char *ksc = a.k_power + (int64_t)p.h * a.s_head, *vsc = a.v_power + (int64_t)p.h * a.s_head;
+      const unsigned char *ksc = k_power + p.h * power_head, *vsc = v_power + p.h * power_head;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         ids[i].template place<D>(a, (p.s0 + i) * kStep, p.last(), at);
         in[i].load_k(kc, ksc, at, kl, lane);
         if (i == 0) t.load_q(a, p.r, p.h, p.rt, lane);
-        in[i].load_v(vc, vsc, at, vl, lane);
+        in[i].load_v(vc, vsc, at, vl, a.c_tok, lane);
       }
     };
     bool have = take(now);
@@ -809,7 +796,7 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
       const int L = now.r.len + now.r.n, h = now.h;
       const float sc = a.scale2 * (E4M3 && a.k_scale ? a.k_scale[h] : 1.0f);
       const unsigned char *kc = a.kc + (int64_t)h * a.c_head, *vc = a.vc + (int64_t)h * a.c_head;
-      const unsigned char *ksc = a.k_power + (int64_t)h * a.s_head, *vsc = a.v_power + (int64_t)h * a.s_head;
+      const unsigned char *ksc = k_power + h * power_head, *vsc = v_power + h * power_head;
       const int full = a.causal ? now.r.len : L - 1;     // tokens up to `full` are seen by every row
       const int last = now.last();
       Groups<G> id = ids[N];
@@ -819,7 +806,7 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           t.step(
-              in[i], base, full, sc, lane,
+              in[i], base, base + kStep - 1 > full, sc, lane,
               [&]() {
                 // (with 64 rows the branch costs more register copies than the loads: those are
                 // the last tokens once more)
@@ -829,7 +816,7 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
                 in[i].load_k(kc, ksc, at, kl, lane);
               },
               [&]() {
-                if (MT == 4 || base + N * kStep <= last) in[i].load_v(vc, vsc, at, vl, lane);
+                if (MT == 4 || base + N * kStep <= last) in[i].load_v(vc, vsc, at, vl, a.c_tok, lane);
               });
           base += kStep;
           if (base > last) goto done;
@@ -850,7 +837,7 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
               const int d = DT * (4 * (lane >> 4) + i) + dt;
               float y;
               if constexpr (kFp4) {
-                const int64_t page0 = (int64_t)((unsigned)page < (unsigned)a.n_pages ? page : 0) * a.s_page;
+                const int64_t page0 = ((unsigned)page < (unsigned)a.n_pages ? page : 0) * a.Hkv * power_head;
                 y = vsc[page0 + (tk & ((1 << a.page_shift) - 1)) * (D / 32) + d / 32] >= 253 ? NAN : 0.0f;
               } else {
                 const uint32_t x = E4M3 ? widen<false>(p[d]) & 0xFFFFu : reinterpret_cast<const uint16_t*>(p)[d];

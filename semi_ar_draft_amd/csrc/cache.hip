@@ -27,48 +27,64 @@ __device__ __forceinline__ uint4 to_cache(const uint16_t* p, float s, float rs) 
   return make_uint4(lo.x, lo.y, hi.x, hi.y);
 }
 
-template <int F>
-__global__ __launch_bounds__(kCacheThreads) void cache_write_impl(const CacheWriteArgs a) {
+// Where a thread's values stand: row, chunk, head, first value; place in the cache.  Whether there is one.
+struct Spot {
+  unsigned row;
+  int h, d0, page, place;
+  int64_t to;
+};
+
+__device__ __forceinline__ bool find(const CacheWriteArgs& a, int elems, Spot& s) {
   const unsigned i = blockIdx.x * kCacheThreads + threadIdx.x;
-  const unsigned row = i / (unsigned)a.chunks;
-  if (row >= (unsigned)a.n_rows) return;
-  const unsigned c = i - row * (unsigned)a.chunks;
-  const int slot = a.slot[row];
+  s.row = i / (unsigned)a.chunks;
+  if (s.row >= (unsigned)a.n_rows) return false;
+  const unsigned c = i - s.row * (unsigned)a.chunks;
+  const int slot = a.slot[s.row];
   if (slot < 0 || slot >= a.n_slots) {
     if (slot != -1 && c == 0) atomicOr(a.err, kErrSlot);
-    return;
+    return false;
   }
-  constexpr int kElems = F == kCacheE4m3 ? 16 : 8;
-  const int h = c >> a.chunk_shift;
-  const int d0 = (c & ((1 << a.chunk_shift) - 1)) * kElems;
-  const int page = slot >> a.page_shift, place = slot & ((1 << a.page_shift) - 1);
-  const int64_t to = (int64_t)page * a.c_page + (int64_t)place * a.c_tok + (int64_t)h * a.c_head;
-  const uint16_t *kp = a.k + row * a.k_row + h * a.k_head + d0, *vp = a.v + row * a.v_row + h * a.v_head + d0;
-  if constexpr (F == kCacheMxfp4) {
-    const uint4 xk = *reinterpret_cast<const uint4*>(kp), xv = *reinterpret_cast<const uint4*>(vp);
-    float k[8], v[8];
-    unpack8(xk, k);
-    unpack8(xv, v);
-    unsigned char pk, pv;
-    const uint32_t wk = to_mxfp4(k, pk), wv = to_mxfp4(v, pv);
-    *reinterpret_cast<uint32_t*>(a.kc + to + d0 / 2) = wk;
-    *reinterpret_cast<uint32_t*>(a.vc + to + d0 / 2) = wv;
-    if ((threadIdx.x & 3) == 0) {
-      const int64_t at = page * a.s_page + h * a.s_head + (int64_t)place * a.blocks + d0 / 32;
-      a.k_power[at] = pk;
-      a.v_power[at] = pv;
-    }
-  } else {
-    float ks = 1.0f, vs = 1.0f;
-    if constexpr (F == kCacheE4m3) {
-      if (a.k_scale) ks = a.k_scale[h];
-      if (a.v_scale) vs = a.v_scale[h];
-    }
-    const uint4 k = to_cache<F>(kp, ks, 1.0f / ks);
-    const uint4 v = to_cache<F>(vp, vs, 1.0f / vs);
-    const int64_t at = to + (F == kCacheE4m3 ? d0 : 2 * d0);
-    *reinterpret_cast<uint4*>(a.kc + at) = k;
-    *reinterpret_cast<uint4*>(a.vc + at) = v;
+  s.h = c >> a.chunk_shift;
+  s.d0 = (c & ((1 << a.chunk_shift) - 1)) * elems;
+  s.page = slot >> a.page_shift;
+  s.place = slot & ((1 << a.page_shift) - 1);
+  s.to = (int64_t)s.page * a.c_page + (int64_t)s.place * a.c_tok + (int64_t)s.h * a.c_head;
+  return true;
+}
+
+template <int F>
+__global__ __launch_bounds__(kCacheThreads) void cache_write_impl(const CacheWriteArgs a) {
+  Spot s;
+  if (!find(a, F == kCacheE4m3 ? 16 : 8, s)) return;
+  float ks = 1.0f, vs = 1.0f;
+  if constexpr (F == kCacheE4m3) {
+    if (a.k_scale) ks = a.k_scale[s.h];
+    if (a.v_scale) vs = a.v_scale[s.h];
+  }
+  const uint4 k = to_cache<F>(a.k + s.row * a.k_row + s.h * a.k_head + s.d0, ks, 1.0f / ks);
+  const uint4 v = to_cache<F>(a.v + s.row * a.v_row + s.h * a.v_head + s.d0, vs, 1.0f / vs);
+  const int64_t at = s.to + (F == kCacheE4m3 ? s.d0 : 2 * s.d0);
+  *reinterpret_cast<uint4*>(a.kc + at) = k;
+  *reinterpret_cast<uint4*>(a.vc + at) = v;
+}
+
+__global__ __launch_bounds__(kCacheThreads) void cache_write_mxfp4_impl(const CacheWritePowers p) {
+  const CacheWriteArgs& a = p.w;
+  Spot s;
+  if (!find(a, 8, s)) return;
+  const uint4 xk = *reinterpret_cast<const uint4*>(a.k + s.row * a.k_row + s.h * a.k_head + s.d0);
+  const uint4 xv = *reinterpret_cast<const uint4*>(a.v + s.row * a.v_row + s.h * a.v_head + s.d0);
+  float k[8], v[8];
+  unpack8(xk, k);
+  unpack8(xv, v);
+  unsigned char pk, pv;
+  const uint32_t wk = to_mxfp4(k, pk), wv = to_mxfp4(v, pv);
+  *reinterpret_cast<uint32_t*>(a.kc + s.to + s.d0 / 2) = wk;
+  *reinterpret_cast<uint32_t*>(a.vc + s.to + s.d0 / 2) = wv;
+  if ((threadIdx.x & 3) == 0) {
+    const int64_t at = s.page * p.s_page + s.h * p.s_head + (int64_t)s.place * p.blocks + s.d0 / 32;
+    p.k_power[at] = pk;
+    p.v_power[at] = pv;
   }
 }
 
@@ -125,7 +141,7 @@ __global__ __launch_bounds__(kCacheThreads) void cache_read_impl(const CacheRead
 }  // namespace
 
 const void* cache_write_kernel(int type) {
-  return type == kCacheMxfp4  ? (const void*)&cache_write_impl<kCacheMxfp4>
+  return type == kCacheMxfp4  ? (const void*)&cache_write_mxfp4_impl
          : type == kCacheE4m3 ? (const void*)&cache_write_impl<kCacheE4m3>
                               : (const void*)&cache_write_impl<kCacheBf16>;
 }

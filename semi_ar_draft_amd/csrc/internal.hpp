@@ -277,14 +277,17 @@ struct CacheWriteArgs {
   int64_t c_page, c_tok, c_head;
   const float* k_scale;          // [heads], 8-bit cache (nullable: 1)
   const float* v_scale;
-  unsigned char* k_power;        // MXFP4 cache: powers of its blocks, steps of a page and a head in bytes
+  int32_t* err;
+};
+struct CacheWritePowers {        // MXFP4 cache: powers of its blocks, steps of a page and a head in bytes
+  CacheWriteArgs w;
+  unsigned char* k_power;
   unsigned char* v_power;
   int64_t s_page, s_head;
   int blocks;                    // d / 32
-  int32_t* err;
 };
 constexpr int kCacheThreads = 256;
-const void* cache_write_kernel(int type);
+const void* cache_write_kernel(int type);   // (MXFP4: of CacheWritePowers)
 
 // Rows of a cache back as bf16 (cache.hip): chunks of eight values.
 struct CacheReadArgs {
@@ -312,13 +315,12 @@ const void* cache_read_kernel(int type);
 struct RopeArgs {
   int n_rows, rows;              // rows of a workgroup: rows * rot / 2 <= kRopeTable
   int heads_q, heads_k;          // heads turned into rows: of the queries, of the keys (rope alone)
-  int heads_kv;                  // heads that go into a cache
-  int d, rot;
+  int rot;
   unsigned units;                // of a head turned into rows: rot / 16, and (d - rot) / 8 where those are copied
-  unsigned units_inv, heads_inv, heads_kv_inv, pairs_inv;   // 2^32 / units, heads_q + heads_k, heads_kv, rot / 2, rounded up (0 for 1)
+  unsigned units_inv, heads_inv, pairs_inv;   // 2^32 / units, heads_q + heads_k, rot / 2, rounded up (0 for 1)
+  float factor;
   const int32_t* pos;            // [n_rows], -1 = skip
   const double* freq;            // [rot / 2] radians a position
-  float factor;
   const uint16_t* q;
   int64_t q_row, q_head;
   uint16_t* qo;
@@ -327,20 +329,24 @@ struct RopeArgs {
   int64_t k_row, k_head;
   uint16_t* ko;
   int64_t ko_row, ko_head;
+  int32_t* err;
+};
+struct RopeWriteArgs {
+  RopeArgs r;
+  int d, heads_kv, page_shift;   // heads_kv: heads that go into the cache
+  unsigned heads_kv_inv;         // 2^32 / heads_kv rounded up
   const uint16_t* v;
   int64_t v_row, v_head;
   const int32_t* slot;           // [n_rows], -1 = skip
   int64_t n_slots;
-  int page_shift;
   unsigned char* kc;
   unsigned char* vc;
   int64_t c_page, c_tok, c_head;
-  const float* k_scale;
+  const float* k_scale;          // e4m3
   const float* v_scale;
-  unsigned char* k_power;
+  unsigned char* k_power;        // MXFP4
   unsigned char* v_power;
   int64_t s_page, s_head;
-  int32_t* err;
 };
 constexpr int kRopeThreads = 256;
 constexpr int kRopeTable = 512;  // pairs of a workgroup's rows
@@ -365,11 +371,8 @@ struct AttendArgs {
   const unsigned char* kc;       // caches, strides in bytes
   const unsigned char* vc;
   int64_t c_page, c_tok, c_head;
-  const float* k_scale;          // [Hkv], e4m3 cache (nullable: 1)
-  const float* v_scale;
-  const unsigned char* k_power;  // MXFP4 cache: powers of its blocks, steps of a page and a head in bytes
-  const unsigned char* v_power;
-  int64_t s_page, s_head;
+  const float* k_scale;          // [Hkv], e4m3 cache (nullable: 1); MXFP4 (attend_impl alone): bytes, the powers of
+  const float* v_scale;          // its blocks
   const int32_t* table;
   int64_t tstride;
   const int32_t* len;

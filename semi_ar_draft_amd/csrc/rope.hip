@@ -188,14 +188,15 @@ __device__ __forceinline__ uint2 to_e4m3_wide(const double (&y)[8], double s) {
 // loaded as the heads above are.
 template <bool PAIRED, int F>
 struct CacheHeads {
+  const RopeWriteArgs& w;
   const RopeArgs& a;
   int row0, c;
   unsigned slots, it, row_in, h;
   bool there;
   uint4 xk, xo, xv;
 
-  __device__ __forceinline__ CacheHeads(const RopeArgs& a_, int row0_) : a(a_), row0(row0_) {
-    const unsigned chunks = a.d / 8;                     // 8, 16 or 32: a quad's threads have one token and head
+  __device__ __forceinline__ CacheHeads(const RopeWriteArgs& w_, int row0_) : w(w_), a(w_.r), row0(row0_) {
+    const unsigned chunks = w.d / 8;                     // 8, 16 or 32: a quad's threads have one token and head
     slots = kRopeThreads / chunks;
     c = threadIdx.x & (chunks - 1);
     it = threadIdx.x / chunks;
@@ -204,16 +205,16 @@ struct CacheHeads {
 
   __device__ __forceinline__ void load() {
     there = false;
-    if (it >= a.rows * (unsigned)a.heads_kv) return;
-    row_in = divide(it, a.heads_kv_inv);
-    h = it - row_in * a.heads_kv;
+    if (it >= a.rows * (unsigned)w.heads_kv) return;
+    row_in = divide(it, w.heads_kv_inv);
+    h = it - row_in * w.heads_kv;
     const int row = row0 + (int)row_in;
     if (row >= a.n_rows) return;
     there = true;
     const int half = a.rot / 16;
     const uint16_t* kp = a.k + row * a.k_row + h * a.k_head;
     xk = *reinterpret_cast<const uint4*>(kp + 8 * c);
-    xv = *reinterpret_cast<const uint4*>(a.v + row * a.v_row + h * a.v_head + 8 * c);
+    xv = *reinterpret_cast<const uint4*>(w.v + row * w.v_row + h * w.v_head + 8 * c);
     // (halves: the partners of the pairs)
     const int co = PAIRED || c >= 2 * half ? c : c < half ? c + half : c - half;
     xo = *reinterpret_cast<const uint4*>(kp + 8 * co);
@@ -221,51 +222,51 @@ struct CacheHeads {
 
   __device__ __forceinline__ void write(const Angle32* t32, const Angle64* t64) {
     const int half = a.rot / 16;
-    while (it < a.rows * (unsigned)a.heads_kv) {
-      const uint4 wk = xk, wo = xo, wv = xv;
+    while (it < a.rows * (unsigned)w.heads_kv) {
+      const uint4 gk = xk, go = xo, gv = xv;
       const unsigned r = row_in, head = h;
       const bool now = there;
       it += slots;
       load();
       if (!now) continue;
       const int row = row0 + (int)r;
-      const int slot = a.slot[row];
+      const int slot = w.slot[row];
       if (a.pos[row] < 0) continue;
-      if (slot < 0 || slot >= a.n_slots) {
+      if (slot < 0 || slot >= w.n_slots) {
         if (slot != -1 && c == 0 && head == 0) atomicOr(a.err, kErrSlot);
         continue;
       }
-      const int page = slot >> a.page_shift, place = slot & ((1 << a.page_shift) - 1);
-      const int64_t to = (int64_t)page * a.c_page + (int64_t)place * a.c_tok + (int64_t)head * a.c_head;
+      const int page = slot >> w.page_shift, place = slot & ((1 << w.page_shift) - 1);
+      const int64_t to = (int64_t)page * w.c_page + (int64_t)place * w.c_tok + (int64_t)head * w.c_head;
       float x[8], xp[8], v[8];
-      unpack8(wk, x);
-      unpack8(wo, xp);
+      unpack8(gk, x);
+      unpack8(go, xp);
       const unsigned row_t = r * (a.rot / 2);
       if constexpr (F == kCacheBf16) {
         float y[8];
         turn_chunk<PAIRED>(a, c, x, xp, t32 + row_t, y);
-        *reinterpret_cast<uint4*>(a.kc + to + 16 * c) = c < 2 * half ? pack8(y) : wk;
-        *reinterpret_cast<uint4*>(a.vc + to + 16 * c) = wv;
+        *reinterpret_cast<uint4*>(w.kc + to + 16 * c) = c < 2 * half ? pack8(y) : gk;
+        *reinterpret_cast<uint4*>(w.vc + to + 16 * c) = gv;
       } else {
         double y[8];
         turn_chunk<PAIRED>(a, c, x, xp, t64 + row_t, y);
-        unpack8(wv, v);
+        unpack8(gv, v);
         if constexpr (F == kCacheE4m3) {
-          const float ks = a.k_scale ? a.k_scale[head] : 1.0f, vs = a.v_scale ? a.v_scale[head] : 1.0f;
-          *reinterpret_cast<uint2*>(a.kc + to + 8 * c) = to_e4m3_wide(y, (double)ks);
-          *reinterpret_cast<uint2*>(a.vc + to + 8 * c) = to_e4m3(v, vs, 1.0f / vs);
+          const float ks = w.k_scale ? w.k_scale[head] : 1.0f, vs = w.v_scale ? w.v_scale[head] : 1.0f;
+          *reinterpret_cast<uint2*>(w.kc + to + 8 * c) = to_e4m3_wide(y, (double)ks);
+          *reinterpret_cast<uint2*>(w.vc + to + 8 * c) = to_e4m3(v, vs, 1.0f / vs);
         } else {
           float z[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) z[i] = to_odd(y[i]);
           unsigned char pk, pv;
           const uint32_t codes_k = to_mxfp4(z, pk), codes_v = to_mxfp4(v, pv);
-          *reinterpret_cast<uint32_t*>(a.kc + to + 4 * c) = codes_k;
-          *reinterpret_cast<uint32_t*>(a.vc + to + 4 * c) = codes_v;
+          *reinterpret_cast<uint32_t*>(w.kc + to + 4 * c) = codes_k;
+          *reinterpret_cast<uint32_t*>(w.vc + to + 4 * c) = codes_v;
           if ((c & 3) == 0) {
-            const int64_t at = page * a.s_page + head * a.s_head + (int64_t)place * (a.d / 32) + c / 4;
-            a.k_power[at] = pk;
-            a.v_power[at] = pv;
+            const int64_t at = page * w.s_page + head * w.s_head + (int64_t)place * (w.d / 32) + c / 4;
+            w.k_power[at] = pk;
+            w.v_power[at] = pv;
           }
         }
       }
@@ -284,12 +285,13 @@ __global__ __launch_bounds__(kRopeThreads) void rope_impl(const RopeArgs a) {
 }
 
 template <bool PAIRED, int F>
-__global__ __launch_bounds__(kRopeThreads) void rope_write_impl(const RopeArgs a) {
+__global__ __launch_bounds__(kRopeThreads) void rope_write_impl(const RopeWriteArgs w) {
+  const RopeArgs& a = w.r;
   constexpr bool kWide = F != kCacheBf16;
   __shared__ Angle32 t32[kRopeTable];
   __shared__ Angle64 t64[kWide ? kRopeTable : 1];
   const int row0 = blockIdx.x * a.rows;
-  CacheHeads<PAIRED, F> cache(a, row0);
+  CacheHeads<PAIRED, F> cache(w, row0);
   Heads<PAIRED> heads(a, t32, row0);
   angles<kWide>(a, row0, t32, t64);
   __syncthreads();
