@@ -360,3 +360,31 @@ def test_timing_class_and_many_rows(ctx):
     wide = torch.ones((1, 1, 1024), dtype=torch.bfloat16, device="cuda").expand(n, 1, 1024)
     refused(lambda: ctx.rope(wide, None, pos, torch.zeros(512, dtype=torch.float64, device="cuda"),
                              q_out=torch.empty((n, 1, 1024), dtype=torch.bfloat16, device="cuda")), "too many rows")
+
+
+@pytest.mark.parametrize("kv", ["e4m3", "mxfp4"])
+@pytest.mark.parametrize("inter", [False, True])
+def test_at_position_0_keys_are_rounded_as_the_cache_write_rounds_them(ctx, kv, inter):
+    """Every finite bf16 value, borders of the quotients with a scale that is no power of two among them."""
+    bits = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    bits = bits[torch.isfinite(bits.float())]
+    n = len(bits) // 32                                  # 65024 values
+    k = torch.zeros((n, 1, 64), dtype=torch.bfloat16)
+    if inter:
+        k[:, 0, 0::2] = bits.view(n, 32)
+    else:
+        k[:, 0, :32] = bits.view(n, 32)
+    k = k.cuda()
+    pages = n // 64 + 1
+    a, b = caches(kv, pages, 64, 1, 64, "token"), caches(kv, pages, 64, 1, 64, "token")
+    if kv == "e4m3":
+        scale = torch.tensor([0.75 * 1.25], device="cuda")
+        a, b = (*a[:2], scale, scale), (*b[:2], scale, scale)
+    slot, pos = i32(np.arange(n)), torch.zeros(n, dtype=torch.int32, device="cuda")
+    ctx.cache_write(k, k, slot, *a)
+    ctx.rope_write(None, k, k, pos, slot, frequencies(64)[0], *b, interleaved=inter)
+    ctx.check()
+    for x, y, s in ((a[0], b[0], 2), (a[1], b[1], 3)):
+        assert np.array_equal(values(x, a[s]), values(y, b[s]))
+    if kv == "mxfp4":
+        assert torch.equal(a[2], b[2]) and torch.equal(a[3], b[3])
