@@ -1348,10 +1348,10 @@ int cache_write_common(dspark_ctx* c, hipStream_t stream, int n_rows, int heads,
 int attend_common(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads, int d,
                   const void* q, int64_t q_stride_row, int64_t q_stride_head, const void* kcache, const void* vcache,
                   int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head, int kv_dtype,
-                  const float* k_scale, const float* v_scale, const uint8_t* k_power, const uint8_t* v_power, int page_size, int n_pages, const int32_t* table,
-                  int64_t table_stride, int max_pages, const int32_t* len, const int32_t* K,
-                  const int32_t* t_offsets, int causal, float scale, void* out, int64_t o_stride_row,
-                  int64_t o_stride_head, float* lse) {
+                  const float* k_scale, const float* v_scale, const uint8_t* k_power, const uint8_t* v_power,
+                  int page_size, int n_pages, const int32_t* table, int64_t table_stride, int max_pages,
+                  const int32_t* len, const int32_t* K, const int32_t* t_offsets, int causal, float scale, void* out,
+                  int64_t o_stride_row, int64_t o_stride_head, float* lse) {
   int rc = check_pages(c, B, page_size, n_pages, max_pages, table_stride, table);
   if (rc) return rc;
   if ((rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype)))

@@ -895,9 +895,10 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
 }
 
 // Adds up the pieces of the tiles that several workgroups share: a workgroup for
-// 16 rows, a wave of it for a quarter of their values, eight pieces in flight
-// (16: 1 us more where a tile has two or three pieces, no less where it has
-// eleven).  Bound by latency: a tile's place, then its pieces, 4 to 11 us.
+// 16 rows, a wave of it for a quarter of their values, eight pieces in flight,
+// or three where no more are left (12 and six: 1 us less where a tile has
+// eleven, 0.3 more where it has two or three).  Bound by latency: a tile's
+// place, then its pieces, 3.5 to 10 us.
 template <int D>
 __global__ __launch_bounds__(kAttendThreads) void attend_join_impl(const AttendArgs a) {
   constexpr int DT = D / 16, kV = DT / 4;
@@ -909,12 +910,11 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_impl(const AttendA
   f32x4_t acc[kV];
 #pragma unroll
   for (int c = 0; c < kV; ++c) acc[c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
-  constexpr int kPieces = 8;
+  constexpr int kPieces = 8, kFew = 3;
   for (int j0 = 0; j0 < d.n; j0 += kPieces) {
     float2 ml[kPieces];
     f32x4_t y[kPieces][kV];
-#pragma unroll
-    for (int j = 0; j < kPieces; ++j) {
+    auto load = [&](int j) {
       // the first piece stands alone, the others at the beginnings of the stretches after it
       const int i = min(j0 + j, d.n - 1);
       const float* p = a.part + (int64_t)(i == 0 ? d.slot : (d.slot & ~1) + 2 * i) * size;
@@ -922,6 +922,19 @@ __global__ __launch_bounds__(kAttendThreads) void attend_join_impl(const AttendA
 #pragma unroll
       for (int c = 0; c < kV; ++c)
         y[j][c] = reinterpret_cast<const f32x4_t*>(p + 2 * rows)[(mt * DT + dt0 + c) * 64 + lane];
+    };
+#pragma unroll
+    for (int j = 0; j < kFew; ++j) load(j);
+    if (d.n - j0 > kFew) {
+#pragma unroll
+      for (int j = kFew; j < kPieces; ++j) load(j);
+    } else {
+#pragma unroll
+      for (int j = kFew; j < kPieces; ++j) {
+        ml[j] = make_float2(-INFINITY, 0.0f);
+#pragma unroll
+        for (int c = 0; c < kV; ++c) y[j][c] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+      }
     }
     float mn = M;
 #pragma unroll
