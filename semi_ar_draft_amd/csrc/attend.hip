@@ -20,8 +20,9 @@
 // with its neighbours it leaves in memory, and a second launch adds the pieces
 // up in the order of their tokens.
 //
-// One workgroup a CU, one wave a SIMD (MXFP4: two, where the registers hold them): its registers hold the next two steps'
-// keys and values in flight (64 to 128 KB a CU), which is what the memory's
+// One workgroup a CU, one wave a SIMD (MXFP4: two, where the registers hold
+// them, one step ahead each): its registers hold the next two steps' keys and
+// values in flight (64 to 128 KB a CU), which is what the memory's
 // latency asks for; with more waves the older ones of a SIMD are served first
 // and the younger ones finish alone (measured: two workgroups a CU 139 us
 // against 131 on 128 requests of 64 to 8192 tokens, 137 against 96 on equal
@@ -43,7 +44,10 @@
 // 131000 tokens in e4m3, 64 rows a tile, 105 and 11 us, bound by the issue of
 // vector instructions (about 255, and 64 matrix ones, a step); 48 draft blocks
 // of 7 positions, heads of 64, 19.5 and 4 us, bound by the latency of finding a
-// stretch and its first keys.
+// stretch and its first keys.  Over MXFP4 (a quarter of bf16's bytes), both
+// launches, the first 62 us (pages that keep a head's tokens together 55), the
+// long ones 118, the blocks 16.6: vector issue, a value being 4 bits to widen and
+// a weight two products, and in the first the 64-byte pieces of a token's heads.
 #include "common.hpp"
 #include "internal.hpp"
 

@@ -8,7 +8,9 @@
 // a quad find together), so both tensors' loads are in flight together, and
 // consecutive threads write consecutive bytes of a token's head.  Measured:
 // 16381 rows of 8 heads of 128 into e4m3, 101 MB, 24.4 us (4.1 TB/s, a copy
-// reaches 4.8); a step's rows of 128 requests 3.3 us.
+// reaches 4.8); a step's rows of 128 requests 3.3 us; 32749 rows of 8 heads of
+// 128 back from MXFP4, 170 MB of which 134 are written, 34.9 us (4.9 TB/s);
+// 63 rows into MXFP4 3.0, back 2.8.
 #include "cache_values.hpp"
 
 namespace dspark {

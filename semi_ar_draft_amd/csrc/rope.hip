@@ -10,10 +10,11 @@
 // cache rounds to 8 or 4 bits in float64, so that a value near a border between
 // two of those goes to the side of the exact one.
 //
-// Bound by memory: 16381 rows of 40 heads of 128 62.9 us (335 MB, 5.3 TB/s, a
-// copy of 2 GiB reaches 4.9), 8190 of 32 and 8 heads into a bf16 cache 40.4 (5.0), into e4m3
-// 45.5, into MXFP4 44 (of which the float64 part hides least).  A row a workgroup: its sines, a quarter of
-// its threads' work, pass under the loads of its values, and several
+// Bound by memory: 16381 rows of 40 heads of 128 62.4 us (335 MB, 5.4 TB/s, a
+// copy of 2 GiB reaches 4.9); 8190 rows, 32 heads to rows and 8 into a bf16 cache
+// 40.4 (5.0 TB/s), into e4m3 45.2, into MXFP4 44.4 (4.0), where the keys' float64
+// part does not hide whole; a step's 821 rows 6.2.  A row a workgroup: its sines,
+// a quarter of its threads' work, pass under the loads of its values, and several
 // workgroups of a CU are at different stages (four rows 69.0 us against 62.4).
 #include "cache_values.hpp"
 
