@@ -596,8 +596,9 @@ int dspark_cache_read(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads
  * theta, stretched as a long context asks (linear: over the stretch s; a base
  * of theta s^(rot / (rot - 2)); or a mixture of freq and freq / s by how often
  * a pair turns within the trained length, with factor = 0.1 ln s + 1); factor:
- * finite, 1 where nothing scales the result.  Angles, sines and cosines are
- * float64, the products float32, the results bf16.
+ * finite as a float32, 1 where nothing scales the result.  Angles, sines and
+ * cosines and their products with the factor are float64, what they are
+ * multiplied with is taken in float32, the results are bf16.
  * q, k: bf16 [n_rows][heads_q], [n_rows][heads] rows of d values through row
  * and head strides (multiples of 8, 16-byte aligned); q_out, k_out likewise,
  * each either the input itself with equal strides, or apart from every input.
@@ -607,7 +608,7 @@ int dspark_cache_read(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads
  * heads <= 8192.  One launch (timing class DSPARK_K_ROPE), no workspace.
  * Errors: DSPARK_EINVAL. */
 int dspark_rope(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads_q, int heads, int d, int rot,
-                int interleaved, const int32_t* row_pos, const double* freq, float factor,
+                int interleaved, const int32_t* row_pos, const double* freq, double factor,
                 const void* q, int64_t q_stride_row, int64_t q_stride_head,
                 const void* k, int64_t k_stride_row, int64_t k_stride_head,
                 void* q_out, int64_t qo_stride_row, int64_t qo_stride_head,
@@ -626,7 +627,7 @@ int dspark_rope(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads_q, in
  * Errors: DSPARK_EINVAL. */
 int dspark_rope_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads_q, int heads, int d, int rot,
                       int interleaved, int page_size, int n_pages,
-                      const int32_t* row_pos, const int32_t* row_slot, const double* freq, float factor,
+                      const int32_t* row_pos, const int32_t* row_slot, const double* freq, double factor,
                       const void* q, int64_t q_stride_row, int64_t q_stride_head,
                       void* q_out, int64_t qo_stride_row, int64_t qo_stride_head,
                       const void* k, int64_t k_stride_row, int64_t k_stride_head,

@@ -41,6 +41,7 @@ KERNEL_CLASSES = ("draft_sweep", "draft_combine", "confidence", "survival", "sch
 _lib = None
 _native_module = None
 _vp, _i32, _i64, _u64, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float
+_f64 = ctypes.c_double
 
 
 class DSparkError(RuntimeError):
@@ -137,10 +138,10 @@ def load_library(path: Optional[str] = None) -> ctypes.CDLL:
         _vp, _vp, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp, *rows, *rows]
     lib.dspark_rope.restype = _i32
     lib.dspark_rope.argtypes = [
-        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _f32, *rows, *rows, *rows, *rows]
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _f64, *rows, *rows, *rows, *rows]
     lib.dspark_rope_write.restype = _i32
     lib.dspark_rope_write.argtypes = [
-        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _f32, *rows, *rows, *rows, *rows,
+        _vp, _vp, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _i32, _vp, _vp, _vp, _f64, *rows, *rows, *rows, *rows,
         _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp, _vp, _vp]
     lib.dspark_attend_mxfp4.restype = _i32
     lib.dspark_attend_mxfp4.argtypes = [

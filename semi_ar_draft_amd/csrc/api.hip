@@ -11,6 +11,7 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <limits>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -1251,13 +1252,14 @@ unsigned inverse(unsigned d) { return d <= 1 ? 0u : (unsigned)(((1ull << 32) + d
 
 // What the calls with rotary positions share: their checks and arguments.
 int rope_args(dspark_ctx* c, RopeArgs& a, int n_rows, int heads_q, int heads, int d, int rot, const int32_t* row_pos,
-              const double* freq, float factor, const void* q, int64_t q_row, int64_t q_head, void* q_out, int64_t qo_row,
+              const double* freq, double factor, const void* q, int64_t q_row, int64_t q_head, void* q_out, int64_t qo_row,
               int64_t qo_head) {
   if (n_rows < 0) return fail(c, DSPARK_EINVAL, "n_rows must be >= 0");
   if (heads_q < 0 || heads < 0 || heads_q + (int64_t)heads > 8192)
     return fail(c, DSPARK_EINVAL, "heads_q and heads must be >= 0, together <= 8192");
   if (rot < 16 || rot % 16 || rot > d) return fail(c, DSPARK_EINVAL, "rot must be a multiple of 16 in 16..d (got %d)", rot);
-  if (!std::isfinite(factor)) return fail(c, DSPARK_EINVAL, "factor must be finite");
+  // (queries and bf16 keys take sines and cosines times the factor in float32)
+  if (!(std::fabs(factor) <= std::numeric_limits<float>::max())) return fail(c, DSPARK_EINVAL, "factor must be finite, as a float32 too");
   if (n_rows == 0) return DSPARK_OK;
   if (!row_pos || !freq) return fail(c, DSPARK_EINVAL, "null pointer argument");
   if (heads_q > 0) {
@@ -2131,7 +2133,7 @@ int dspark_cache_read(dspark_ctx* c, hipStream_t stream, int n_rows, int heads, 
 }
 
 int dspark_rope(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q, int heads, int d, int rot, int interleaved,
-                const int32_t* row_pos, const double* freq, float factor, const void* q, int64_t q_stride_row,
+                const int32_t* row_pos, const double* freq, double factor, const void* q, int64_t q_stride_row,
                 int64_t q_stride_head, const void* k, int64_t k_stride_row, int64_t k_stride_head, void* q_out,
                 int64_t qo_stride_row, int64_t qo_stride_head, void* k_out, int64_t ko_stride_row,
                 int64_t ko_stride_head) {
@@ -2172,7 +2174,7 @@ int dspark_rope(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q, int 
 
 int dspark_rope_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q, int heads, int d, int rot,
                       int interleaved, int page_size, int n_pages, const int32_t* row_pos, const int32_t* row_slot,
-                      const double* freq, float factor, const void* q, int64_t q_stride_row, int64_t q_stride_head,
+                      const double* freq, double factor, const void* q, int64_t q_stride_row, int64_t q_stride_head,
                       void* q_out, int64_t qo_stride_row, int64_t qo_stride_head, const void* k, int64_t k_stride_row,
                       int64_t k_stride_head, const void* v, int64_t v_stride_row, int64_t v_stride_head, void* kcache,
                       void* vcache, int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,

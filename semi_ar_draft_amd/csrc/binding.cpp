@@ -51,11 +51,12 @@ class Args {
   }
   int int32(const char* name) { return (int)integer(name, INT32_MIN, INT32_MAX); }
 
-  float real(const char*) {
+  double real64(const char*) {
     const double x = PyFloat_AsDouble(next());
     if (PyErr_Occurred()) throw Raised();
-    return (float)x;
+    return x;
   }
+  float real(const char* name) { return (float)real64(name); }
 
   bool truth() {
     const int x = PyObject_IsTrue(next());
@@ -286,14 +287,14 @@ int cache_read(Args& a) {
 struct Turn {
   const double* freq;
   int rot;
-  float factor;
+  double factor;
   bool interleaved;
   explicit Turn(Args& a) {
     const T* f = a.vector("freq", at::kDouble, -1);
     rot = to_int("freq", 2 * f->size(0));
     freq = Args::data<double>(f);
     interleaved = a.truth();
-    factor = a.real("factor");
+    factor = a.real64("factor");
   }
 };
 

@@ -318,7 +318,7 @@ struct RopeArgs {
   int rot;
   unsigned units;                // of a head turned into rows: rot / 16, and (d - rot) / 8 where those are copied
   unsigned units_inv, heads_inv, pairs_inv;   // 2^32 / units, heads_q + heads_k, rot / 2, rounded up (0 for 1)
-  float factor;
+  double factor;                 // of sines and cosines, before these are rounded to anything
   const int32_t* pos;            // [n_rows], -1 = skip
   const double* freq;            // [rot / 2] radians a position
   const uint16_t* q;

@@ -3,8 +3,8 @@
 //
 // Pair j of a row at position t is turned by a = t f_j: (x0, x1) -> factor
 // (x0 cos a - x1 sin a, x1 cos a + x0 sin a).  A far position's angle needs more
-// than 24 bits, so turns = t f_j / 2 pi, their fraction and the sine and cosine
-// are float64; a workgroup works them out once for its rows and keeps them in
+// than 24 bits, so turns = t f_j / 2 pi, their fraction, the sine and cosine and
+// their products with the factor are float64; a workgroup works them out once for its rows and keeps them in
 // LDS, where every head reads them (a row's 64 pairs, 40 heads: a sine and
 // cosine for 40 pairs).  What becomes bf16 is turned in float32; keys that a
 // cache rounds to 8 or 4 bits in float64, so that a value near a border between
@@ -53,8 +53,8 @@ __device__ __forceinline__ void angles(const RopeArgs& a, int row0, Angle32* t32
     const double part = turns - __builtin_rint(turns);
     double s, c;
     sincospi(part + part, &s, &c);
-    c *= (double)a.factor;
-    s *= (double)a.factor;
+    c *= a.factor;
+    s *= a.factor;
     t32[i] = {(float)c, (float)s};
     if constexpr (WIDE) t64[i] = {c, s};
   }
