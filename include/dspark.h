@@ -535,8 +535,9 @@ int dspark_pages_commit(dspark_ctx* ctx, hipStream_t stream, int B, int page_siz
  * k / k_scale[head] (ties to even, magnitudes above 448 become 448; NaN
  * stays), a single rounding of the exact quotient; k_scale, v_scale float
  * [heads], positive and normal, or NULL for 1; they must be NULL for BF16.
- * k and v may not overlap the caches.  One launch (timing class
- * DSPARK_K_CACHE).  Errors: DSPARK_EINVAL. */
+ * k and v may not overlap the caches, nor the caches each other (kcache may
+ * be vcache where k is v, with equal strides and scales).  One launch (timing
+ * class DSPARK_K_CACHE).  Errors: DSPARK_EINVAL. */
 int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
                        const void* k, int64_t k_stride_row, int64_t k_stride_head,
                        const void* v, int64_t v_stride_row, int64_t v_stride_head,
@@ -558,7 +559,7 @@ int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int head
  * that every value of magnitude up to 7 * 2^125 is off by at most half the
  * distance of its two neighbours.  A block with a NaN has byte 255 and codes
  * 0.  The rows of a slot given twice may mix, a block's codes and its power
- * too. */
+ * too.  Caches and powers are four arrays. */
 int dspark_cache_write_mxfp4(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads, int d, int page_size,
                              int n_pages, const void* k, int64_t k_stride_row, int64_t k_stride_head,
                              const void* v, int64_t v_stride_row, int64_t v_stride_head,
@@ -574,8 +575,9 @@ int dspark_cache_write_mxfp4(dspark_ctx* ctx, hipStream_t stream, int n_rows, in
  * have them, those of other types NULL.  k, v: bf16 [n_rows][heads][d] through
  * row and head strides (multiples of 8, 16-byte aligned).  bf16 and MXFP4
  * values come back exactly (MXFP4: from 2^-126 on), E4M3 ones times their scale rounded
- * to float32 and then to bf16.  k and v may not overlap each other or the
- * caches.  One launch (timing class DSPARK_K_CACHE).  Errors: DSPARK_EINVAL. */
+ * to float32 and then to bf16.  k and v may not overlap each other, the
+ * caches or the powers.  One launch (timing class DSPARK_K_CACHE).  Errors:
+ * DSPARK_EINVAL. */
 int dspark_cache_read(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
                       const int32_t* row_slot, const void* kcache, const void* vcache,
                       int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
@@ -622,9 +624,9 @@ int dspark_rope(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads_q, in
  * to bf16 in between, a key may go to its second nearest value).  Slots,
  * caches, scales and powers as the writes have them (scales: E4M3, powers:
  * MXFP4, else NULL); a row with slot -1 has its query turned all the same; d =
- * 64, 128 or 256.  q_out may be q with equal strides; k and v may not overlap
- * it or the caches.  One launch (timing class DSPARK_K_ROPE), no workspace.
- * Errors: DSPARK_EINVAL. */
+ * 64, 128 or 256.  q_out may be q with equal strides; otherwise q_out, the
+ * caches and the powers overlap neither each other nor an input.  One launch
+ * (timing class DSPARK_K_ROPE), no workspace.  Errors: DSPARK_EINVAL. */
 int dspark_rope_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads_q, int heads, int d, int rot,
                       int interleaved, int page_size, int n_pages,
                       const int32_t* row_pos, const int32_t* row_slot, const double* freq, double factor,

@@ -1203,13 +1203,19 @@ int check_cache(dspark_ctx* c, int heads, int d, int page_size, const void* kc, 
   return DSPARK_OK;
 }
 
+// Whether an array is one of the others, null ones aside.
+template <typename... P>
+bool same_as(const void* p, P... others) {
+  return p && ((p == static_cast<const void*>(others)) || ...);
+}
+
 // A cache's element type, and its scales or powers as the type needs them.
 int cache_type(int kv_dtype) {
   return kv_dtype == DSPARK_MXFP4 ? kCacheMxfp4 : kv_dtype == DSPARK_E4M3 ? kCacheE4m3 : kCacheBf16;
 }
 
-int check_scales(dspark_ctx* c, int kv_dtype, const float* k_scale, const float* v_scale, const uint8_t* k_power,
-                 const uint8_t* v_power) {
+int check_scales(dspark_ctx* c, int kv_dtype, const void* kc, const void* vc, const float* k_scale, const float* v_scale,
+                 const uint8_t* k_power, const uint8_t* v_power) {
   if (kv_dtype != DSPARK_E4M3 && (k_scale || v_scale)) return fail(c, DSPARK_EINVAL, "scales belong to an e4m3 cache");
   if (kv_dtype != DSPARK_MXFP4) {
     if (k_power || v_power) return fail(c, DSPARK_EINVAL, "powers belong to an mxfp4 cache");
@@ -1218,6 +1224,8 @@ int check_scales(dspark_ctx* c, int kv_dtype, const float* k_scale, const float*
   if (!k_power || !v_power) return fail(c, DSPARK_EINVAL, "null pointer argument");
   if (!aligned16(k_power) || !aligned16(v_power) || k_power == v_power)
     return fail(c, DSPARK_EINVAL, "the powers must be two 16-byte aligned arrays");
+  if (same_as(k_power, kc, vc) || same_as(v_power, kc, vc))
+    return fail(c, DSPARK_EINVAL, "the powers and the caches must be different arrays");
   return DSPARK_OK;
 }
 
@@ -1301,13 +1309,16 @@ int cache_write_common(dspark_ctx* c, hipStream_t stream, int n_rows, int heads,
   int rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype);
   if (rc) return rc;
   const bool e4m3 = kv_dtype == DSPARK_E4M3;
-  if ((rc = check_scales(c, kv_dtype, k_scale, v_scale, k_power, v_power))) return rc;
+  if ((rc = check_scales(c, kv_dtype, kcache, vcache, k_scale, v_scale, k_power, v_power))) return rc;
   if (n_rows < 0) return fail(c, DSPARK_EINVAL, "n_rows must be >= 0");
   if (n_rows == 0) return DSPARK_OK;
   if (!k || !v || !row_slot) return fail(c, DSPARK_EINVAL, "null pointer argument");
   if (!aligned16(k) || !aligned16(v) || (k_stride_row & 7) || (k_stride_head & 7) || (v_stride_row & 7) ||
       (v_stride_head & 7) || k_stride_row < 0 || k_stride_head < 0 || v_stride_row < 0 || v_stride_head < 0)
     return fail(c, DSPARK_EINVAL, "k and v must be 16-byte aligned, their strides multiples of 8");
+  // (what is written twice must be the same bytes)
+  if (kcache == vcache && (k != v || k_stride_row != v_stride_row || k_stride_head != v_stride_head || k_scale != v_scale))
+    return fail(c, DSPARK_EINVAL, "kcache and vcache must be different arrays unless k and v are the same rows");
   const int per_head = e4m3 ? d / 16 : d / 8;
   if ((int64_t)n_rows * heads * per_head > INT32_MAX - kCacheThreads)
     return fail(c, DSPARK_EINVAL, "too many rows (%d)", n_rows);
@@ -1360,7 +1371,7 @@ int attend_common(dspark_ctx* c, hipStream_t stream, int B, int n_rows, int gamm
     return rc;
   const int sh = page_shift(page_size);
   const bool e4m3 = kv_dtype == DSPARK_E4M3;
-  if ((rc = check_scales(c, kv_dtype, k_scale, v_scale, k_power, v_power))) return rc;
+  if ((rc = check_scales(c, kv_dtype, kcache, vcache, k_scale, v_scale, k_power, v_power))) return rc;
   if (gamma < 0 || gamma > kMaxGamma) return fail(c, DSPARK_EINVAL, "gamma must be in 0..%d", kMaxGamma);
   if (n_rows < 0 || (!t_offsets && (int64_t)B * (gamma + 1) > n_rows))
     return fail(c, DSPARK_EINVAL, "n_rows must hold B * (gamma + 1) rows where t_offsets is NULL");
@@ -2087,14 +2098,14 @@ int dspark_cache_read(dspark_ctx* c, hipStream_t stream, int n_rows, int heads, 
   if (rc) return rc;
   if ((rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype)))
     return rc;
-  if ((rc = check_scales(c, kv_dtype, k_scale, v_scale, k_power, v_power))) return rc;
+  if ((rc = check_scales(c, kv_dtype, kcache, vcache, k_scale, v_scale, k_power, v_power))) return rc;
   if (n_rows < 0) return fail(c, DSPARK_EINVAL, "n_rows must be >= 0");
   if (n_rows == 0) return DSPARK_OK;
   if (!row_slot) return fail(c, DSPARK_EINVAL, "null pointer argument");
   if ((rc = check_out_rows(c, "k", k, n_rows, heads, d, k_stride_row, k_stride_head))) return rc;
   if ((rc = check_out_rows(c, "v", v, n_rows, heads, d, v_stride_row, v_stride_head))) return rc;
-  if (k == v || k == kcache || k == vcache || v == kcache || v == vcache)
-    return fail(c, DSPARK_EINVAL, "k, v and the caches must be different arrays");
+  if (same_as(k, v, kcache, vcache, k_power, v_power) || same_as(v, kcache, vcache, k_power, v_power))
+    return fail(c, DSPARK_EINVAL, "k, v, the caches and their powers must be different arrays");
   if ((int64_t)n_rows * heads * (d / 8) > INT32_MAX - kCacheThreads)
     return fail(c, DSPARK_EINVAL, "too many rows (%d)", n_rows);
   DeviceGuard dg(c->device);
@@ -2186,7 +2197,7 @@ int dspark_rope_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q
   if (rc) return rc;
   if ((rc = check_cache(c, heads, d, page_size, kcache, vcache, c_stride_page, c_stride_tok, c_stride_head, kv_dtype)))
     return rc;
-  if ((rc = check_scales(c, kv_dtype, k_scale, v_scale, k_power, v_power))) return rc;
+  if ((rc = check_scales(c, kv_dtype, kcache, vcache, k_scale, v_scale, k_power, v_power))) return rc;
   RopeWriteArgs p;
   memset(&p, 0, sizeof(p));
   RopeArgs& a = p.r;
@@ -2197,8 +2208,9 @@ int dspark_rope_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q
   if (!row_slot) return fail(c, DSPARK_EINVAL, "null pointer argument");
   if ((rc = check_rows(c, "k", k, k_stride_row, k_stride_head))) return rc;
   if ((rc = check_rows(c, "v", v, v_stride_row, v_stride_head))) return rc;
-  if (heads_q > 0 && (q_out == k || q_out == v))
-    return fail(c, DSPARK_EINVAL, "q_out must be another array than k and v");
+  if (kcache == vcache) return fail(c, DSPARK_EINVAL, "kcache and vcache must be different arrays");
+  if (heads_q > 0 && same_as(q_out, k, v, kcache, vcache, k_power, v_power))
+    return fail(c, DSPARK_EINVAL, "q_out must be another array than k, v, the caches and their powers");
   DeviceGuard dg(c->device);
   if (!dg.ok) return fail(c, DSPARK_EHIP, "hipSetDevice failed");
   const int64_t size = kv_dtype == DSPARK_BF16 ? 2 : 1;
