@@ -50,6 +50,7 @@
 // a weight two products, and in the first the 64-byte pieces of a token's heads.
 #include "common.hpp"
 #include "internal.hpp"
+#include "power_place.hpp"
 
 namespace dspark {
 namespace {
@@ -404,7 +405,7 @@ struct Groups {
       }
       at.v[j] = (int64_t)p * a.c_page + (int64_t)(first(base, j, last) & ((1 << a.page_shift) - 1)) * a.c_tok;
       if constexpr (F == kCacheMxfp4)
-        at.s[j] = (((int64_t)p * a.Hkv << a.page_shift) + (first(base, j, last) & ((1 << a.page_shift) - 1))) * (D / 32);
+        at.s[j] = power_place(p, a.Hkv, 0, a.page_shift, first(base, j, last) & ((1 << a.page_shift) - 1), D / 32);
     }
   }
 };
@@ -841,8 +842,9 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
               const int d = DT * (4 * (lane >> 4) + i) + dt;
               float y;
               if constexpr (kFp4) {
-                const int64_t page0 = ((unsigned)page < (unsigned)a.n_pages ? page : 0) * a.Hkv * power_head;
-                y = vsc[page0 + (tk & ((1 << a.page_shift) - 1)) * (D / 32) + d / 32] >= 253 ? NAN : 0.0f;
+                const int64_t at_s = power_place((unsigned)page < (unsigned)a.n_pages ? page : 0, a.Hkv, 0, a.page_shift,
+                                                 tk & ((1 << a.page_shift) - 1), D / 32);
+                y = vsc[at_s + d / 32] >= 253 ? NAN : 0.0f;
               } else {
                 const uint32_t x = E4M3 ? widen<false>(p[d]) & 0xFFFFu : reinterpret_cast<const uint16_t*>(p)[d];
                 y = (x & 0x7F80u) == 0x7F80u ? __uint_as_float(x << 16) : 0.0f;
