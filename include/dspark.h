@@ -551,8 +551,8 @@ int dspark_cache_write(dspark_ctx* ctx, hipStream_t stream, int n_rows, int head
  * contiguous, either order as above).  k_power, v_power: bytes [n_pages]
  * [heads][page_size][d / 32], contiguous whatever the order of the caches, 16-
  * byte aligned: value i of a head is its code times 2^(power[i / 32] - 127),
- * NaN where that byte is 255 (bytes of 253 and 254 are not written; what rows
- * that see such a block get is not defined).
+ * NaN where that byte is 255 (bytes of 253 and 254 are not written, but read:
+ * what passes the largest bf16 value is infinite then).
  * With A the largest magnitude of 32 values, their power is the least 2^e with
  * A <= 7 * 2^e, e kept within -120 .. 125 (0 where A is 0), and each becomes the value nearest
  * it (ties to the even code; larger ones, infinities too, become 6 * 2^e), so
@@ -574,8 +574,8 @@ int dspark_cache_write_mxfp4(dspark_ctx* ctx, hipStream_t stream, int n_rows, in
  * any number of times.  Caches, scales (E4M3) and powers (MXFP4) as the writes
  * have them, those of other types NULL.  k, v: bf16 [n_rows][heads][d] through
  * row and head strides (multiples of 8, 16-byte aligned).  bf16 and MXFP4
- * values come back exactly (MXFP4: from 2^-126 on), E4M3 ones times their scale rounded
- * to float32 and then to bf16.  k and v may not overlap each other, the
+ * values come back exactly (MXFP4: from 2^-126 on, infinite past the largest
+ * bf16 value), E4M3 ones times their scale rounded to float32 and then to bf16.  k and v may not overlap each other, the
  * caches or the powers.  One launch (timing class DSPARK_K_CACHE).  Errors:
  * DSPARK_EINVAL. */
 int dspark_cache_read(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
@@ -680,10 +680,11 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
                   void* out, int64_t o_stride_row, int64_t o_stride_head, float* lse);
 
 /* The same over a cache of 4 bits (MXFP4, placed as dspark_cache_write_mxfp4
- * has it).  Keys and values are taken exactly (below 2^-126 as bf16 has them);
- * weights are rounded as over a bf16 cache, and results are finite for values
- * up to 2^100.  A value block with byte 255 is NaN to the rows that see its
- * token, a key block makes their results NaN. */
+ * has it).  Keys and values are taken exactly (below 2^-126 and past the largest
+ * bf16 value as bf16 has them); weights are rounded as over a bf16 cache, and
+ * results are finite for values up to 2^100.  A value block with byte 255 is
+ * NaN to the rows that see its token, an infinite value (bytes 253 and 254)
+ * infinite or NaN; a key block with byte 255 makes their results NaN. */
 int dspark_attend_mxfp4(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads,
                         int d, const void* q, int64_t q_stride_row, int64_t q_stride_head,
                         const void* kcache, const void* vcache,

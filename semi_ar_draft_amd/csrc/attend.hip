@@ -130,7 +130,13 @@ __device__ __forceinline__ uint32_t odd_e4m3(uint32_t x) {
 __device__ __forceinline__ float power_at(uint32_t x, unsigned turn) {
   return __uint_as_float(__builtin_amdgcn_alignbit(x, x, turn));
 }
-__device__ __forceinline__ bool odd_power(float s) { return (__float_as_uint(s) & 0x7F800000u) >= 0x7E800000u; }
+// The bits of the codes (of a word of eight) that are infinite or NaN in bf16 times the power of a byte: all of 255's, of
+// 2^127 those from 2 on, of 2^126 those from 4 on, none of a lower one.
+__device__ __forceinline__ uint32_t odd_codes(uint32_t w, unsigned byte) {
+  if (byte == 255) return 0xFFFFFFFFu;
+  const uint32_t m = byte == 254 ? w >> 2 : byte == 253 ? w >> 2 & w >> 1 : 0u;
+  return (m & 0x11111111u) * 15u;
+}
 
 // Two e2m1 values (byte c of w) times a power of two as bf16: exact from 2^-126 on, NaN for a byte of 255.
 __device__ __forceinline__ uint32_t widen4(uint32_t w, float s, int c) {
@@ -357,24 +363,32 @@ struct Loaded {
   // Takes infinite and NaN values out; whether there were any.
   __device__ __forceinline__ uint32_t take_odd() {
     uint32_t odd = 0;
+    if constexpr (kFp4) {
+      // (vs: the powers' bytes from bit 23 on, anything around them)
+      uint32_t top = 0;
 #pragma unroll
-    for (int t = 0; t < 8; ++t) {
-      if constexpr (kFp4) {
-        // whole blocks: those whose power says so
-        if (odd_power(__uint_as_float(vs[t]))) {
-          odd = 1;
-          vs[t] = 0x3F800000u;
+      for (int t = 0; t < 8; ++t) top = max(top, vs[t] & 0x7F800000u);
+      if (__builtin_expect(!__any(top >= 253u << 23), 1)) return 0;
 #pragma unroll
-          for (int w = 0; w < VW; ++w) v[t][w] = 0;
+      for (int t = 0; t < 8; ++t) {
+        const unsigned byte = vs[t] >> 23 & 255;
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          const uint32_t x = odd_codes(v[t][w], byte);
+          odd |= x;
+          v[t][w] &= ~x;
         }
-      } else {
+        if (byte == 255) vs[t] = 0x3F800000u;
+      }
+    } else {
+#pragma unroll
+      for (int t = 0; t < 8; ++t)
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
           const uint32_t x = kBf16 ? odd_bf16(v[t][w]) : odd_e4m3(v[t][w]);
           odd |= x;
           v[t][w] &= ~x;
         }
-      }
     }
     return odd;
   }
@@ -835,24 +849,39 @@ __global__ __launch_bounds__(kAttendThreads, attend_waves(D, MT, F)) void attend
           const int page = now.table[tk >> a.page_shift];
           const unsigned char* p = vc + (int64_t)((unsigned)page < (unsigned)a.n_pages ? page : 0) * a.c_page +
                                    (int64_t)(tk & ((1 << a.page_shift) - 1)) * a.c_tok;
+          if constexpr (kFp4) {
+            // 0 times them all: NaN for those that were left out.  (The lane's D / 4 values of a token have one
+            // power, or one for each half of them.)
+            const unsigned char* ps = vsc + power_place((unsigned)page < (unsigned)a.n_pages ? page : 0, a.Hkv, 0, a.page_shift,
+                                                        tk & ((1 << a.page_shift) - 1), D / 32) + (D / 4) * (lane >> 4) / 32;
+            const uint16_t* pw = reinterpret_cast<const uint16_t*>(p) + DT * (lane >> 4);
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
+            for (int mt = 0; mt < MT; ++mt) {
+              if (tk > t.lim[mt]) continue;
 #pragma unroll
-            for (int dt = 0; dt < DT; ++dt) {
-              const int d = DT * (4 * (lane >> 4) + i) + dt;
-              float y;
-              if constexpr (kFp4) {
-                const int64_t at_s = power_place((unsigned)page < (unsigned)a.n_pages ? page : 0, a.Hkv, 0, a.page_shift,
-                                                 tk & ((1 << a.page_shift) - 1), D / 32);
-                y = vsc[at_s + d / 32] >= 253 ? NAN : 0.0f;
-              } else {
-                const uint32_t x = E4M3 ? widen<false>(p[d]) & 0xFFFFu : reinterpret_cast<const uint16_t*>(p)[d];
-                y = (x & 0x7F80u) == 0x7F80u ? __uint_as_float(x << 16) : 0.0f;
+              for (int i = 0; i < 4; ++i) {
+                const float s = __uint_as_float((uint32_t)ps[D == 256 ? i / 2 : 0] << 23);
+#pragma unroll
+                for (int dt = 0; dt < DT; dt += 2) {
+                  const uint32_t x = widen4(pw[(DT * i + dt) / 4], s, dt / 2 & 1);
+                  t.o[mt][dt][i] = __builtin_fmaf(__uint_as_float(x << 16), 0.0f, t.o[mt][dt][i]);
+                  t.o[mt][dt + 1][i] = __builtin_fmaf(__uint_as_float(x & 0xFFFF0000u), 0.0f, t.o[mt][dt + 1][i]);
+                }
               }
-#pragma unroll
-              for (int mt = 0; mt < MT; ++mt)
-                if (tk <= t.lim[mt]) t.o[mt][dt][i] += y;
             }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+              for (int dt = 0; dt < DT; ++dt) {
+                const int d = DT * (4 * (lane >> 4) + i) + dt;
+                const uint32_t x = E4M3 ? widen<false>(p[d]) & 0xFFFFu : reinterpret_cast<const uint16_t*>(p)[d];
+                const float y = (x & 0x7F80u) == 0x7F80u ? __uint_as_float(x << 16) : 0.0f;
+#pragma unroll
+                for (int mt = 0; mt < MT; ++mt)
+                  if (tk <= t.lim[mt]) t.o[mt][dt][i] += y;
+              }
+          }
         }
       }
       if (have) begin(next);                             // under way while this piece is finished
