@@ -692,7 +692,7 @@ class Context:
         """What the caches (bf16, float8_e4m3fn or mxfp4, with their scales as
         cache_write has them) hold in the slots row_slot (int32 [n_rows], -1: none), as bf16
         [n_rows][heads][d].  Returns (k, v), or ``out``; rows of slot -1 are
-        left as they are (new ones hold zeros there)."""
+        left as they are (new ones hold zeros there, all of them written first)."""
         dev = self.device
         if out is None:
             d = kcache.shape[-1] * (2 if kcache.dtype in _FOUR_BITS else 1)
@@ -713,7 +713,7 @@ class Context:
         (2 j, 2 j + 1), by row_pos * freq[j] radians (freq float64, see
         rope_frequencies), times factor.  q_out and k_out may be q and k
         themselves.  Returns (q_out, k_out); rows of position -1 are left as
-        they are (new ones hold zeros there)."""
+        they are (new ones hold zeros there, all of them written first)."""
         dev = self.device
         if (q is not None and q_out is None) or (k is not None and k_out is None):
             with _on(stream):

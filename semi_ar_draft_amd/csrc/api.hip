@@ -2241,8 +2241,13 @@ int dspark_rope_write(dspark_ctx* c, hipStream_t stream, int n_rows, int heads_q
   p.s_head = (int64_t)page_size * (d / 32);
   p.s_page = heads * p.s_head;
   // Rows of a workgroup: one, or where there are many and their keys are turned in float64 two, which
-  // keep its waves busier (8190 rows of 32 and 8 heads of 128 into e4m3 46.6 us with one, 45.2 with two, 48.4 with four;
-  // into bf16 40.3, 42.0, 46.1)
+  // keep its waves busier.  Us with one / two / four, replays of a graph, into e4m3 (MXFP4 lies 10% lower, the
+  // same way): 32 and 8 heads of 128, 1024 rows 8.5 / 9.4 / 12.9, 2048 15.1 / 13.7 / 15.8, 8190 49.0 / 47.1 / 49.8,
+  // 16381 86.4 / 80.5 / 84.7; 16 and 16 heads of 64, 1024 rows 6.8 / 6.8 / 8.7, 2048 12.2 / 9.2 / 10.5, 16381 68.7 /
+  // 53.1 / 52.5; 16 and 4 heads of 256, 1024 rows 9.5 / 10.6 / 15.7, 2048 15.6 / 14.8 / 18.7, 16381 112.5 / 97.6 / 101.9;
+  // 64 and 8 heads of 128, 1024 rows 11.3 / 12.6 / 17.2, 2048 18.5 / 17.9 / 20.5, 3000 24.5 / 25.8 / 25.0, 16381 128 /
+  // 125 / 137; 8 and 1 heads of 128 6.2 / 6.2 / 5.8, 8.8 / 6.6 / 6.5, 42.3 / 27.2 / 20.7.  Into bf16, 32 and 8
+  // heads, 8190 rows 40.3 / 42.0 / 46.1.
   if (kv_dtype != DSPARK_BF16 && n_rows >= 8 * c->cu_count) a.rows = std::max(a.rows, 2);
   const int grid = (n_rows + a.rows - 1) / a.rows;
   return klaunch(c, DSPARK_K_ROPE, rope_write_kernel(interleaved != 0, cache_type(kv_dtype)), dim3(grid),

@@ -46,8 +46,13 @@
 // of 7 positions, heads of 64, 19.5 and 4 us, bound by the latency of finding a
 // stretch and its first keys.  Over MXFP4 (a quarter of bf16's bytes), both
 // launches, the first 62 us (pages that keep a head's tokens together 55), the
-// long ones 118, the blocks 16.6: vector issue, a value being 4 bits to widen and
-// a weight two products, and in the first the 64-byte pieces of a token's heads.
+// long ones 116, the blocks 16.5.  The long ones: a wave's vector instructions
+// (48% of a SIMD's time) and its products (30%), a value being 4 bits to widen
+// and a weight two products, run one after the other with one wave a SIMD.  The
+// first: neither (37 and 18%), nor memory (56 us all in the caches); of the two waves of
+// a SIMD the older ends after 35 us, the younger after 42, the last one after 50, and
+// 9 us are the join.  The blocks: the latencies of the books (2 us), the first loads (2),
+// of two or three steps (5) and of the launches.
 #include "common.hpp"
 #include "internal.hpp"
 #include "power_place.hpp"
@@ -62,8 +67,11 @@ constexpr int kWaves = kAttendThreads / 64;
 // 1, 119 with 2, 123 with 4; one row of one request of up to 1200 tokens: 14.2 us
 // with at least 1 step, 16.1 with 2 (a wave's first step waits for its loads,
 // the second is nearly free, but so is the wave that would take it).
-// Over MXFP4, whose steps are shorter beside it, with the heads' tokens together 58.5 us with a cost of 1, 55.7 with 2,
-// 56.8 with 3.
+// Over MXFP4, whose steps are shorter beside it, costs of 1 / 2 / 3 / 4 on those requests, tokens before heads and heads
+// before tokens: 62.7 / 63.6 / 61.2 / 60.9 and 57.4 / 54.5 / 55.2 / 54.9 us; one row each 53.3 / 53.8 / 54.7 / 53.2 and
+// 40.2 / 39.2 / 40.3 / 40.2; of up to 600 tokens 25.5 / 23.9 / 24.7 / 26.1 and 25.0 / 23.8 / 24.9 / 25.8; one row of one
+// request 13.4 / 12.5 / 13.4 / 13.6; 256 of 2 rows, heads of 64, 33.6 / 32.9 / 30.9 / 32.5 and 31.0 / 27.0 / 26.9 / 27.6; 64
+// with heads of 256 32.8 / 34.3 / 34.4 / 34.0.
 template <int F>
 constexpr int kCost = F == kCacheMxfp4 ? 2 : 1;
 constexpr int kMinSteps = 1;

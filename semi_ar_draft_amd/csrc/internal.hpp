@@ -389,11 +389,11 @@ struct AttendArgs {
 };
 constexpr int kAttendThreads = 256;
 constexpr float kRestFactor = 1.0f + 0x1p-16f;   // of a weight's rest beside its leading bits
-constexpr int kAttendMaxGrid = 512;    // workgroups: one per CU
+constexpr int kAttendMaxGrid = 512;    // workgroups: one or two per CU (attend_waves)
 constexpr size_t kAttendJoinBytes = kAttendMaxGrid * sizeof(AttendJoin);
 constexpr size_t kAttendPartBytes = kAttendMaxGrid * 2 * 8320 * sizeof(float);   // 16 mt (d + 2) <= 64 * 130
-// Waves of a SIMD, which is workgroups of a CU.  Over MXFP4 a step is bound by the issue of
-// vector instructions, of which one wave reaches two thirds (16 rows a tile, all in the caches: 115 us with
+// Waves of a SIMD, which is workgroups of a CU.  Over MXFP4 one wave's vector and matrix instructions follow each
+// other, two waves' pass side by side where the registers hold them (16 rows a tile, all in the caches: 115 us with
 // one wave, 95 with two, 97 with three; heads of 256 77 with one, 78 with two).
 constexpr int attend_waves(int d, int mt, int type) { return type == kCacheMxfp4 && d <= 128 && mt <= 2 ? 2 : 1; }
 // mt: 16-row blocks of a tile (1, 2; 4 where d < 256)
