@@ -575,9 +575,9 @@ int dspark_cache_write_mxfp4(dspark_ctx* ctx, hipStream_t stream, int n_rows, in
  * have them, those of other types NULL.  k, v: bf16 [n_rows][heads][d] through
  * row and head strides (multiples of 8, 16-byte aligned).  bf16 and MXFP4
  * values come back exactly (MXFP4: from 2^-126 on, infinite past the largest
- * bf16 value), E4M3 ones times their scale rounded to float32 and then to bf16.  k and v may not overlap each other, the
- * caches or the powers.  One launch (timing class DSPARK_K_CACHE).  Errors:
- * DSPARK_EINVAL. */
+ * bf16 value), E4M3 ones times their scale rounded to float32 and then to bf16.
+ * k and v may not overlap each other, the caches or the powers.  One launch
+ * (timing class DSPARK_K_CACHE).  Errors: DSPARK_EINVAL. */
 int dspark_cache_read(dspark_ctx* ctx, hipStream_t stream, int n_rows, int heads, int d, int page_size, int n_pages,
                       const int32_t* row_slot, const void* kcache, const void* vcache,
                       int64_t c_stride_page, int64_t c_stride_tok, int64_t c_stride_head,
@@ -684,7 +684,8 @@ int dspark_attend(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int ga
  * bf16 value as bf16 has them); weights are rounded as over a bf16 cache, and
  * results are finite for values up to 2^100.  A value block with byte 255 is
  * NaN to the rows that see its token, an infinite value (bytes 253 and 254)
- * infinite or NaN; a key block with byte 255 makes their results NaN. */
+ * infinite or NaN; a key block with byte 255 makes their results NaN.  Results
+ * of equal inputs are bitwise equal, as dspark_attend's. */
 int dspark_attend_mxfp4(dspark_ctx* ctx, hipStream_t stream, int B, int n_rows, int gamma, int heads_q, int heads,
                         int d, const void* q, int64_t q_stride_row, int64_t q_stride_head,
                         const void* kcache, const void* vcache,
